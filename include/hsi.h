@@ -516,6 +516,174 @@ hsi_status hsi_reindex_layer(const uint8_t* q_rec, const float* g_q, const float
                              int32_t k, int32_t* top_idx, float* top_val, hsi_format format, void* ws,
                              size_t ws_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------- */
+
+/*
+ * Rotary positions and a paged K/V cache with a budget: what stands on both
+ * sides of the indexer in a served model. The pages have no counterpart: they
+ * leave positions and core attention to the model.
+ */
+typedef enum {
+    HSI_BF16 = 0,
+    HSI_FP16 = 1,
+    HSI_FP32 = 2 /* hsi_rope only */
+} hsi_dtype;
+
+typedef enum {
+    HSI_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot) radians per position */
+    HSI_ROPE_LINEAR = 1, /* f_i / factor */
+    HSI_ROPE_NTK = 2,    /* base * factor^(rot/(rot-2)) in place of base */
+    HSI_ROPE_YARN = 3    /* f_i where a pair turns more than beta_fast times over original_len, f_i / factor
+                            where it turns less than beta_slow times, a linear ramp over the pairs between
+                            (their indices rounded outwards); gain 0.1 ln(factor) + 1 */
+} hsi_rope_scaling;
+
+/*
+ * The rotation of rot / 2 pairs, on the host: steps[i] (host, out) is pair i's
+ * turns per position in units of 2^-64, *gain (host, out) the factor on the
+ * rotated values. The caller copies steps to the device. factor >= 1 for every
+ * scaling but PLAIN; original_len, beta_fast >= beta_slow > 0 for YARN.
+ * rot even, 2 .. 4096; base > 1.
+ */
+hsi_status hsi_rope_steps(int32_t rot, double base, hsi_rope_scaling scaling, double factor, double original_len,
+                          double beta_fast, double beta_slow, uint64_t* steps, float* gain);
+
+/*
+ * Rotary positions of T tokens of H heads of D values. With the angle
+ *   a_i = 2 pi frac(positions[t] * steps[i] / 2^64)
+ * (the product wraps in 64-bit integers, so far positions lose nothing) the
+ * pair (u, v) becomes gain * (u cos a - v sin a, u sin a + v cos a); inverse
+ * turns by -a (the transpose: the gradient of the rotation). Pair i is
+ * dims (2i, 2i+1) (interleaved) or (i, i + rot/2) of [rot_offset, rot_offset +
+ * rot); the other dims are copied. Arithmetic in fp32, rounded once.
+ *  x, y    (dev) dtype; value d of head h of token t at t * token_stride + h *
+ *          head_stride + d (elements). y may be x (same strides); otherwise
+ *          they must not overlap. 16-byte aligned addresses, strides, D,
+ *          rot_offset and rot (halves: rot / 2) take the vector kernel.
+ *  positions (dev) int32 [T] (negative ones turn backwards); steps (dev) [rot / 2].
+ * Errors: INVALID_ARG for null pointers, non-positive sizes, odd rot, rotated
+ * dims outside the head, strides that lay two results over each other.
+ */
+hsi_status hsi_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, hsi_dtype dtype, int64_t T, int32_t H,
+                    int32_t D, const int32_t* positions, const uint64_t* steps, int32_t rot, int32_t rot_offset,
+                    int32_t interleaved, float gain, int32_t inverse, void* y, int64_t y_token_stride,
+                    int64_t y_head_stride, cudaStream_t stream);
+
+/*
+ * A paged K/V cache of B sequences. Entry e of sequence b lies in page
+ * table[b][e / page_size], at its place e mod page_size; value d of KV head h
+ * there at page * page_stride + place * token_stride + h * head_stride + d
+ * (elements; the same for K and V, so that both layouts [page][place][head]
+ * and [page][head][place] are strides). K and V may lie in one allocation.
+ *  k, v    (dev) 16-byte aligned; strides multiples of 8 elements, at least dim.
+ *  table   (dev) int32 [B][ld_table]; only the pages of entries below kv_len are read.
+ *  kv_len  (dev) int32 [B]: entries, the call's new tokens among them (a
+ *          sequence's new tokens are its last entries).
+ *  dim     64 or 128; page_size a power of two, 8 .. 4096; dtype BF16 or FP16
+ *          (UNSUPPORTED otherwise).
+ * A length outside [0, the call's bound], a page id outside [0, n_pages) or a
+ * q_start that descends is clamped or skipped and reported as
+ * HSI_ERR_DEVICE_ARG by hsi_device_error. What the pages hold past a
+ * sequence's length never reaches a result, NaN included.
+ *
+ * New tokens of all sequences lie side by side: sequence b's are tokens
+ * q_start[b] .. q_start[b+1] - 1 (dev, int32 [B + 1]) of the calls' T tokens.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t n_pages;
+    const int32_t* table;
+    int64_t ld_table;
+    const int32_t* kv_len;
+    int32_t B, heads, dim, page_size;
+    hsi_dtype dtype;
+} hsi_paged_kv;
+
+/*
+ * The new tokens' keys and values into the cache, in one launch with their
+ * rotation: token i of sequence b's n becomes entry kv_len[b] - n + i. steps
+ * NULL: k is copied; otherwise rotated as by hsi_rope (rot a multiple of 16,
+ * rot_offset of 8: UNSUPPORTED otherwise). q (may be NULL; needs steps): the
+ * tokens' query heads, rotated into q_out (may be q).
+ *  k_new, v_new (dev) [T][heads][dim], q, q_out [T][q_heads][dim] with strides
+ *          in elements, 16-byte aligned, multiples of 8.
+ * Tokens outside every sequence are left alone.
+ */
+hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* v_new, int64_t v_token_stride, int64_t v_head_stride, const int32_t* q_start,
+                            int64_t T, const int32_t* positions, const uint64_t* steps, int32_t rot, int32_t rot_offset,
+                            int32_t interleaved, float gain, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, int32_t q_heads, void* q_out, int64_t o_token_stride,
+                            int64_t o_head_stride, cudaStream_t stream);
+
+/*
+ * Attention of the new tokens over the cache. Query head h reads KV head
+ * h / (q_heads / heads). Row (token i of sequence b's n, head h) sees entries
+ * e < kv_len[b] - n + i + 1 (causal) or e < kv_len[b]:
+ *   out = sum_e p_e v_e / sum_e p_e,  p_e = exp(scale q.k_e),
+ *   lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0).
+ * The products run on the tensor cores with fp32 sums; p is rounded to the
+ * cache's type for the second one.
+ *  q, out  (dev) [T][q_heads][dim] of the cache's type, strides in elements
+ *          (multiples of 8, 16-byte aligned); distinct. Entries that a row sees
+ *          must be finite for the row to be.
+ *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
+ *  lse     (dev) fp32 [T][q_heads], may be NULL.
+ *  ws      (dev) hsi_paged_attention_ws(...) bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED (the cache's dims), WORKSPACE.
+ */
+size_t hsi_paged_attention_ws(int32_t B, int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t max_q, int64_t max_kv);
+hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               int32_t q_heads, const int32_t* q_start, int64_t T, int32_t max_q, int64_t max_kv,
+                               float scale, int32_t causal, void* out, int64_t o_token_stride, int64_t o_head_stride,
+                               float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The attention weight each entry has gathered, per KV head g:
+ *   acc_out[b][g][e] = decay * acc_in[b][g][e] + sum over rows (token, head of g) that see e
+ *                      of exp(scale q.k_e - lse[row])        (e < kv_len[b])
+ * with the lse that hsi_paged_attention wrote for the same arguments. Entries
+ * at or past kv_len[b] are left untouched. fp32 sums in a fixed order.
+ *  acc_in  (dev) fp32 [B][heads][ld_acc_in], may be NULL (zeros) or acc_out;
+ *  acc_out (dev) fp32 [B][heads][ld_acc_out]; both ld at least the entries' bound.
+ */
+hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 int32_t q_heads, const float* lse, const int32_t* q_start, int64_t T, int32_t max_q,
+                                 int64_t max_kv, float scale, int32_t causal, float decay, const float* acc_in,
+                                 int64_t ld_acc_in, float* acc_out, int64_t ld_acc_out, cudaStream_t stream);
+
+/*
+ * Which entries a budget keeps, per (sequence, KV head): all of them when
+ * kv_len[b] <= budget; otherwise the first `sink`, the last `recent` and the
+ * largest acc among the rest, ties to the lowest index, `budget` in all.
+ *  acc     (dev) fp32 [B][heads][ld_acc], not NaN; max_len (host) bounds kv_len.
+ *  keep    (dev) out int32 [B][heads][ld_keep]: the kept entries ascending, -1
+ *          up to `budget`.
+ *  new_len (dev) out int32 [B]: min(kv_len[b], budget). Distinct from kv_len.
+ *  acc_out (dev, may be NULL) fp32 [B][heads][ld_out]: the kept entries' acc in
+ *          the order of keep, zeros up to `budget`. It may be acc (up to 393000
+ *          entries, UNSUPPORTED beyond): then zeros up to max_len.
+ * Errors: INVALID_ARG (sink + recent > budget among them).
+ */
+hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_len, int32_t B, int32_t heads,
+                            int64_t max_len, int32_t budget, int32_t sink, int32_t recent, int32_t* keep,
+                            int64_t ld_keep, int32_t* new_len, float* acc_out, int64_t ld_out, cudaStream_t stream);
+
+/*
+ * Moves the kept entries to the front: entry keep[b][g][i] of KV head g becomes
+ * entry i < new_len[b] of the table dst_table (dev, int32 [B][ld_dst]).
+ * dst_table is cache->table itself (in place) or lists pages that no table row
+ * of the cache lists. The cache's kv_len still holds the old lengths; the
+ * caller sets it to new_len (and table to dst_table) afterwards.
+ * keep must ascend, as hsi_evict_select writes it.
+ */
+hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int64_t ld_keep, const int32_t* new_len,
+                             int32_t budget, const int32_t* dst_table, int64_t ld_dst, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+
 typedef enum {
     HSI_WS_QUANTIZE = 0,
     HSI_WS_SCORE = 1,

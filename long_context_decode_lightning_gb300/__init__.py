@@ -33,7 +33,22 @@ EXPORTS = ["hsi_quantize_nvfp4", "hsi_score_full", "hsi_topk", "hsi_candidate_po
            "hsi_kernel_launches", "hsi_calib_read", "hsi_calib_mma", "hsi_full_layer", "hsi_reindex_layer",
            "hsi_topk_noalloc", "hsi_debug_set", "hsi_pool_gather", "hsi_quantize_mxfp4", "hsi_quantize_mainkv",
            "hsi_gather_mainkv", "hsi_append_token", "hsi_mask_scores", "hsi_prefill_layer",
-           "hsi_gather_mainkv_layers"]
+           "hsi_gather_mainkv_layers", "hsi_rope_steps", "hsi_rope", "hsi_paged_append", "hsi_paged_attention_ws",
+           "hsi_paged_attention", "hsi_attention_weights", "hsi_evict_select", "hsi_paged_compact"]
+
+
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class _PagedKV(ctypes.Structure):
+    """hsi_paged_kv of include/hsi.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int)]
 
 
 class HsiError(RuntimeError):
@@ -98,6 +113,23 @@ def lib() -> ctypes.CDLL:
         L.hsi_calib_mma.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp]
         L.hsi_kernel_launches.argtypes = []
         L.hsi_kernel_launches.restype = ctypes.c_uint64
+        f32, f64, kvp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_PagedKV)
+        L.hsi_rope_steps.argtypes = [i32, f64, ctypes.c_int, f64, f64, f64, f64, vp, vp]
+        L.hsi_rope.argtypes = [vp, i64, i64, ctypes.c_int, i64, i32, i32, vp, vp, i32, i32, i32, f32, i32, vp, i64, i64,
+                               vp]
+        L.hsi_paged_append.argtypes = [kvp, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, i32, i32, i32, f32, vp, i64,
+                                       i64, i32, vp, i64, i64, vp]
+        L.hsi_paged_attention_ws.argtypes = [i32, i32, i32, i32, i32, i64]
+        L.hsi_paged_attention_ws.restype = sz
+        L.hsi_paged_attention.argtypes = [kvp, vp, i64, i64, i32, vp, i64, i32, i64, f32, i32, vp, i64, i64, vp, vp, sz,
+                                          vp]
+        L.hsi_attention_weights.argtypes = [kvp, vp, i64, i64, i32, vp, vp, i64, i32, i64, f32, i32, f32, vp, i64, vp,
+                                            i64, vp]
+        L.hsi_evict_select.argtypes = [vp, i64, vp, i32, i32, i64, i32, i32, i32, vp, i64, vp, vp, i64, vp]
+        L.hsi_paged_compact.argtypes = [kvp, vp, i64, vp, i32, vp, i64, vp]
+        for name in ("hsi_rope_steps", "hsi_rope", "hsi_paged_append", "hsi_paged_attention", "hsi_attention_weights",
+                     "hsi_evict_select", "hsi_paged_compact"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("hsi_quantize_nvfp4", "hsi_score_full", "hsi_topk", "hsi_candidate_pool", "hsi_score_pool",
                      "hsi_device_error", "hsi_device_check", "hsi_calib_read", "hsi_calib_mma", "hsi_full_layer",
                      "hsi_reindex_layer", "hsi_topk_noalloc", "hsi_debug_set", "hsi_pool_gather",
@@ -356,3 +388,158 @@ def reindex_layer(q_rec, g_q, w, k_rec, g_k, k_rec_off, n_visible, block_ids, n_
         _ptr(block_ids),
         _ptr(n_kept), _ptr(n_pool), n_keep, B, _ptr(pool_scores), ld, k, _ptr(top_idx), _ptr(top_val), fmt,
         _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype(t: torch.Tensor) -> int:
+    _need(t.dtype in _DTYPES, f"unsupported dtype {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _i32(t: torch.Tensor, name: str, dim: int) -> torch.Tensor:
+    _need(t.dtype == torch.int32 and t.dim() == dim and t.stride(-1) == 1, f"{name}: int32, {dim}-d, contiguous rows")
+    return t
+
+
+def _heads(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    """A [tokens, heads, dims] tensor with contiguous dims."""
+    _need(t.dim() == 3 and t.dtype == dtype and t.stride(2) == 1, f"{name}: [tokens, heads, dims] of {dtype}, dims contiguous")
+    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def rope_steps(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda") -> tuple[torch.Tensor, float]:
+    """The rotation of rot / 2 pairs: (steps int64 [rot / 2] on the device, in 2^-64 turns a position, gain)."""
+    steps, gain = torch.empty(max(rot, 2) // 2, dtype=torch.int64), ctypes.c_float()
+    _need(scaling in ROPE_SCALING, f"unknown scaling {scaling!r}")
+    _check("hsi_rope_steps", lib().hsi_rope_steps(rot, base, ROPE_SCALING[scaling], factor, original_len, beta_fast,
+                                                  beta_slow, _ptr(steps), ctypes.byref(gain)))
+    return steps.to(device), gain.value
+
+
+def rope(x, positions, steps, out, rot_offset: int = 0, interleaved: bool = False, gain: float = 1.0,
+         inverse: bool = False, stream=None):
+    """x [T, H, D] (bf16, fp16 or fp32) rotated into out (may be x) at positions int32 [T]; inverse: the gradient."""
+    _heads(x, "x", x.shape, x.dtype)
+    _heads(out, "out", x.shape, x.dtype)
+    _need(_i32(positions, "positions", 1).numel() == x.shape[0], "positions: one a token")
+    _need(steps.dtype == torch.int64 and steps.is_contiguous(), "steps: int64, contiguous")
+    T, H, D = x.shape
+    _check("hsi_rope", lib().hsi_rope(
+        _ptr(x), x.stride(0), x.stride(1), _dtype(x), T, H, D, _ptr(positions), _ptr(steps), 2 * steps.numel(),
+        rot_offset, int(interleaved), gain, int(inverse), _ptr(out), out.stride(0), out.stride(1), _stream(stream)))
+
+
+class PagedKV:
+    """A paged cache for the calls below: k, v [pages, page size, heads, dim] (any strides with contiguous
+    dims, the same for both; a [pages, heads, page size, dim] cache is passed transposed), table int32
+    [B, pages a sequence], kv_len int32 [B] on the device. Keeps the tensors; their contents may change."""
+
+    def __init__(self, k, v, table, kv_len):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride(3) == 1 and v.stride() == k.stride(),
+              "k, v: [pages, page size, heads, dim], the same strides, dims contiguous")
+        _i32(table, "table", 2)
+        _need(_i32(kv_len, "kv_len", 1).numel() == table.shape[0], "kv_len: one a sequence")
+        self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
+        self.B, self.heads, self.dim, self.page_size = table.shape[0], k.shape[2], k.shape[3], k.shape[1]
+        self.c = _PagedKV(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[0], _ptr(table),
+                          table.stride(0) if table.shape[0] > 1 else table.shape[1], _ptr(kv_len), self.B, self.heads,
+                          self.dim, self.page_size, _dtype(k))
+        self.ref = ctypes.byref(self.c)
+
+
+def _q_start(q_start, kv):
+    _need(_i32(q_start, "q_start", 1).numel() == kv.B + 1, "q_start: one a sequence and the end")
+    return _ptr(q_start)
+
+
+def paged_append(kv: PagedKV, k_new, v_new, q_start, max_q=None, positions=None, steps=None, rot_offset: int = 0,
+                 interleaved: bool = False, gain: float = 1.0, q=None, q_out=None, stream=None):
+    """k_new, v_new [T, heads, dim] into the cache's last entries of each sequence; with steps, k (and q [T,
+    q heads, dim] into q_out) rotated at positions int32 [T] in the same launch. max_q is not needed here."""
+    T = k_new.shape[0]
+    _heads(k_new, "k_new", (T, kv.heads, kv.dim), kv.k.dtype)
+    _heads(v_new, "v_new", (T, kv.heads, kv.dim), kv.k.dtype)
+    _need(positions is None or _i32(positions, "positions", 1).numel() == T, "positions: one a token")
+    _need(steps is None or (steps.dtype == torch.int64 and steps.is_contiguous()), "steps: int64, contiguous")
+    if q is not None:
+        _heads(q, "q", (T, q.shape[1], kv.dim), kv.k.dtype)
+        _heads(q_out, "q_out", q.shape, kv.k.dtype)
+    _check("hsi_paged_append", lib().hsi_paged_append(
+        kv.ref, _ptr(k_new), k_new.stride(0), k_new.stride(1), _ptr(v_new), v_new.stride(0), v_new.stride(1),
+        _q_start(q_start, kv), T, _ptr(positions), _ptr(steps), 0 if steps is None else 2 * steps.numel(), rot_offset,
+        int(interleaved), gain, _ptr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
+        0 if q is None else q.shape[1], _ptr(q_out), 0 if q is None else q_out.stride(0),
+        0 if q is None else q_out.stride(1), _stream(stream)))
+
+
+def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int) -> torch.Tensor:
+    """A caller-owned scratch buffer for paged_attention."""
+    n = int(lib().hsi_paged_attention_ws(kv.B, kv.heads, q.shape[1], kv.dim, max_q, max_kv))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(kv: PagedKV, q, q_start, max_q: int, max_kv: int, scale: float, out, lse=None, causal: bool = True,
+                    ws=None, stream=None):
+    """q [T, q heads, dim] over the cache into out (and lse fp32 [T, q heads])."""
+    _heads(q, "q", (q.shape[0], q.shape[1], kv.dim), kv.k.dtype)
+    _heads(out, "out", q.shape, kv.k.dtype)
+    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == tuple(q.shape[:2])),
+          "lse: fp32 [tokens, q heads], contiguous")
+    if ws is None:
+        ws = paged_attention_workspace(kv, q, max_q, max_kv)
+    _check("hsi_paged_attention", lib().hsi_paged_attention(
+        kv.ref, _ptr(q), q.stride(0), q.stride(1), q.shape[1], _q_start(q_start, kv), q.shape[0], max_q, max_kv, scale,
+        int(causal), _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _acc(t, name, kv_shape):
+    _need(t.dtype == torch.float32 and t.dim() == 3 and t.stride(2) == 1 and tuple(t.shape[:2]) == tuple(kv_shape),
+          f"{name}: fp32 [sequences, KV heads, entries]")
+    ld = t.stride(1) if t.shape[1] > 1 else (t.stride(0) if t.shape[0] > 1 else t.shape[2])
+    _need(t.shape[0] == 1 or t.stride(0) == t.shape[1] * ld, f"{name}: rows evenly spaced")
+    return ld
+
+
+def attention_weights(kv: PagedKV, q, lse, q_start, max_q: int, max_kv: int, scale: float, acc_in, acc_out,
+                      decay: float = 1.0, causal: bool = True, stream=None):
+    """acc_out [B, heads, entries] = decay * acc_in + the attention weight of every entry, summed over the rows of
+    its KV head. acc_in None: zeros; it may be acc_out."""
+    _heads(q, "q", (q.shape[0], q.shape[1], kv.dim), kv.k.dtype)
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == tuple(q.shape[:2]),
+          "lse: fp32 [tokens, q heads], contiguous")
+    shape = (kv.B, kv.heads)
+    _check("hsi_attention_weights", lib().hsi_attention_weights(
+        kv.ref, _ptr(q), q.stride(0), q.stride(1), q.shape[1], _ptr(lse), _q_start(q_start, kv), q.shape[0], max_q,
+        max_kv, scale, int(causal), decay, _ptr(acc_in), 0 if acc_in is None else _acc(acc_in, "acc_in", shape),
+        _ptr(acc_out), _acc(acc_out, "acc_out", shape), _stream(stream)))
+
+
+def evict_select(acc, kv_len, max_len: int, budget: int, keep, new_len, sink: int = 0, recent: int = 0, acc_out=None,
+                 stream=None):
+    """The entries a budget keeps, per sequence and KV head: keep int32 [B, heads, >= budget], new_len int32 [B]."""
+    B, H = acc.shape[0], acc.shape[1]
+    ld = _acc(acc, "acc", (B, H))
+    _need(keep.dtype == torch.int32 and keep.is_contiguous() and keep.shape[:2] == acc.shape[:2],
+          "keep: int32 [sequences, KV heads, places], contiguous")
+    _need(_i32(kv_len, "kv_len", 1).numel() == B and _i32(new_len, "new_len", 1).numel() == B, "lengths: one a sequence")
+    _check("hsi_evict_select", lib().hsi_evict_select(
+        _ptr(acc), ld, _ptr(kv_len), B, H, max_len, budget, sink, recent, _ptr(keep), keep.shape[2], _ptr(new_len),
+        _ptr(acc_out), 0 if acc_out is None else _acc(acc_out, "acc_out", (B, H)), _stream(stream)))
+
+
+def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, stream=None):
+    """Entry keep[b, g, i] of KV head g becomes entry i of dst_table int32 [B, pages] (None: in place).
+    budget: bound of new_len (keep's width by default)."""
+    dst = kv.table if dst_table is None else _i32(dst_table, "dst_table", 2)
+    _need(keep.dtype == torch.int32 and keep.is_contiguous() and tuple(keep.shape[:2]) == (kv.B, kv.heads),
+          "keep: int32 [sequences, KV heads, places], contiguous")
+    _need(dst.shape[0] == kv.B and _i32(new_len, "new_len", 1).numel() == kv.B, "a row of dst_table and a length a sequence")
+    _check("hsi_paged_compact", lib().hsi_paged_compact(
+        kv.ref, _ptr(keep), keep.shape[2], _ptr(new_len), keep.shape[2] if budget is None else budget, _ptr(dst),
+        dst.stride(0) if kv.B > 1 else dst.shape[1], _stream(stream)))

@@ -1,0 +1,579 @@
+// Attention of a few new tokens over a paged cache, and the attention weights
+// of its entries, for up to a few rows per KV head (a row: one new token and
+// one query head). Rows of one KV head share its K and V tiles: with r rows an
+// entry costs 4 D bytes and 4 D r flops, far below the tensor rate for r <= 16,
+// so the bound is HBM and the work is to keep it busy:
+//
+//  - The (sequence, row tile, KV head) units, each ceil(length / 64) tiles of 64
+//    entries, form one line of tiles that is cut into equal runs, one per CTA, two CTAs
+//    an SM. Long and short sequences mix freely and no SM waits for another; a
+//    unit that spans CTAs is joined from their partial sums by a second kernel.
+//  - A producer warp fetches tiles with one TMA box per page (or 64 entries of
+//    it) into a ring of shared-memory stages, a lane per box.
+//  - Each of four warps owns 16 entries of a tile: S = Q K^T by mma.sync
+//    (16 rows x 16 entries), its own running maximum and sum, P V into its own
+//    16 x D accumulator. Nothing is exchanged between warps before the unit's end.
+//
+// mma.sync suffices here: a 64-entry tile needs 128 of them in the ~1400
+// cycles its 32 KB take at the SM's share of HBM. P is rounded to the cache's
+// type for the second product (weights in [0, 1], error 2^-9 relative per term
+// in bf16, averaged by the sum); maxima, sums and the output stay in fp32.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace hsi {
+
+constexpr int AT_ROWS = 16;      // rows of a unit
+constexpr int AT_KT = 64;        // entries of a tile
+constexpr int AT_WARPS = 4;      // consumer warps, 16 entries of a tile each
+constexpr int AT_THREADS = 32 * (AT_WARPS + 1);
+
+struct AttendParams {
+    PagedView kv;
+    const void* q;
+    int64_t qt, qh;  // token and head strides (elements)
+    const int32_t* q_start;
+    int64_t T;       // tokens of q
+    int max_q, max_kv, Hq, group;  // host bounds of new tokens and entries; query heads, per KV head
+    float sl2;       // scale * log2(e)
+    int causal;
+    void* out;
+    int64_t ot, oh;
+    float* lse;      // [T][Hq] or null
+    // partial sums: slot s holds AT_ROWS x D accumulators, AT_ROWS maxima (base 2), AT_ROWS sums
+    float* part;
+    int64_t* base;   // [B + 1] first tile of each sequence on the line
+    // weights only
+    const float* lse_in;
+    const float* acc_in;
+    float* acc_out;
+    int64_t ld_acc_in, ld_acc_out;
+    float decay;
+};
+
+template <int D>
+__host__ __device__ constexpr int attend_slot_floats(int rows) { return rows * (D + 2); }
+
+// A line of `total` tiles is cut into G <= total runs, so that none is empty.
+// First tile of run `c`:
+__device__ __forceinline__ int64_t line_cut(int64_t total, int64_t c, int64_t G) { return G ? c * total / G : 0; }
+// The run that holds tile x.
+__device__ __forceinline__ int64_t line_run(int64_t total, int64_t x, int64_t G) {
+    return ((x + 1) * G + total - 1) / total - 1;
+}
+
+// ---------------------------------------------------------------- mma.sync --
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_16816<__half>(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// --------------------------------------------------------------- the kernel --
+
+template <int D, bool WEIGHTS>
+struct AttendCfg {
+    static constexpr int HALF_BYTES = AT_KT * 128;                 // 64 values of every entry of a tile
+    static constexpr int K_BYTES = HALF_BYTES * (D / 64);
+    static constexpr int STAGE_BYTES = WEIGHTS ? K_BYTES : 2 * K_BYTES;
+    static constexpr int STAGES = 98304 / STAGE_BYTES;             // 96 KB a CTA, two CTAs an SM
+    static constexpr int RED_BYTES = WEIGHTS ? 0 : AT_WARPS * AT_ROWS * 32 * 4;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + RED_BYTES;
+};
+
+// Where a walk along the line stands: the sequence, its tiles and what is left.
+struct LineWalk {
+    int b;
+    int64_t first;    // first tile of sequence b
+    int32_t len, m, at;  // entries, new tokens, first new token
+    int nt, units;    // tiles of a unit, units of the sequence (row tiles x KV heads)
+};
+
+template <bool WEIGHTS>
+__device__ __forceinline__ void walk_load(const AttendParams& p, LineWalk& w) {
+    w.len = paged_len(p.kv, w.b, p.max_kv);
+    w.m = paged_new(p.q_start, w.b, p.max_q, p.T, &w.at);
+    w.nt = (w.len + AT_KT - 1) / AT_KT;
+    const int rt = (w.m * p.group + AT_ROWS - 1) / AT_ROWS;
+    w.units = (WEIGHTS ? 1 : rt) * p.kv.H;  // the weights' units take every row of a KV head
+}
+__device__ __forceinline__ int64_t walk_tiles(const LineWalk& w) { return (int64_t)w.nt * w.units; }
+
+template <typename T, int D, bool WEIGHTS>
+__global__ void __launch_bounds__(AT_THREADS, 2)
+    attend_token_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+    using C = AttendCfg<D, WEIGHTS>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+    __shared__ int64_t s_total, s_first;
+    __shared__ int s_b, s_abort;
+    __shared__ float s_m[AT_WARPS][AT_ROWS], s_l[AT_WARPS][AT_ROWS];
+    uint8_t* const stage0 = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* const red = reinterpret_cast<float*>(stage0 + C::STAGES * C::STAGE_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], AT_WARPS);
+        }
+        fence_mbar_init();
+        s_abort = 0;
+        tma_prefetch_map(&kmap);
+        if (!WEIGHTS) tma_prefetch_map(&vmap);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // the line: total tiles, then the sequence that holds this run's first tile
+    if (warp == 0) {
+        int64_t total = 0;
+        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+            LineWalk w;
+            w.b = b0 + lane;
+            int64_t n = 0;
+            if (w.b < p.kv.B) {
+                walk_load<WEIGHTS>(p, w);
+                n = walk_tiles(w);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(~0u, n, o);
+                if (lane >= o) n += up;
+            }
+            if (!WEIGHTS && blockIdx.x == 0 && w.b < p.kv.B) p.base[w.b + 1] = total + n;
+            total += __shfl_sync(~0u, n, 31);
+        }
+        if (!WEIGHTS && blockIdx.x == 0 && lane == 0) p.base[0] = 0;
+        const int64_t lo = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
+        int64_t before = 0;
+        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+            LineWalk w;
+            w.b = b0 + lane;
+            int64_t n = 0;
+            if (w.b < p.kv.B) {
+                walk_load<WEIGHTS>(p, w);
+                n = walk_tiles(w);
+            }
+            int64_t upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(~0u, upto, o);
+                if (lane >= o) upto += up;
+            }
+            const int64_t f = before + upto - n;
+            if (n && lo >= f && lo < f + n) {
+                s_b = w.b;
+                s_first = f;
+            }
+            before += __shfl_sync(~0u, upto, 31);
+            if (before > lo) break;
+        }
+        if (lane == 0) s_total = total;
+    }
+    __syncthreads();
+    const int64_t total = s_total;
+    const int64_t G = min((int64_t)gridDim.x, total);
+    if (blockIdx.x >= G) return;
+    int64_t x = line_cut(total, blockIdx.x, G);
+    const int64_t hi = line_cut(total, blockIdx.x + 1, G);
+    LineWalk w;
+    w.b = s_b;
+    w.first = s_first;
+    walk_load<WEIGHTS>(p, w);
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    bool ok = true;  // false once a wait has run out: no more copies or results, but every barrier is kept
+
+    while (x < hi) {
+        while (x >= w.first + walk_tiles(w)) {
+            w.first += walk_tiles(w);
+            ++w.b;
+            walk_load<WEIGHTS>(p, w);
+        }
+        const int64_t local = x - w.first;
+        const int unit = (int)(local / w.nt), tile0 = (int)(local % w.nt);
+        const int n_tiles = (int)(hi - x < w.nt - tile0 ? hi - x : w.nt - tile0);
+        const int head = unit % p.kv.H, rt = unit / p.kv.H;
+        x += n_tiles;
+
+        if (warp == AT_WARPS) {  // producer: a lane per box
+            const int box = p.kv.page_shift < 6 ? 1 << p.kv.page_shift : AT_KT;  // entries of a box
+            const int nbox = AT_KT / box, halves = D / 64;
+            const int per = nbox * halves;
+            const int bi = lane % per, kind = lane / per;  // box; 0: K, 1: V
+            const int e = (bi / halves) * box, dim = (bi % halves) * 64;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int e0 = (tile0 + i) * AT_KT;
+                const int live = (min(w.len - e0, AT_KT) + box - 1) / box * halves;  // boxes with entries
+                const bool mine = kind < (WEIGHTS ? 1 : 2) && e0 + e < w.len;
+                int page = 0;
+                if (mine) page = paged_page(p.kv, w.b, (e0 + e) >> p.kv.page_shift);
+                ok = wait_bounded(&empty[stage], phase ^ 1, &s_abort);
+                if (!__all_sync(~0u, ok)) {  // let the copies in flight land before the block goes
+                    for (int k = fills > C::STAGES ? fills - C::STAGES : 0; k < fills; ++k)
+                        wait_drain(&full[k % C::STAGES], (k / C::STAGES) & 1);
+                    return;
+                }
+                ++fills;
+                if (fills == 1 && *(volatile int*)&g_hsi_skip_first_copy) goto next;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], live * box * 128 * (WEIGHTS ? 1 : 2));
+                __syncwarp();
+                if (mine) {
+                    uint8_t* dst = stage0 + stage * C::STAGE_BYTES + kind * C::K_BYTES + (dim / 64) * C::HALF_BYTES +
+                                   e * 128;
+                    tma_page_box(dst, kind ? &vmap : &kmap, dim, (e0 + e) & ((1 << p.kv.page_shift) - 1), head, page,
+                                 &full[stage]);
+                }
+            next:
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            continue;
+        }
+
+        // ---- consumers ----
+        const int rows = w.m * p.group;
+        const int r_lo = lane >> 2, kq = (lane & 3) * 2;
+        const int rt_end = WEIGHTS ? (rows + AT_ROWS - 1) / AT_ROWS : rt + 1;
+        uint32_t qf[D / 16][4];
+        int lim[2];         // entries that rows r_lo, r_lo + 8 see
+        float lse2[2] = {}; // weights: log-sum-exp (base 2)
+        auto load_rows = [&](int rtile) {
+            const uint32_t* src[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = rtile * AT_ROWS + r_lo + 8 * j;
+                src[j] = nullptr;
+                lim[j] = 0;
+                if (r >= rows) continue;
+                const int t = r / p.group, h = head * p.group + r % p.group;
+                src[j] = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + (w.at + t) * p.qt + h * p.qh);
+                lim[j] = p.causal ? min(w.len, w.len - w.m + t + 1) : w.len;
+                if (WEIGHTS) {
+                    const float v = __ldg(p.lse_in + (int64_t)(w.at + t) * p.Hq + h);
+                    if (v == -INFINITY) lim[j] = 0;
+                    lse2[j] = v * LOG2E;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    qf[k][j] = src[j & 1] ? __ldg(src[j & 1] + k * 8 + (j >> 1) * 4 + (lane & 3)) : 0u;
+            }
+        };
+        load_rows(WEIGHTS ? 0 : rt);
+
+        float o[WEIGHTS ? 1 : D / 8][4] = {};
+        float m2[2] = {-INFINITY, -INFINITY}, l[2] = {};
+        // shared-memory addresses of this lane's ldmatrix rows, within a tile
+        const int mat = lane >> 3, mrow = lane & 7;
+        const int krow = warp * 16 + (mat >> 1) * 8 + mrow;  // K: matrices (entries 0-7, 0-7, 8-15, 8-15) x (chunk, +1)
+        const int vrow = warp * 16 + (mat & 1) * 8 + mrow;   // V: matrices (0-7, 8-15) x (chunk, chunk, +1, +1)
+
+        for (int i = 0; i < n_tiles; ++i) {
+            ok = ok && __all_sync(~0u, wait_bounded(&full[stage], phase, &s_abort));
+            const uint32_t kbase = smem_u32(stage0 + stage * C::STAGE_BYTES);
+            const int e0 = (tile0 + i) * AT_KT + warp * 16;
+            float add[4] = {};  // weights of entries kq, kq + 1, 8 + kq, 9 + kq
+            for (int rr = WEIGHTS ? 0 : rt; ok && rr < rt_end; ++rr) {
+                if (WEIGHTS && rt_end > 1) load_rows(rr);
+                float s[2][4] = {};
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t kf[4];
+                    const int chunk = 2 * k + (mat & 1);
+                    ldmatrix_x4(kbase + (chunk >> 3) * C::HALF_BYTES + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), kf);
+                    mma_16816<T>(s[0], qf[k], kf[0], kf[1]);
+                    mma_16816<T>(s[1], qf[k], kf[2], kf[3]);
+                }
+                if (WEIGHTS) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int j = c >> 1, key = e0 + n * 8 + kq + (c & 1);
+                            const float pr = key < lim[j] ? ex2(fmaf(s[n][c], p.sl2, -lse2[j])) : 0.f;
+                            add[n * 2 + (c & 1)] += pr;
+                        }
+                    }
+                    continue;
+                }
+                float mx[2] = {m2[0], m2[1]};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = c >> 1, key = e0 + n * 8 + kq + (c & 1);
+                        s[n][c] = key < lim[j] ? s[n][c] * p.sl2 : -INFINITY;
+                        mx[j] = fmaxf(mx[j], s[n][c]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mx[j] = fmaxf(mx[j], __shfl_xor_sync(~0u, mx[j], 1));
+                    mx[j] = fmaxf(mx[j], __shfl_xor_sync(~0u, mx[j], 2));
+                }
+                if (__any_sync(~0u, mx[0] > m2[0] || mx[1] > m2[1])) {
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f[j] = mx[j] == -INFINITY ? 1.f : ex2(m2[j] - mx[j]);
+                        m2[j] = mx[j];
+                        l[j] *= f[j];
+                    }
+#pragma unroll
+                    for (int d = 0; d < (WEIGHTS ? 1 : D / 8); ++d) {
+                        o[d][0] *= f[0];
+                        o[d][1] *= f[0];
+                        o[d][2] *= f[1];
+                        o[d][3] *= f[1];
+                    }
+                }
+                float base[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) base[j] = m2[j] == -INFINITY ? 0.f : m2[j];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[n][c] = ex2(s[n][c] - base[c >> 1]);
+                        l[c >> 1] += s[n][c];
+                    }
+                }
+                const uint32_t pf[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
+                                        pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
+                const uint32_t vbase = kbase + C::K_BYTES;
+                if (e0 + 16 > w.len) {
+                    // entries past the length hold whatever the page holds (or nothing was
+                    // loaded): 0 * NaN would reach every row, so they become zeros
+                    for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
+                        const int r = warp * 16 + idx / (D / 8), ch = idx % (D / 8);
+                        if ((tile0 + i) * AT_KT + r >= w.len)
+                            *reinterpret_cast<uint4*>(stage0 + stage * C::STAGE_BYTES + C::K_BYTES +
+                                                      (ch >> 3) * C::HALF_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int d = 0; d < (WEIGHTS ? 0 : D / 16); ++d) {
+                    uint32_t vf[4];
+                    const int chunk = 2 * d + (mat >> 1);
+                    ldmatrix_x4_trans(
+                        vbase + (chunk >> 3) * C::HALF_BYTES + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), vf);
+                    mma_16816<T>(o[2 * d], pf, vf[0], vf[1]);
+                    mma_16816<T>(o[2 * d + 1], pf, vf[2], vf[3]);
+                }
+            }
+            fence_proxy_async_smem();  // what this warp wrote or read precedes the next TMA into the stage
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (WEIGHTS && ok) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    add[c] += __shfl_xor_sync(~0u, add[c], 4);
+                    add[c] += __shfl_xor_sync(~0u, add[c], 8);
+                    add[c] += __shfl_xor_sync(~0u, add[c], 16);
+                }
+                if (lane < 4) {
+                    const int64_t row = (int64_t)w.b * p.kv.H + head;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int key = e0 + (c >> 1) * 8 + kq + (c & 1);
+                        if (key >= w.len) continue;
+                        const float old = p.acc_in ? p.decay * p.acc_in[row * p.ld_acc_in + key] : 0.f;
+                        p.acc_out[row * p.ld_acc_out + key] = old + add[c];
+                    }
+                }
+            }
+        }
+        if constexpr (!WEIGHTS) {  // join the four warps
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[j] += __shfl_xor_sync(~0u, l[j], 1);
+                l[j] += __shfl_xor_sync(~0u, l[j], 2);
+            }
+            if ((lane & 3) == 0) {
+                s_m[warp][r_lo] = m2[0];
+                s_m[warp][r_lo + 8] = m2[1];
+                s_l[warp][r_lo] = l[0];
+                s_l[warp][r_lo + 8] = l[1];
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = r_lo + 8 * j;
+                float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                f[j] = m2[j] == -INFINITY ? 0.f : ex2(m2[j] - m);
+            }
+            const bool whole = tile0 == 0 && n_tiles == w.nt;
+            float* slot = p.part + (int64_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * attend_slot_floats<D>(AT_ROWS);
+            // 32 dims at a time: thread -> row tid / 8, dims (tid % 8) * 4 .. + 3
+            const int orow = threadIdx.x >> 3, od = (threadIdx.x & 7) * 4;
+            const float rm = fmaxf(fmaxf(s_m[0][orow], s_m[1][orow]), fmaxf(s_m[2][orow], s_m[3][orow]));
+            float rl = 0.f;
+#pragma unroll
+            for (int i = 0; i < AT_WARPS; ++i)
+                rl += s_m[i][orow] == -INFINITY ? 0.f : s_l[i][orow] * ex2(s_m[i][orow] - rm);
+            const int r = rt * AT_ROWS + orow;
+            const int64_t tok = w.at + (r < rows ? r / p.group : 0);
+            const int h = head * p.group + (r < rows ? r % p.group : 0);
+            const float inv = rl > 0.f || rl != rl ? 1.f / rl : 0.f;
+#pragma unroll
+            for (int c = 0; c < (WEIGHTS ? 0 : D / 32); ++c) {
+                float* mine = red + warp * AT_ROWS * 32;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const float(&v)[4] = o[4 * c + d];
+                    *reinterpret_cast<float2*>(mine + r_lo * 32 + d * 8 + kq) = make_float2(v[0] * f[0], v[1] * f[0]);
+                    *reinterpret_cast<float2*>(mine + (r_lo + 8) * 32 + d * 8 + kq) = make_float2(v[2] * f[1], v[3] * f[1]);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < AT_WARPS; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(red + i * AT_ROWS * 32 + orow * 32 + od);
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                if (!whole) {
+                    *reinterpret_cast<float4*>(slot + orow * D + c * 32 + od) = sum;
+                } else if (r < rows) {
+                    uint2 v = make_uint2(pack2<T>(sum.x * inv, sum.y * inv), pack2<T>(sum.z * inv, sum.w * inv));
+                    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + c * 32 + od) = v;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+            if ((threadIdx.x & 7) == 0) {
+                if (!whole) {
+                    slot[AT_ROWS * D + orow] = rm;
+                    slot[AT_ROWS * D + AT_ROWS + orow] = rl;
+                } else if (r < rows && p.lse) {
+                    p.lse[tok * p.Hq + h] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * LN2;
+                }
+            }
+        }
+    }
+}
+
+// Joins the units that several runs hold: a block per (sequence, row tile, KV
+// head), a thread per output value. Runs of a unit lie side by side: the first
+// wrote its CTA's slot 1, the others their slots 0. Sequences without entries
+// get zeros and lse -inf here.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int grid) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int b = blockIdx.z, head = blockIdx.y, rt = blockIdx.x;
+    LineWalk w;
+    w.b = b;
+    walk_load<false>(p, w);
+    const int rows = w.m * p.group;
+    if (rt * AT_ROWS >= rows) return;
+    const int64_t total = p.base[p.kv.B];
+    const int64_t G = min((int64_t)grid, total);
+    const int64_t s0 = p.base[b] + ((int64_t)rt * p.kv.H + head) * w.nt;
+    int64_t c0 = 0, c1 = -1;
+    if (w.nt) {
+        c0 = line_run(total, s0, G);
+        c1 = line_run(total, s0 + w.nt - 1, G);
+        if (c0 == c1) return;  // written whole
+    }
+    constexpr int SLOT = attend_slot_floats<D>(AT_ROWS);
+    for (int i = threadIdx.x; i < AT_ROWS * (D / 4); i += 128) {
+        const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = rt * AT_ROWS + row;
+        if (r >= rows) break;
+        float m = -INFINITY;
+        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part[(2 * c + (c == c0)) * SLOT + AT_ROWS * D + row]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        for (int64_t c = c0; c <= c1; ++c) {
+            const float* slot = p.part + (2 * c + (c == c0)) * SLOT;
+            const float mc = slot[AT_ROWS * D + row];
+            const float f = mc == -INFINITY ? 0.f : ex2(mc - m);
+            const float4 v = *reinterpret_cast<const float4*>(slot + row * D + d);
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+            l += f * slot[AT_ROWS * D + AT_ROWS + row];
+        }
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const int64_t tok = w.at + r / p.group;
+        const int h = head * p.group + r % p.group;
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + d) =
+            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        if (d == 0 && p.lse) p.lse[tok * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+    }
+}
+
+}  // namespace hsi

@@ -1077,3 +1077,5 @@ hsi_status hsi_reindex_layer(const uint8_t* q_rec, const float* g_q, const float
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

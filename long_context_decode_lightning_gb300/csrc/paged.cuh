@@ -1,0 +1,107 @@
+// The paged K/V cache as the kernels see it, and its TMA loads.
+//
+// Pages of 2^page_shift entries; entry e of sequence b is entry e mod page of
+// page table[b][e / page]. A page id outside [0, n_pages) is reported through
+// the sticky error word: a load then reads zeros (the TMA's fill for a
+// coordinate past the tensor), a store is skipped.
+#pragma once
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace hsi {
+
+struct PagedView {
+    void *k, *v;
+    int64_t page_stride, token_stride, head_stride;  // elements
+    int64_t n_pages;
+    const int32_t* table;
+    int64_t ld_table;
+    const int32_t* kv_len;
+    int B, H, D, page_shift;
+};
+
+constexpr int64_t PAGED_NO_ENTRY = -1, PAGED_NO_TOKEN = -2;
+
+// Entries of sequence b, clamped to what its table row can hold and to the host's bound.
+__device__ __forceinline__ int32_t paged_len(const PagedView& kv, int b, int64_t bound = INT32_MAX) {
+    const int32_t n = __ldg(kv.kv_len + b);
+    const int64_t most = min(kv.ld_table << kv.page_shift, bound);
+    if (n < 0 || n > most) {
+        raise_error(DEVERR_ARG);
+        return n < 0 ? 0 : (int32_t)most;
+    }
+    return n;
+}
+
+// New tokens of sequence b: [*first, *first + returned); a descending q_start counts as none.
+__device__ __forceinline__ int32_t paged_new(const int32_t* q_start, int b, int32_t most, int64_t total, int32_t* first) {
+    const int32_t a = __ldg(q_start + b), e = __ldg(q_start + b + 1);
+    *first = a;
+    if (a < 0 || e < a || e > total || e - a > most) {
+        raise_error(DEVERR_ARG);
+        return 0;
+    }
+    return e - a;
+}
+
+// The sequence of new token t: the last b with q_start[b] <= t.
+__device__ __forceinline__ int paged_seq_of(const int32_t* q_start, int B, int64_t t) {
+    int lo = 0, hi = B;  // q_start[lo] <= t < q_start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(q_start + mid) <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Element offset (head 0) of the place of new token t: entry kv_len - (new
+// tokens of its sequence) + its index among them. PAGED_NO_TOKEN where t lies
+// outside every sequence, PAGED_NO_ENTRY (reported) where it has no valid place.
+__device__ __forceinline__ int64_t paged_new_row(const PagedView& kv, const int32_t* q_start, int64_t t) {
+    if (t < __ldg(q_start) || t >= __ldg(q_start + kv.B)) return PAGED_NO_TOKEN;
+    const int b = paged_seq_of(q_start, kv.B, t);
+    const int32_t a = __ldg(q_start + b), e1 = __ldg(q_start + b + 1);
+    const int32_t n = paged_len(kv, b);
+    const int64_t e = (int64_t)n - (e1 - a) + (t - a);
+    if (e < 0 || e >= n) {
+        raise_error(DEVERR_ARG);
+        return PAGED_NO_ENTRY;
+    }
+    const int32_t page = __ldg(kv.table + b * kv.ld_table + (e >> kv.page_shift));
+    if (page < 0 || page >= kv.n_pages) {
+        raise_error(DEVERR_ARG);
+        return PAGED_NO_ENTRY;
+    }
+    return page * kv.page_stride + (e & ((1 << kv.page_shift) - 1)) * kv.token_stride;
+}
+
+// Page id of page `i` of sequence b; n_pages (past the tensor: zeros) where the table is wrong.
+__device__ __forceinline__ int32_t paged_page(const PagedView& kv, int b, int64_t i) {
+    const int32_t page = __ldg(kv.table + b * kv.ld_table + i);
+    if (page < 0 || page >= kv.n_pages) {
+        raise_error(DEVERR_ARG);
+        return (int32_t)kv.n_pages;
+    }
+    return page;
+}
+
+// One box of a {dim, entry, head, page} tensor map into 128-byte-swizzled rows
+// of 64 values. The dim coordinate is a multiple of 64: 16-byte aligned.
+__device__ __forceinline__ void tma_page_box(void* dst, const CUtensorMap* map, int dim, int entry, int head, int page,
+                                             uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(dim), "r"(entry), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+}  // namespace hsi
