@@ -101,6 +101,11 @@ __device__ __forceinline__ void mma_16816<__half>(float (&d)[4], const uint32_t*
 }
 
 template <typename T>
+constexpr bool is_bf16 = false;
+template <>
+constexpr bool is_bf16<__nv_bfloat16> = true;
+
+template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {

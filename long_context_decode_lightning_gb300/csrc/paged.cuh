@@ -100,6 +100,16 @@ __device__ __forceinline__ void tma_page_box(void* dst, const CUtensorMap* map, 
         : "memory");
 }
 
+// One box of a {dim, head, token} tensor map of the query rows.
+__device__ __forceinline__ void tma_rows_box(void* dst, const CUtensorMap* map, int dim, int head, int token,
+                                             uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(dim), "r"(head), "r"(token), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

@@ -9,6 +9,7 @@
 #include "evict.cuh"
 #include "paged.cuh"
 #include "rope.cuh"
+#include "weights.cuh"
 
 namespace {
 
@@ -42,6 +43,52 @@ hsi_status paged_map(const hsi_paged_kv& c, const PagedView& v, void* base, int 
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? HSI_OK : HSI_ERR_INVALID_ARG;
+}
+
+// {dim, head, token} map of the query rows; a box is 64 dims of `tpt` tokens'
+// heads of one group. INVALID_ARG where a stride has no map (a broadcast axis).
+hsi_status rows_map(hsi_dtype dt, const void* q, int64_t qt, int64_t qh, int64_t T, int Hq, int D, int group, int tpt,
+                    CUtensorMap* map) {
+    const auto encode = tensor_map_encode();
+    if (!encode) return HSI_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)(Hq > 1 ? qh : D) * 2, (cuuint64_t)(T > 1 ? qt : D) * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)group, (cuuint32_t)tpt};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = encode(map, dt == HSI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                              const_cast<void*>(q), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? HSI_OK : HSI_ERR_INVALID_ARG;
+}
+
+// Many rows per KV head go to the tensor-memory kernels, whose tiles hold
+// whole tokens of 128 rows (groups of at most 128 heads, no broadcast axis of q).
+bool chunk_rows(const AttendParams& p) {
+    return (int64_t)p.max_q * p.group > AT_ROWS && p.group <= 128 && (p.qt > 0 || p.T == 1) && (p.qh > 0 || p.Hq == 1);
+}
+
+// A launch in clusters of `csize` blocks, in the programmatic chain.
+template <typename... KArgs, typename... Args>
+hsi_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int csize, cudaStream_t s,
+                          Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_ok(e);
 }
 
 hsi_status paged_view(const hsi_paged_kv* c, PagedView* v) {
@@ -140,6 +187,24 @@ hsi_status run_attend_token(const AttendParams& p, hsi_dtype dt, const CUtensorM
                              : launch_attend_token<__nv_bfloat16, 64, WEIGHTS>(p, km, vm, grid, s);
     return p.kv.D == 128 ? launch_attend_token<__half, 128, WEIGHTS>(p, km, vm, grid, s)
                          : launch_attend_token<__half, 64, WEIGHTS>(p, km, vm, grid, s);
+}
+
+template <typename T, int D>
+hsi_status launch_weights_chunk(const AttendParams& p, const CUtensorMap& km, const CUtensorMap& qm, int tpt,
+                                cudaStream_t s) {
+    using C = WeightsCfg<D>;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (smem_attr_once(weights_chunk_kernel<T, D>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
+    const int sms = sm_count();
+    if (sms <= 0) return HSI_ERR_CUDA;
+    const int64_t units = (int64_t)p.kv.B * p.kv.H * (((int64_t)p.max_kv + WC_KEYS - 1) / WC_KEYS);
+    const int64_t tiles = (p.max_q + tpt - 1) / tpt;
+    // units that leave SMs idle are shared by clusters, no CTA without a query tile
+    int csize = 1;
+    while (csize < EV_MAX_CLUSTER && 2 * csize * units <= sms && 2 * csize <= tiles) csize *= 2;
+    const int64_t grid = csize > 1 || units < sms ? units * csize : sms;
+    return launch_cluster(weights_chunk_kernel<T, D>, dim3((unsigned)grid), dim3(WC_THREADS), C::SMEM_BYTES, csize, s, p,
+                          km, qm, csize, tpt);
 }
 
 // The checks that attention and weights share.
@@ -331,6 +396,19 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
     p.ld_acc_out = ld_acc_out;
     p.decay = decay;
     CUtensorMap km;
+    if (chunk_rows(p)) {
+        const int tpt = WC_ROWS / p.group;
+        CUtensorMap qm;
+        if ((st = paged_map(*cache, p.kv, cache->k, 128, &km)) != HSI_OK) return st;
+        if ((st = rows_map(cache->dtype, q, q_token_stride, q_head_stride, T, q_heads, cache->dim, p.group, tpt, &qm)) !=
+            HSI_OK)
+            return st;
+        if (cache->dtype == HSI_BF16)
+            return cache->dim == 128 ? launch_weights_chunk<__nv_bfloat16, 128>(p, km, qm, tpt, stream)
+                                     : launch_weights_chunk<__nv_bfloat16, 64>(p, km, qm, tpt, stream);
+        return cache->dim == 128 ? launch_weights_chunk<__half, 128>(p, km, qm, tpt, stream)
+                                 : launch_weights_chunk<__half, 64>(p, km, qm, tpt, stream);
+    }
     if ((st = paged_map(*cache, p.kv, cache->k, AT_KT, &km)) != HSI_OK) return st;
     const int64_t grid = attend_grid(cache->B, cache->heads, p.group, p.max_q, p.max_kv, true);
     if (grid <= 0) return HSI_ERR_CUDA;
@@ -367,23 +445,8 @@ hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_
     p.new_len = new_len;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(evict_select_kernel, (int)sizeof(EvictSmem), attr_set) != HSI_OK) return HSI_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(B * heads * csize));
-    cfg.blockDim = dim3(EV_THREADS);
-    cfg.dynamicSmemBytes = sizeof(EvictSmem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = csize;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = csize > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, csize);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return cuda_ok(e);
+    return launch_cluster(evict_select_kernel, dim3((unsigned)(B * heads * csize)), dim3(EV_THREADS), sizeof(EvictSmem),
+                          csize, stream, p, csize);
 }
 
 hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int64_t ld_keep, const int32_t* new_len,

@@ -1,0 +1,291 @@
+// The attention weights of a chunk of many rows: exp(scale q.k - lse) summed
+// over the rows, per entry, on the tensor cores.
+//
+// S^T = K Q^T with the entries as the rows of the accumulator: a thread of the
+// epilogue owns one entry (one lane of tensor memory), walks the columns (the
+// query rows) and adds up in its own registers; nothing is exchanged, and the
+// order of the sum is fixed. Rows of a tile: whole tokens with their group of
+// query heads (row = token * group + head), one TMA box each 64 dims, so that
+// every group size fills a tile of 128 up to its last whole token.
+//
+// Per 128 x 128 tile of S: 128 x 128 x D multiply-adds (512 cycles at D = 128)
+// and 16384 exponentials (512 cycles of the SM's special-function units): both
+// bound it together. A CTA keeps 256 entries of K in shared memory and streams
+// the query tiles past them (one 32 KB tile per 1024 tensor cycles; 128 entries
+// would ask twice the L2 rate), two warpgroups with two accumulators each.
+// Few entries: a cluster shares a unit's query tiles and adds up the partial
+// sums through distributed shared memory, in rank order.
+#pragma once
+#include <cstdint>
+
+#include "attend.cuh"
+#include "common.cuh"
+#include "evict.cuh"
+#include "paged.cuh"
+
+namespace hsi {
+
+constexpr int WC_KEYS = 256;                 // entries of a unit: two accumulator tiles of 128
+constexpr int WC_ROWS = 128;                 // query rows of a tile
+constexpr int WC_THREADS = 32 * 11;          // 8 epilogue warps, MMA, query producer, key producer
+
+template <int D>
+struct WeightsCfg {
+    static constexpr int HALF_BYTES = 128 * 128;            // 64 dims of 128 rows
+    static constexpr int Q_BYTES = HALF_BYTES * (D / 64);
+    static constexpr int K_BYTES = 2 * Q_BYTES;             // of a unit
+    static constexpr int K_STAGES = 2;
+    static constexpr int Q_STAGES = D == 128 ? 3 : 6;
+    static constexpr int RING_BYTES = K_STAGES * K_BYTES + Q_STAGES * Q_BYTES;
+    struct Tail {
+        float nl[2][2][WC_ROWS];  // -lse (base 2) of a tile's rows, per warpgroup, double-buffered
+        uint64_t k_full[K_STAGES], k_empty[K_STAGES], q_full[Q_STAGES], q_empty[Q_STAGES];
+        uint64_t s_full[2][2], s_empty[2][2], done;
+        uint32_t tmem;
+        int abort;
+    };
+    static constexpr int SMEM_BYTES = RING_BYTES + (int)sizeof(Tail);
+    static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
+};
+
+// A walk over the units (sequence, KV head, 256 entries), u ascending.
+struct WeightsWalk {
+    int b, len, m, at, nt;
+    int64_t first;
+    __device__ __forceinline__ void load(const AttendParams& p) {
+        len = paged_len(p.kv, b, p.max_kv);
+        m = paged_new(p.q_start, b, p.max_q, p.T, &at);
+        nt = (len + WC_KEYS - 1) / WC_KEYS;
+    }
+    // false when u lies past the last unit
+    __device__ __forceinline__ bool seek(const AttendParams& p, int64_t u) {
+        while (b < p.kv.B && u >= first + (int64_t)nt * p.kv.H) {
+            first += (int64_t)nt * p.kv.H;
+            if (++b < p.kv.B) load(p);
+        }
+        return b < p.kv.B;
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(WC_THREADS, 1)
+    weights_chunk_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap qmap, int csize, int tpt) {
+    using C = WeightsCfg<D>;
+    extern __shared__ __align__(1024) uint8_t ring[];
+    uint8_t* const k_ring = ring;
+    uint8_t* const q_ring = ring + C::K_STAGES * C::K_BYTES;
+    typename C::Tail& s = *reinterpret_cast<typename C::Tail*>(ring + C::RING_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rpt = tpt * p.group;  // rows of a tile
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::K_STAGES; ++i) mbar_init(&s.k_full[i], 1), mbar_init(&s.k_empty[i], 1);
+        for (int i = 0; i < C::Q_STAGES; ++i) mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&s.s_full[i >> 1][i & 1], 1), mbar_init(&s.s_empty[i >> 1][i & 1], 4);
+        mbar_init(&s.done, 1);
+        fence_mbar_init();
+        s.abort = 0;
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&qmap);
+    }
+    if (warp == 8) tmem_alloc(&s.tmem, 512);
+    // the rows past a tile's last whole token are never loaded: zeros, so that their products are
+    for (int i = threadIdx.x; i < C::Q_STAGES * (D / 64) * (WC_ROWS - rpt) * 8; i += WC_THREADS) {
+        const int ch = i & 7, r = (i >> 3) % (WC_ROWS - rpt), half = (i >> 3) / (WC_ROWS - rpt);
+        *reinterpret_cast<uint4*>(q_ring + half * C::HALF_BYTES + (rpt + r) * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = s.tmem;
+
+    const int rank = csize > 1 ? (int)cluster_ctarank() : 0;
+    const int64_t step = gridDim.x / csize;
+    WeightsWalk w;
+    w.b = 0;
+    w.first = 0;
+    w.load(p);
+    bool ok = true;
+    int kf = 0, qf = 0;  // fills (or uses) of the key and query rings so far
+    for (int64_t u = blockIdx.x / csize; w.seek(p, u); u += step) {
+        const int local = (int)(u - w.first), head = local / w.nt, k0 = (local % w.nt) * WC_KEYS;
+        // query tiles that see any of the unit's entries
+        const int past = w.len - w.m, t_first = p.causal && k0 > past ? k0 - past : 0;
+        const int j0 = t_first / tpt + rank, j1 = (w.m + tpt - 1) / tpt;
+
+        if (warp == 10) {  // keys: a lane per box
+            const int box = p.kv.page_shift < 7 ? 1 << p.kv.page_shift : 128;
+            const int halves = D / 64, nbox = WC_KEYS / box * halves;
+            const int n = min(w.len - k0, WC_KEYS), live = (n + box - 1) / box * halves;
+            if (j0 < j1) {
+                const int st = kf % C::K_STAGES;
+                ok = ok && __all_sync(~0u, wait_bounded(&s.k_empty[st], (kf / C::K_STAGES & 1) ^ 1, &s.abort));
+                if (ok) {
+                    if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], live * box * 128);
+                    __syncwarp();
+                    for (int i = lane; i < nbox; i += 32) {
+                        const int e = (i / halves) * box, half = i % halves;
+                        if (e >= n) continue;
+                        const int page = paged_page(p.kv, w.b, (k0 + e) >> p.kv.page_shift);
+                        tma_page_box(k_ring + st * C::K_BYTES + (e >> 7) * C::Q_BYTES + half * C::HALF_BYTES +
+                                         (e & 127) * 128,
+                                     &kmap, half * 64, (k0 + e) & ((1 << p.kv.page_shift) - 1), head, page,
+                                     &s.k_full[st]);
+                    }
+                    ++kf;
+                }
+            }
+        } else if (warp == 9) {  // query tiles
+            if (lane == 0) {
+                for (int j = j0; j < j1 && ok; j += csize) {
+                    const int st = qf % C::Q_STAGES;
+                    ok = wait_bounded(&s.q_empty[st], (qf / C::Q_STAGES & 1) ^ 1, &s.abort);
+                    if (!ok) break;
+                    ++qf;
+                    if (qf == 1 && *(volatile int*)&g_hsi_skip_first_copy) continue;
+                    mbar_arrive_expect_tx(&s.q_full[st], rpt * 128 * (D / 64));
+                    for (int half = 0; half < D / 64; ++half)
+                        tma_rows_box(q_ring + st * C::Q_BYTES + half * C::HALF_BYTES, &qmap, half * 64, head * p.group,
+                                     w.at + j * tpt, &s.q_full[st]);
+                }
+            }
+        } else if (warp == 8) {  // products
+            if (lane == 0 && j0 < j1) {
+                constexpr uint32_t idesc = idesc_f16(is_bf16<T>, 128, WC_ROWS, false);
+                const int kst = kf % C::K_STAGES;
+                ok = ok && wait_bounded(&s.k_full[kst], kf / C::K_STAGES & 1, &s.abort);
+                for (int j = j0; j < j1 && ok; j += csize) {
+                    const int qst = qf % C::Q_STAGES;
+                    ok = wait_bounded(&s.q_full[qst], qf / C::Q_STAGES & 1, &s.abort);
+                    if (!ok) break;
+                    const uint32_t qa = smem_u32(q_ring + qst * C::Q_BYTES);
+                    const int buf = qf & 1;
+                    for (int kt = 0; kt < 2 && ok; ++kt) {
+                        ok = wait_bounded(&s.s_empty[kt][buf], (qf >> 1 & 1) ^ 1, &s.abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t ka = smem_u32(k_ring + kst * C::K_BYTES + kt * C::Q_BYTES);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k >> 2) * C::HALF_BYTES + (k & 3) * 32;
+                            mma_f16_ss(tmem + (kt * 2 + buf) * 128, smem_desc_sw128(ka + off), smem_desc_sw128(qa + off),
+                                       idesc, k > 0);
+                        }
+                        tc_commit(&s.s_full[kt][buf]);
+                    }
+                    tc_commit(&s.q_empty[qst]);
+                    ++qf;
+                }
+                tc_commit(&s.k_empty[kst]);
+                ++kf;
+            }
+        } else {  // weights: a thread per entry
+            const int wg = warp >> 2, key = k0 + wg * 128 + (threadIdx.x & 127), row = threadIdx.x & 127;
+            const int rtok = row / p.group, rhead = head * p.group + row % p.group;
+            // first token that sees this entry
+            const int t_min = p.causal ? key - past : 0;
+            const uint64_t sl2 = f2_pack(p.sl2, p.sl2);
+            float total = 0.f;
+            auto load_nl = [&](int j) {  // of this thread's row in tile j
+                const int t = j * tpt + rtok;
+                if (j >= j1 || row >= rpt || t >= w.m) return -INFINITY;
+                const float v = __ldg(p.lse_in + (int64_t)(w.at + t) * p.Hq + rhead);
+                return v == -INFINITY ? -INFINITY : -v * LOG2E;
+            };
+            float nl = load_nl(j0);
+            for (int j = j0; j < j1; j += csize, ++qf) {
+                const int buf = qf & 1;
+                s.nl[wg][buf][row] = nl;
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+                nl = load_nl(j + csize);
+                ok = ok && __all_sync(~0u, wait_bounded(&s.s_full[wg][buf], qf >> 1 & 1, &s.abort));
+                if (!ok) continue;
+                tc_fence_after();
+                const uint32_t ta = tmem + (uint32_t)((warp & 3) * 32 << 16) + (wg * 2 + buf) * 128;
+                // columns [c_lo, c_hi) count; tiles where all do need no comparison
+                const int rows = min(rpt, (w.m - j * tpt) * p.group);
+                const int c_lo = (t_min - j * tpt) * p.group;
+                const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + wg * 128 + 127 - past);
+                uint64_t add[2] = {0, 0};
+                uint32_t r[2][32];
+                tmem_ld32_issue(ta, r[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait(r[c & 1]);
+                    if (c < 3) tmem_ld32_issue(ta + (c + 1) * 32, r[(c + 1) & 1]);
+                    const ulonglong2* nlv = reinterpret_cast<const ulonglong2*>(&s.nl[wg][buf][c * 32]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const ulonglong2 l2 = nlv[i];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int n = 4 * i + 2 * h;
+                            const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[c & 1][n]), __uint_as_float(r[c & 1][n + 1])),
+                                                      sl2, h ? l2.y : l2.x);
+                            float a, b;
+                            f2_unpack(x, a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            if (!whole) {
+                                const int col = c * 32 + n;
+                                a = col >= c_lo && col < rows ? a : 0.f;
+                                b = col + 1 >= c_lo && col + 1 < rows ? b : 0.f;
+                            }
+                            add[h] = f2_add(add[h], f2_pack(a, b));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.s_empty[wg][buf]);
+                float a, b, c, d;
+                f2_unpack(add[0], a, b);
+                f2_unpack(add[1], c, d);
+                total += (a + b) + (c + d);
+            }
+            if (csize > 1) {
+                // the partial sums change hands in the first tile's -lse buffers, which are free here
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+                s.nl[wg][0][row] = total;
+                cluster_sync();
+                if (rank == 0) {
+                    total = 0.f;
+                    for (int r = 0; r < csize; ++r)
+                        total += __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(&s.nl[wg][0][row]), r));
+                }
+            }
+            if (rank == 0 && key < w.len && ok) {
+                const int64_t at = (int64_t)w.b * p.kv.H + head;
+                const float old = p.acc_in ? p.decay * p.acc_in[at * p.ld_acc_in + key] : 0.f;
+                p.acc_out[at * p.ld_acc_out + key] = old + total;
+            }
+        }
+        if (csize > 1) {
+            __syncwarp();
+            if (warp >= 8) cluster_sync();
+            cluster_sync();  // the sums have been read
+        }
+    }
+    // nothing of this block may be in flight when it goes
+    __syncwarp();
+    if (warp == 8 && lane == 0) {
+        tc_commit(&s.done);
+        wait_drain(&s.done, 0);
+    }
+    if (warp == 9 && lane == 0)
+        for (int i = qf > C::Q_STAGES ? qf - C::Q_STAGES : 0; i < qf; ++i)
+            wait_drain(&s.q_full[i % C::Q_STAGES], i / C::Q_STAGES & 1);
+    if (warp == 10 && lane == 0)
+        for (int i = kf > C::K_STAGES ? kf - C::K_STAGES : 0; i < kf; ++i)
+            wait_drain(&s.k_full[i % C::K_STAGES], i / C::K_STAGES & 1);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace hsi
