@@ -41,8 +41,8 @@ struct AttendParams {
     const int32_t* q_start;
     int64_t T;       // tokens of q
     int max_q, max_kv, Hq, group;  // host bounds of new tokens and entries; query heads, per KV head
-    float sl2;       // scale * log2(e)
-    int causal;
+    float sl2;       // scale * log2(e) (attend_chunk_kernel: its size, above 0, and its sign)
+    int causal, negate;
     void* out;
     int64_t ot, oh;
     float* lse;      // [T][Hq] or null

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "attend.cuh"
+#include "attend_chunk.cuh"
 #include "evict.cuh"
 #include "paged.cuh"
 #include "rope.cuh"
@@ -190,6 +191,28 @@ hsi_status run_attend_token(const AttendParams& p, hsi_dtype dt, const CUtensorM
 }
 
 template <typename T, int D>
+hsi_status launch_attend_chunk(const AttendParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                               const CUtensorMap& qm, int tpt, int64_t grid, cudaStream_t s) {
+    using C = ChunkCfg<D>;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (smem_attr_once(attend_chunk_kernel<T, D>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
+    const hsi_status st = launch(attend_chunk_kernel<T, D>, dim3((unsigned)grid), dim3(CH_THREADS), C::SMEM_BYTES, s, p, km,
+                                 vm, qm, tpt);
+    if (st != HSI_OK) return st;
+    const unsigned rt = (unsigned)((p.max_q + 2 * tpt - 1) / (2 * tpt)) * (D / 16);
+    return launch(attend_chunk_join_kernel<T, D>, dim3(rt, p.kv.H, p.kv.B), dim3(2 * CH_ROWS), 0, s, p, (int)grid, tpt);
+}
+
+// CTAs of the chunk kernel: one an SM, no more than there can be key tiles.
+int64_t chunk_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int64_t max_kv) {
+    const int tpt = CH_ROWS / group;
+    const int64_t tiles =
+        (int64_t)B * heads * ((max_q + 2 * tpt - 1) / (2 * tpt)) * ((max_kv + CH_KEYS - 1) / CH_KEYS);
+    const int64_t most = sm_count();
+    return tiles < most ? tiles : most;
+}
+
+template <typename T, int D>
 hsi_status launch_weights_chunk(const AttendParams& p, const CUtensorMap& km, const CUtensorMap& qm, int tpt,
                                 cudaStream_t s) {
     using C = WeightsCfg<D>;
@@ -348,8 +371,13 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
 
 size_t hsi_paged_attention_ws(int32_t B, int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t max_q, int64_t max_kv) {
     if (B <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads || dim <= 0 || max_q <= 0 || max_kv <= 0) return 0;
-    const int64_t grid = attend_grid(B, kv_heads, q_heads / kv_heads, max_q, max_kv, false);
-    return attend_base_bytes(B) + align_up((size_t)grid * 2 * AT_ROWS * (dim + 2) * 4, 256);
+    const int group = q_heads / kv_heads;
+    size_t floats = (size_t)attend_grid(B, kv_heads, group, max_q, max_kv, false) * 2 * AT_ROWS * (dim + 2);
+    if ((int64_t)max_q * group > AT_ROWS && group <= 128) {
+        const size_t chunk = (size_t)chunk_grid(B, kv_heads, group, max_q, max_kv) * 2 * chunk_slot_floats(dim);
+        if (chunk > floats) floats = chunk;
+    }
+    return attend_base_bytes(B) + align_up(floats * 4, 256);
 }
 
 hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -372,6 +400,24 @@ hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t
     p.base = static_cast<int64_t*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attend_base_bytes(cache->B));
     CUtensorMap km, vm;
+    if (chunk_rows(p)) {
+        const int tpt = CH_ROWS / p.group;
+        CUtensorMap qm;
+        if ((st = paged_map(*cache, p.kv, cache->k, CH_KEYS, &km)) != HSI_OK) return st;
+        if ((st = paged_map(*cache, p.kv, cache->v, CH_KEYS, &vm)) != HSI_OK) return st;
+        if ((st = rows_map(cache->dtype, q, q_token_stride, q_head_stride, T, q_heads, cache->dim, p.group, tpt, &qm)) !=
+            HSI_OK)
+            return st;
+        p.negate = p.sl2 < 0.f;
+        p.sl2 = std::fmax(std::fabs(p.sl2), 1e-30f);  // above 0, so that -inf stays -inf: at scale 0 every p is 1
+        const int64_t grid = chunk_grid(cache->B, cache->heads, p.group, p.max_q, p.max_kv);
+        if (grid <= 0) return HSI_ERR_CUDA;
+        if (cache->dtype == HSI_BF16)
+            return cache->dim == 128 ? launch_attend_chunk<__nv_bfloat16, 128>(p, km, vm, qm, tpt, grid, stream)
+                                     : launch_attend_chunk<__nv_bfloat16, 64>(p, km, vm, qm, tpt, grid, stream);
+        return cache->dim == 128 ? launch_attend_chunk<__half, 128>(p, km, vm, qm, tpt, grid, stream)
+                                 : launch_attend_chunk<__half, 64>(p, km, vm, qm, tpt, grid, stream);
+    }
     if ((st = paged_map(*cache, p.kv, cache->k, AT_KT, &km)) != HSI_OK) return st;
     if ((st = paged_map(*cache, p.kv, cache->v, AT_KT, &vm)) != HSI_OK) return st;
     const int64_t grid = attend_grid(cache->B, cache->heads, p.group, p.max_q, p.max_kv, false);
