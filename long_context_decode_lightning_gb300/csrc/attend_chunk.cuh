@@ -13,8 +13,8 @@
 //
 // The running maximum is lazy: O is rescaled only where a row's maximum has
 // grown by more than 2^8 since the last time (p stays below 256, exact enough
-// in either type), which after the first tiles hardly happens; the row sum is
-// taken from the fp32 p after P has been handed over.
+// in either type), which after the first tiles hardly happens; the row sum
+// is taken from the fp32 p in the shadow of the exponentials.
 //
 // The units' key tiles (causal: only those that some row of the unit sees)
 // form one line that is cut into equal runs, one per SM, as for single tokens;
@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     }
     bool ok = true;  // false once a wait has run out: the role ends, after what it has in flight
 
-    // The softmax holds a row of S in registers: 208 a thread of the 168 x 12 warps that the
-    // block was launched with (8 x 208 + 4 x 88 = 12 x 168).
+    // The softmax holds a row of S in registers: 216 a thread of the 168 x 12 warps that the
+    // block was launched with (8 x 216 + 4 x 72 = 12 x 168).
     if (warp < 8) {  // softmax, a thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         int kvn = 0, seg = 0, it = 0;
         const int w = warp >> 2, row = threadIdx.x & 127;
         for (; ok && k.begin(p, tpt); k.advance(p, tpt)) {
@@ -260,23 +260,29 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 float mx = -INFINITY;
                 const bool full = k0 + CH_KEYS <= lim_all;
                 const int edge = lim - k0;  // columns below it are seen
-                tmem_ld32_issue(ts, r[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait(r[c]);
-                    if (c < 3) tmem_ld32_issue(ts + (c + 1) * 32, r[c + 1]);
-                    if (!full) {
+                    tmem_ld32_issue(ts + c * 32, r[c]);
+                }
+                tmem_ld_wait(r[0]);
+#pragma unroll
+                for (int c = 1; c < 4; ++c) tmem_ld_waited(r[c]);
+                if (!full) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[c][j] = c * 32 + j < edge ? r[c][j] : 0xFF800000u;
-                    }
-                    float m0 = __uint_as_float(r[c][0]), m1 = __uint_as_float(r[c][1]);
-#pragma unroll
-                    for (int j = 2; j < 32; j += 4) {
-                        m0 = max3(m0, __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
-                        if (j + 2 < 32) m1 = max3(m1, __uint_as_float(r[c][j + 2]), __uint_as_float(r[c][j + 3]));
-                    }
-                    mx = max3(mx, m0, m1);
                 }
+                float top[4];  // four chains of three-way maxima
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = max3(__uint_as_float(r[c][0]), __uint_as_float(r[c][1]), __uint_as_float(r[c][2]));
+#pragma unroll
+                    for (int j = 3; j < 31; j += 2)
+                        top[c] = max3(top[c], __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
+                    top[c] = fmaxf(top[c], __uint_as_float(r[c][31]));
+                }
+                mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                 const float mt = mx * p.sl2;  // p.sl2 > 0
                 if (__any_sync(~0u, mt > m_used + CH_LAZY)) {
                     const float m_new = fmaxf(m_used, mt);
@@ -311,6 +317,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t pk[32];
@@ -324,8 +331,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                             f2_unpack(x, a, e);
                             a = ex2(a);
                             e = ex2(e);
-                            r[c][j] = __float_as_uint(a);
-                            r[c][j + 1] = __float_as_uint(e);
+                            sum[j >> 1 & 1] = f2_add(sum[j >> 1 & 1], f2_pack(a, e));
                             pk[(c - 2 * hf) * 16 + j / 2] = pack2<T>(a, e);
                         }
                     }
@@ -335,14 +341,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.p_full[w][hf]);
                 }
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        sum[0] = f2_add(sum[0], f2_pack(__uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1])));
-                        sum[1] = f2_add(sum[1], f2_pack(__uint_as_float(r[c][j + 2]), __uint_as_float(r[c][j + 3])));
-                    }
                 float a, e, c2, d2;
                 f2_unpack(sum[0], a, e);
                 f2_unpack(sum[1], c2, d2);
@@ -391,7 +389,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             it += k.n;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 9) {  // copies: Q, then K and V in turn
             int qn = 0, kvn = 0;  // fills of the query ring, and of the key and value ring, so far
             for (; ok && k.begin(p, tpt); k.advance(p, tpt)) {
@@ -437,77 +435,103 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 for (int i = kvn > C::KV_STAGES ? kvn - C::KV_STAGES : 0; i < kvn; ++i)
                     wait_drain(&s.kv_full[i % C::KV_STAGES], i / C::KV_STAGES & 1);
             }
-        } else if (warp == 8) {  // products, one thread
-            int qn = 0, kvn = 0;                  // uses of the rings so far
-            int seg[2] = {0, 0}, it[2] = {0, 0};  // of each row tile: segments and key tiles so far
-            for (; lane == 0 && ok && k.begin(p, tpt); k.advance(p, tpt)) {
-                if (lane == 0) {
-                    constexpr uint32_t id_s = idesc_f16(is_bf16<T>, 128, CH_KEYS, false);
-                    constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, D, true);
-                    const uint32_t neg = p.negate ? 1u << 13 : 0u;  // S of -Q: a negative scale
-                    const int qst = qn % C::Q_STAGES;
-                    auto product_s = [&](int w, int st) {
-                        const uint32_t qa = smem_u32(q_ring + (qst * 2 + w) * C::TILE_BYTES);
-                        const uint32_t ka = smem_u32(kv_ring + st * C::TILE_BYTES);
+        } else if (warp == 8) {  // products: the warp waits, one lane issues
+            constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, D, true);
+            const uint32_t id_s = idesc_f16(is_bf16<T>, 128, CH_KEYS, false) | (p.negate ? 1u << 13 : 0u);  // of -Q
+            constexpr uint32_t TILE16 = C::TILE_BYTES >> 4;
+            const uint32_t tm = uniform(tmem);
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_ring)), k_desc = smem_desc_sw128(smem_u32(kv_ring)),
+                           v_desc = smem_desc_sw128(smem_u32(kv_ring), C::HALF_BYTES);
+            int qst = 0, st = 0;          // the query stage, the stage of the next K or V
+            uint32_t qph = 0, ph = 0;     // and their phases
+            uint32_t it = 0, seg = 0;     // of row tile w, in bit w: parities of its key tiles and segments so far
+            auto product_s = [&](int w) {
+                const uint64_t a = uniform(q_desc + (qst * 2 + w) * TILE16), b = uniform(k_desc + st * TILE16);
+                if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = (ks >> 2) * C::HALF_BYTES + (ks & 3) * 32;
-                            mma_f16_ss(tmem + w * 128, smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_s | neg, ks > 0);
-                        }
-                        tc_commit(&s.s_full[w]);
-                    };
-                    // the first tile of the segment
-                    ok = ok && wait_bounded(&s.q_full[qst], qn / C::Q_STAGES & 1, &s.abort);
-                    ok = ok && wait_bounded(&s.kv_full[kvn % C::KV_STAGES], kvn / C::KV_STAGES & 1, &s.abort);
-                    if (ok) {
-                        tc_fence_after();
-                        for (int w = 0; w < k.tiles; ++w) product_s(w, kvn % C::KV_STAGES);
-                        tc_commit(&s.kv_empty[kvn % C::KV_STAGES]);
-                        if (k.n == 1) tc_commit(&s.q_empty[qst]);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * C::HALF_BYTES + (ks & 3) * 32) >> 4;
+                        if (ks == 0) mma_f16_ss(tm + w * 128, a, b, id_s);
+                        else mma_f16_ss_add(tm + w * 128, a + off, b + off, id_s);
                     }
-                    for (int i = 0; i < k.n && ok; ++i) {
-                        const int vst = (kvn + 1) % C::KV_STAGES, vph = (kvn + 1) / C::KV_STAGES & 1;
-                        const int kst = (kvn + 2) % C::KV_STAGES, kph = (kvn + 2) / C::KV_STAGES & 1;
-                        const uint32_t va = smem_u32(kv_ring + vst * C::TILE_BYTES);
-                        for (int w = 0; w < k.tiles && ok; ++w) {
-                            if (w == 0) ok = wait_bounded(&s.kv_full[vst], vph, &s.abort);
-                            if (i == 0) ok = ok && wait_bounded(&s.o_empty[w], (seg[w] & 1) ^ 1, &s.abort);
+                    tc_commit(&s.s_full[w]);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            auto next = [&]() {
+                if (++st == C::KV_STAGES) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            for (; k.begin(p, tpt); k.advance(p, tpt)) {
+                // S of the first key tile
+                ok = wait_bounded(&s.q_full[qst], qph, &s.abort) && wait_bounded(&s.kv_full[st], ph, &s.abort);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                product_s(0);
+                if (k.tiles == 2) product_s(1);
+                commit(&s.kv_empty[st]);
+                if (k.n == 1) commit(&s.q_empty[qst]);
+                next();
+                for (int i = 0; i < k.n; ++i) {
+                    const int vst = st;
+                    const uint64_t v = uniform(v_desc + vst * TILE16);
+                    const uint32_t more = uniform((uint32_t)i);
+                    ok = wait_bounded(&s.kv_full[st], ph, &s.abort);
+                    next();  // to the next K
+                    auto tile = [&](int w) {
+                        if (i == 0) ok = ok && wait_bounded(&s.o_empty[w], (seg >> w & 1) ^ 1, &s.abort);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait_bounded(&s.p_full[w][h], (it[w] + i) & 1, &s.abort);
-                                if (!ok) break;
-                                tc_fence_after();
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && wait_bounded(&s.p_full[w][h], (it >> w ^ i) & 1, &s.abort);
+                            if (!__all_sync(~0u, ok)) return;
+                            tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
-                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                                    mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8,
-                                               smem_desc_sw128(va + ks * 2048, C::HALF_BYTES), id_o, i > 0 || ks > 0);
+                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks) {
+                                    const uint32_t d = tm + 256 + w * 128, a = tm + w * 128 + ks * 8;
+                                    if (ks == 0) mma_f16_ts(d, a, v, id_o, more);
+                                    else mma_f16_ts_add(d, a, v + ks * 128, id_o);
+                                }
                             }
-                            if (!ok) break;
-                            if (i + 1 < k.n) {
-                                if (w == 0) ok = wait_bounded(&s.kv_full[kst], kph, &s.abort);
-                                if (!ok) break;
-                                tc_fence_after();
-                                product_s(w, kst);
-                            } else {
-                                tc_commit(&s.o_full[w]);
-                            }
+                            __syncwarp();
                         }
-                        if (!ok) break;
-                        tc_commit(&s.kv_empty[vst]);
                         if (i + 1 < k.n) {
-                            tc_commit(&s.kv_empty[kst]);
-                            if (i + 2 == k.n) tc_commit(&s.q_empty[qst]);
+                            if (w == 0) ok = wait_bounded(&s.kv_full[st], ph, &s.abort);
+                            if (!__all_sync(~0u, ok)) return;
+                            tc_fence_after();
+                            product_s(w);
+                        } else {
+                            commit(&s.o_full[w]);
                         }
-                        kvn += 2;
-                    }
-                    ++qn;
-                    for (int w = 0; w < k.tiles; ++w) {
-                        ++seg[w];
-                        it[w] += k.n;
+                    };
+                    tile(0);
+                    if (k.tiles == 2) tile(1);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    commit(&s.kv_empty[vst]);
+                    if (i + 1 < k.n) {
+                        commit(&s.kv_empty[st]);
+                        if (i + 2 == k.n) commit(&s.q_empty[qst]);
+                        next();
                     }
                 }
+                if (!ok) break;
+                if (++qst == C::Q_STAGES) {
+                    qst = 0;
+                    qph ^= 1;
+                }
+                const uint32_t both = k.tiles == 2 ? 3 : 1;
+                seg ^= both;
+                if (k.n & 1) it ^= both;
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_commit(&s.done);
                 wait_drain(&s.done, 0);
             }

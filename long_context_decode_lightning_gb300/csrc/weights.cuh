@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
     w.load(p);
     bool ok = true;
     int kf = 0, qf = 0;  // fills (or uses) of the key and query rings so far
+    int q_st = 0;        // the products' query stage and its phase
+    uint32_t q_ph = 0;
     for (int64_t u = blockIdx.x / csize; w.seek(p, u); u += step) {
         const int local = (int)(u - w.first), head = local / w.nt, k0 = (local % w.nt) * WC_KEYS;
         // query tiles that see any of the unit's entries
@@ -153,34 +155,44 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                                      w.at + j * tpt, &s.q_full[st]);
                 }
             }
-        } else if (warp == 8) {  // products
-            if (lane == 0 && j0 < j1) {
+        } else if (warp == 8) {  // products: the warp waits, one lane issues
+            if (j0 < j1) {
                 constexpr uint32_t idesc = idesc_f16(is_bf16<T>, 128, WC_ROWS, false);
                 const int kst = kf % C::K_STAGES;
+                const uint32_t tm = uniform(tmem);
+                const uint64_t kd = uniform(smem_desc_sw128(smem_u32(k_ring + kst * C::K_BYTES)));
                 ok = ok && wait_bounded(&s.k_full[kst], kf / C::K_STAGES & 1, &s.abort);
-                for (int j = j0; j < j1 && ok; j += csize) {
-                    const int qst = qf % C::Q_STAGES;
-                    ok = wait_bounded(&s.q_full[qst], qf / C::Q_STAGES & 1, &s.abort);
-                    if (!ok) break;
-                    const uint32_t qa = smem_u32(q_ring + qst * C::Q_BYTES);
+                for (int j = j0; j < j1 && __all_sync(~0u, ok); j += csize) {
                     const int buf = qf & 1;
-                    for (int kt = 0; kt < 2 && ok; ++kt) {
-                        ok = wait_bounded(&s.s_empty[kt][buf], (qf >> 1 & 1) ^ 1, &s.abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t ka = smem_u32(k_ring + kst * C::K_BYTES + kt * C::Q_BYTES);
+                    ok = wait_bounded(&s.q_full[q_st], q_ph, &s.abort);
+                    const uint64_t qd = uniform(smem_desc_sw128(smem_u32(q_ring + q_st * C::Q_BYTES)));
+                    const uint32_t d0 = uniform(tm + buf * 128);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (k >> 2) * C::HALF_BYTES + (k & 3) * 32;
-                            mma_f16_ss(tmem + (kt * 2 + buf) * 128, smem_desc_sw128(ka + off), smem_desc_sw128(qa + off),
-                                       idesc, k > 0);
+                    for (int kt = 0; kt < 2; ++kt) {
+                        ok = ok && wait_bounded(&s.s_empty[kt][buf], (qf >> 1 & 1) ^ 1, &s.abort);
+                        if (!__all_sync(~0u, ok)) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t off = ((ks >> 2) * C::HALF_BYTES + (ks & 3) * 32) >> 4;
+                                const uint64_t a = kd + kt * (C::Q_BYTES >> 4) + off;
+                                if (ks == 0) mma_f16_ss(d0 + kt * 256, a, qd, idesc);
+                                else mma_f16_ss_add(d0 + kt * 256, a, qd + off, idesc);
+                            }
+                            tc_commit(&s.s_full[kt][buf]);
+                            if (kt == 1) tc_commit(&s.q_empty[q_st]);
                         }
-                        tc_commit(&s.s_full[kt][buf]);
+                        __syncwarp();
                     }
-                    tc_commit(&s.q_empty[qst]);
                     ++qf;
+                    if (++q_st == C::Q_STAGES) {
+                        q_st = 0;
+                        q_ph ^= 1;
+                    }
                 }
-                tc_commit(&s.k_empty[kst]);
+                if (elect_one()) tc_commit(&s.k_empty[kst]);
+                __syncwarp();
                 ++kf;
             }
         } else {  // weights: a thread per entry
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
     }
     // nothing of this block may be in flight when it goes
     __syncwarp();
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
         tc_commit(&s.done);
         wait_drain(&s.done, 0);
     }
