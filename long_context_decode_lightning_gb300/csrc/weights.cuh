@@ -12,11 +12,14 @@
 // and 16384 exponentials (512 cycles of the SM's special-function units): both
 // bound it together. A CTA keeps 256 entries of K in shared memory and streams
 // the query tiles past them (one 32 KB tile per 1024 tensor cycles; 128 entries
-// would ask twice the L2 rate), two warpgroups with two accumulators each.
+// would ask twice the L2 rate), two accumulators per 128 entries, and
+// four warpgroups: one per 128 entries and half of the columns, so that four warps a
+// scheduler hide the latencies of loads and exponentials (two: 204 us against 165).
 // Few entries: a cluster shares a unit's query tiles and adds up the partial
 // sums through distributed shared memory, in rank order.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "attend.cuh"
 #include "common.cuh"
@@ -27,7 +30,7 @@ namespace hsi {
 
 constexpr int WC_KEYS = 256;                 // entries of a unit: two accumulator tiles of 128
 constexpr int WC_ROWS = 128;                 // query rows of a tile
-constexpr int WC_THREADS = 32 * 11;          // 8 epilogue warps, MMA, query producer, key producer
+constexpr int WC_THREADS = 32 * 19;          // 16 epilogue warps, MMA, query producer, key producer
 
 template <int D>
 struct WeightsCfg {
@@ -38,7 +41,7 @@ struct WeightsCfg {
     static constexpr int Q_STAGES = D == 128 ? 3 : 6;
     static constexpr int RING_BYTES = K_STAGES * K_BYTES + Q_STAGES * Q_BYTES;
     struct Tail {
-        float nl[2][2][WC_ROWS];  // -lse (base 2) of a tile's rows, per warpgroup, double-buffered
+        float nl[4][2][WC_ROWS / 2];  // -lse (base 2) of a warpgroup's columns, double-buffered
         uint64_t k_full[K_STAGES], k_empty[K_STAGES], q_full[Q_STAGES], q_empty[Q_STAGES];
         uint64_t s_full[2][2], s_empty[2][2], done;
         uint32_t tmem;
@@ -82,14 +85,14 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::K_STAGES; ++i) mbar_init(&s.k_full[i], 1), mbar_init(&s.k_empty[i], 1);
         for (int i = 0; i < C::Q_STAGES; ++i) mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&s.s_full[i >> 1][i & 1], 1), mbar_init(&s.s_empty[i >> 1][i & 1], 4);
+        for (int i = 0; i < 4; ++i) mbar_init(&s.s_full[i >> 1][i & 1], 1), mbar_init(&s.s_empty[i >> 1][i & 1], 8);
         mbar_init(&s.done, 1);
         fence_mbar_init();
         s.abort = 0;
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&qmap);
     }
-    if (warp == 8) tmem_alloc(&s.tmem, 512);
+    if (warp == 16) tmem_alloc(&s.tmem, 512);
     // the rows past a tile's last whole token are never loaded: zeros, so that their products are
     for (int i = threadIdx.x; i < C::Q_STAGES * (D / 64) * (WC_ROWS - rpt) * 8; i += WC_THREADS) {
         const int ch = i & 7, r = (i >> 3) % (WC_ROWS - rpt), half = (i >> 3) / (WC_ROWS - rpt);
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
         const int past = w.len - w.m, t_first = p.causal && k0 > past ? k0 - past : 0;
         const int j0 = t_first / tpt + rank, j1 = (w.m + tpt - 1) / tpt;
 
-        if (warp == 10) {  // keys: a lane per box
+        if (warp == 18) {  // keys: a lane per box
             const int box = p.kv.page_shift < 7 ? 1 << p.kv.page_shift : 128;
             const int halves = D / 64, nbox = WC_KEYS / box * halves;
             const int n = min(w.len - k0, WC_KEYS), live = (n + box - 1) / box * halves;
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                     ++kf;
                 }
             }
-        } else if (warp == 9) {  // query tiles
+        } else if (warp == 17) {  // query tiles
             if (lane == 0) {
                 for (int j = j0; j < j1 && ok; j += csize) {
                     const int st = qf % C::Q_STAGES;
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                                      w.at + j * tpt, &s.q_full[st]);
                 }
             }
-        } else if (warp == 8) {  // products: the warp waits, one lane issues
+        } else if (warp == 16) {  // products: the warp waits, one lane issues
             if (j0 < j1) {
                 constexpr uint32_t idesc = idesc_f16(is_bf16<T>, 128, WC_ROWS, false);
                 const int kst = kf % C::K_STAGES;
@@ -195,82 +198,100 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                 __syncwarp();
                 ++kf;
             }
-        } else {  // weights: a thread per entry
-            const int wg = warp >> 2, key = k0 + wg * 128 + (threadIdx.x & 127), row = threadIdx.x & 127;
+        } else {  // weights: a thread per entry and half of the columns
+            const int wg = warp >> 2, kt = wg >> 1, half = wg & 1;
+            const int key = k0 + kt * 128 + (threadIdx.x & 127), row = half * 64 + (threadIdx.x & 63);
+            const bool loads = (threadIdx.x & 127) < 64;
             const int rtok = row / p.group, rhead = head * p.group + row % p.group;
             // first token that sees this entry
             const int t_min = p.causal ? key - past : 0;
             const uint64_t sl2 = f2_pack(p.sl2, p.sl2);
             float total = 0.f;
-            auto load_nl = [&](int j) {  // of this thread's row in tile j
+            // the lse of this thread's row in tile j, loaded a tile ahead; nothing is computed from it
+            // before the next tile, which would wait for the load
+            const float* lse = p.lse_in + (int64_t)w.at * p.Hq + rhead;
+            auto load_lse = [&](int j) {
                 const int t = j * tpt + rtok;
-                if (j >= j1 || row >= rpt || t >= w.m) return -INFINITY;
-                const float v = __ldg(p.lse_in + (int64_t)(w.at + t) * p.Hq + rhead);
-                return v == -INFINITY ? -INFINITY : -v * LOG2E;
+                float v = -INFINITY;
+                if (loads && j < j1 && row < rpt && t < w.m) v = __ldg(lse + (int64_t)t * p.Hq);
+                return v;
             };
-            float nl = load_nl(j0);
+            float next = load_lse(j0);
             for (int j = j0; j < j1; j += csize, ++qf) {
                 const int buf = qf & 1;
-                s.nl[wg][buf][row] = nl;
+                if (loads) s.nl[wg][buf][threadIdx.x & 63] = next == -INFINITY ? -INFINITY : -next * LOG2E;
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-                nl = load_nl(j + csize);
-                ok = ok && __all_sync(~0u, wait_bounded(&s.s_full[wg][buf], qf >> 1 & 1, &s.abort));
+                next = load_lse(j + csize);
+                ok = ok && __all_sync(~0u, wait_bounded(&s.s_full[kt][buf], qf >> 1 & 1, &s.abort));
                 if (!ok) continue;
                 tc_fence_after();
-                const uint32_t ta = tmem + (uint32_t)((warp & 3) * 32 << 16) + (wg * 2 + buf) * 128;
-                // columns [c_lo, c_hi) count; tiles where all do need no comparison
-                const int rows = min(rpt, (w.m - j * tpt) * p.group);
-                const int c_lo = (t_min - j * tpt) * p.group;
-                const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + wg * 128 + 127 - past);
-                uint64_t add[2] = {0, 0};
-                uint32_t r[2][32];
-                tmem_ld32_issue(ta, r[0]);
+                const uint32_t ta = tmem + (uint32_t)((warp & 3) * 32 << 16) + (kt * 2 + buf) * 128 + half * 64;
+                // columns [c_lo, c_hi) of this half count; tiles where all do need no comparison
+                const int rows = min(rpt, (w.m - j * tpt) * p.group), c_hi = rows - half * 64;
+                const int c_lo = (t_min - j * tpt) * p.group - half * 64;
+                const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + kt * 128 + 127 - past);
+                uint64_t add[4] = {0, 0, 0, 0};
+                auto columns = [&](auto masked) {
+                    uint32_t r[2][32];
+                    tmem_ld32_issue(ta, r[0]);
+                    tmem_ld32_issue(ta + 32, r[1]);
+                    tmem_ld_wait(r[0]);
+                    tmem_ld_waited(r[1]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait(r[c & 1]);
-                    if (c < 3) tmem_ld32_issue(ta + (c + 1) * 32, r[(c + 1) & 1]);
-                    const ulonglong2* nlv = reinterpret_cast<const ulonglong2*>(&s.nl[wg][buf][c * 32]);
+                    for (int c = 0; c < 2; ++c) {
+                        const ulonglong2* nlv = reinterpret_cast<const ulonglong2*>(&s.nl[wg][buf][c * 32]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const ulonglong2 l2 = nlv[i];
+                        for (int i = 0; i < 8; ++i) {
+                            const ulonglong2 l2 = nlv[i];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int n = 4 * i + 2 * h;
-                            const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[c & 1][n]), __uint_as_float(r[c & 1][n + 1])),
-                                                      sl2, h ? l2.y : l2.x);
-                            float a, b;
-                            f2_unpack(x, a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            if (!whole) {
-                                const int col = c * 32 + n;
-                                a = col >= c_lo && col < rows ? a : 0.f;
-                                b = col + 1 >= c_lo && col + 1 < rows ? b : 0.f;
+                            for (int h = 0; h < 2; ++h) {
+                                const int n = 4 * i + 2 * h;
+                                const uint64_t x =
+                                    f2_fma(f2_pack(__uint_as_float(r[c][n]), __uint_as_float(r[c][n + 1])), sl2,
+                                           h ? l2.y : l2.x);
+                                float a, b;
+                                f2_unpack(x, a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                if (masked.value) {
+                                    const int col = c * 32 + n;
+                                    a = col >= c_lo && col < c_hi ? a : 0.f;
+                                    b = col + 1 >= c_lo && col + 1 < c_hi ? b : 0.f;
+                                }
+                                add[n / 2 & 3] = f2_add(add[n / 2 & 3], f2_pack(a, b));
                             }
-                            add[h] = f2_add(add[h], f2_pack(a, b));
                         }
                     }
-                }
+                };
+                if (whole) columns(std::false_type{});
+                else columns(std::true_type{});
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.s_empty[wg][buf]);
+                if (lane == 0) mbar_arrive(&s.s_empty[kt][buf]);
                 float a, b, c, d;
-                f2_unpack(add[0], a, b);
-                f2_unpack(add[1], c, d);
+                f2_unpack(f2_add(add[0], add[1]), a, b);
+                f2_unpack(f2_add(add[2], add[3]), c, d);
                 total += (a + b) + (c + d);
             }
+            // the two halves' sums, then the ranks', through the -lse buffers (128 values a
+            // warpgroup), which nobody reads past the barrier
+            const int tid = threadIdx.x & 127;
+            float* part = &s.nl[wg][0][0] + tid;
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+            if (half == 1) *part = total;
+            asm volatile("bar.sync %0, 256;" ::"r"(5 + kt) : "memory");
+            if (half == 0) total += (&s.nl[wg + 1][0][0])[tid];
+            asm volatile("bar.sync %0, 256;" ::"r"(5 + kt) : "memory");
             if (csize > 1) {
-                // the partial sums change hands in the first tile's -lse buffers, which are free here
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-                s.nl[wg][0][row] = total;
+                if (half == 0) *part = total;
                 cluster_sync();
-                if (rank == 0) {
+                if (rank == 0 && half == 0) {
                     total = 0.f;
                     for (int r = 0; r < csize; ++r)
-                        total += __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(&s.nl[wg][0][row]), r));
+                        total += __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(part), r));
                 }
             }
-            if (rank == 0 && key < w.len && ok) {
+            if (rank == 0 && half == 0 && key < w.len && ok) {
                 const int64_t at = (int64_t)w.b * p.kv.H + head;
                 const float old = p.acc_in ? p.decay * p.acc_in[at * p.ld_acc_in + key] : 0.f;
                 p.acc_out[at * p.ld_acc_out + key] = old + total;
@@ -278,26 +299,26 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
         }
         if (csize > 1) {
             __syncwarp();
-            if (warp >= 8) cluster_sync();
+            if (warp >= 16) cluster_sync();
             cluster_sync();  // the sums have been read
         }
     }
     // nothing of this block may be in flight when it goes
     __syncwarp();
-    if (warp == 8 && elect_one()) {
+    if (warp == 16 && elect_one()) {
         tc_commit(&s.done);
         wait_drain(&s.done, 0);
     }
-    if (warp == 9 && lane == 0)
+    if (warp == 17 && lane == 0)
         for (int i = qf > C::Q_STAGES ? qf - C::Q_STAGES : 0; i < qf; ++i)
             wait_drain(&s.q_full[i % C::Q_STAGES], i / C::Q_STAGES & 1);
-    if (warp == 10 && lane == 0)
+    if (warp == 18 && lane == 0)
         for (int i = kf > C::K_STAGES ? kf - C::K_STAGES : 0; i < kf; ++i)
             wait_drain(&s.k_full[i % C::K_STAGES], i / C::K_STAGES & 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace hsi
