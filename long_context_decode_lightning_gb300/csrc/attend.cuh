@@ -133,7 +133,10 @@ struct AttendCfg {
     static constexpr int HALF_BYTES = AT_KT * 128;                 // 64 values of every entry of a tile
     static constexpr int K_BYTES = HALF_BYTES * (D / 64);
     static constexpr int STAGE_BYTES = WEIGHTS ? K_BYTES : 2 * K_BYTES;
-    static constexpr int STAGES = 98304 / STAGE_BYTES;             // 96 KB a CTA, two CTAs an SM
+    // CTAs an SM, and stages that fill its shared memory. The weights' tiles are half the bytes
+    // at the same latency of a tile's work: two CTAs reach 72% of the copy rate, three 90%.
+    static constexpr int CTAS = WEIGHTS ? 3 : 2;
+    static constexpr int STAGES = (WEIGHTS ? 65536 : 98304) / STAGE_BYTES;
     static constexpr int RED_BYTES = WEIGHTS ? 0 : AT_WARPS * AT_ROWS * 32 * 4;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + RED_BYTES;
 };
@@ -157,7 +160,7 @@ __device__ __forceinline__ void walk_load(const AttendParams& p, LineWalk& w) {
 __device__ __forceinline__ int64_t walk_tiles(const LineWalk& w) { return (int64_t)w.nt * w.units; }
 
 template <typename T, int D, bool WEIGHTS>
-__global__ void __launch_bounds__(AT_THREADS, 2)
+__global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     attend_token_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
     using C = AttendCfg<D, WEIGHTS>;
@@ -332,10 +335,22 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
         const int krow = warp * 16 + (mat >> 1) * 8 + mrow;  // K: matrices (entries 0-7, 0-7, 8-15, 8-15) x (chunk, +1)
         const int vrow = warp * 16 + (mat & 1) * 8 + mrow;   // V: matrices (0-7, 8-15) x (chunk, chunk, +1, +1)
 
+        // weights: lanes 0 .. 15 write an entry each, the one whose sum they hold after the
+        // shuffles; its old weight is loaded a tile ahead
+        const int mine = (lane >> 3 & 1) * 8 + (lane & 3) * 2 + (lane >> 2 & 1);
+        const int64_t acc_row = (int64_t)w.b * p.kv.H + head;
+        const float* acc_in = WEIGHTS && p.acc_in ? p.acc_in + acc_row * p.ld_acc_in : nullptr;
+        float* acc_out = WEIGHTS ? p.acc_out + acc_row * p.ld_acc_out : nullptr;
+        float old = 0.f;
+        if (WEIGHTS && acc_in && lane < 16 && tile0 * AT_KT + warp * 16 + mine < w.len)
+            old = acc_in[tile0 * AT_KT + warp * 16 + mine];
+
         for (int i = 0; i < n_tiles; ++i) {
             ok = ok && __all_sync(~0u, wait_bounded(&full[stage], phase, &s_abort));
             const uint32_t kbase = smem_u32(stage0 + stage * C::STAGE_BYTES);
             const int e0 = (tile0 + i) * AT_KT + warp * 16;
+            float next = 0.f;
+            if (WEIGHTS && acc_in && lane < 16 && e0 + AT_KT + mine < w.len) next = acc_in[e0 + AT_KT + mine];
             float add[4] = {};  // weights of entries kq, kq + 1, 8 + kq, 9 + kq
             for (int rr = WEIGHTS ? 0 : rt; ok && rr < rt_end; ++rr) {
                 if (WEIGHTS && rt_end > 1) load_rows(rr);
@@ -441,16 +456,11 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
                     add[c] += __shfl_xor_sync(~0u, add[c], 8);
                     add[c] += __shfl_xor_sync(~0u, add[c], 16);
                 }
-                if (lane < 4) {
-                    const int64_t row = (int64_t)w.b * p.kv.H + head;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int key = e0 + (c >> 1) * 8 + kq + (c & 1);
-                        if (key >= w.len) continue;
-                        const float old = p.acc_in ? p.decay * p.acc_in[row * p.ld_acc_in + key] : 0.f;
-                        p.acc_out[row * p.ld_acc_out + key] = old + add[c];
-                    }
+                if (e0 + mine < w.len && lane < 16) {
+                    const float sum = lane < 8 ? (lane < 4 ? add[0] : add[1]) : (lane < 12 ? add[2] : add[3]);
+                    acc_out[e0 + mine] = p.decay * old + sum;
                 }
+                old = next;
             }
         }
         if constexpr (!WEIGHTS) {  // join the four warps

@@ -156,11 +156,11 @@ hsi_status launch_rope(const RopeParams& p0, cudaStream_t s) {
     return launch(rope_kernel<T>, dim3((unsigned)((p.T + p.tb - 1) / p.tb)), dim3(ROPE_THREADS), 0, s, p);
 }
 
-// CTAs of the few-row kernels: two an SM, no more than there can be tiles.
+// CTAs of the few-row kernels: what the SMs hold, no more than there can be tiles.
 int64_t attend_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int64_t max_kv, bool weights) {
     const int64_t rt = weights ? 1 : ((int64_t)max_q * group + AT_ROWS - 1) / AT_ROWS;
     const int64_t tiles = (int64_t)B * heads * rt * ((max_kv + AT_KT - 1) / AT_KT);
-    const int64_t most = 2 * (int64_t)sm_count();
+    const int64_t most = (weights ? AttendCfg<64, true>::CTAS : AttendCfg<64, false>::CTAS) * (int64_t)sm_count();
     return tiles < most ? tiles : most;
 }
 
