@@ -7,17 +7,20 @@
 //
 // evict_select_kernel: one cluster per row. Each CTA reads its slice of the
 // weights once and keeps them in shared memory (past EV_CAP of them it reads the
-// rest again each pass, and then acc_out must not be acc); three radix passes
-// (11, 11, 10 bits from the top) find the key of the last kept entry, the
-// histograms of the slices added up through distributed shared memory. A
-// second walk over the slice counts, then writes, in index order. Bound: one
+// rest again each pass, and then acc_out must not be acc). Passes of 2048 bins
+// over the keys' own range (a fixed first digit would drop all weights of like
+// size into a few bins, whose atomics serialise) narrow down the key of the
+// last kept entry; the histograms of the slices are added up through
+// distributed shared memory. Two passes mostly do, three always. A
+// last walk over the slice counts, then writes, in index order. Bound: one
 // 4-byte read per entry, and the latency of the passes.
 //
-// paged_compact_kernel: copies of 64-byte column slices, 64 entries at a time
-// and eight such rounds in flight. In place (the same table), a CTA walks its
-// slice from the front: the sources of places i >= c lie at c or behind, so
-// nothing that is still to be read has been written when a round's reads
-// precede its writes. To other pages the places are split over more CTAs.
+// paged_compact_kernel: copies of whole entries, eight 16-byte vectors of each
+// thread in flight. In place (the same table), the places are walked from the
+// front in turns: the sources of places i >= c lie at c or behind, so nothing
+// that is still to be read has been written when a turn's reads precede its
+// writes; the blocks of a turn are a cluster with a barrier between the two.
+// To other pages every block goes its own way.
 // Bound: HBM, one read and one write of the kept entries.
 #pragma once
 #include <cstdint>
@@ -48,11 +51,10 @@ struct EvictParams {
 
 struct EvictSmem {
     uint32_t hist[EV_BINS];
-    uint32_t warp_gt[EV_THREADS / 32], warp_eq[EV_THREADS / 32];
-    uint32_t gt, eq;         // of this slice
-    uint32_t digit, above;   // the pass's bin and the entries above it
-    uint32_t scan[EV_THREADS / 32];
-    float w[EV_CAP];         // the slice's weights
+    uint32_t scan[EV_THREADS / 32], scan2[EV_THREADS / 32];
+    uint32_t low, high;            // of this slice: the range of the unprotected keys; later its two counts
+    uint32_t digit, above, count;  // the pass's bin, the entries above it and in it
+    float w[EV_CAP];               // the slice's weights
 };
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -70,6 +72,20 @@ __device__ __forceinline__ uint32_t dsmem_load(const uint32_t* mine, uint32_t ra
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// The sum of v over the threads before this one. Whole block; scan: a word a warp.
+__device__ __forceinline__ uint32_t block_before(uint32_t* scan, uint32_t v) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    return incl - v + __reduce_add_sync(~0u, lane < warp ? scan[lane] : 0u);
 }
 
 __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams p, int csize) {
@@ -91,148 +107,174 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
     const int n_keep = (int)(len < p.budget ? len : p.budget);
     if (rank == 0 && row % p.H == 0 && tid == 0) p.new_len[b] = n_keep;
 
-    // this CTA's slice [lo, hi), in whole warps' turns of 32
-    const int64_t per = ((len + csize - 1) / csize + 31) / 32 * 32;
-    const int64_t lo = min(len, rank * per), hi = min(len, lo + per);
-    const int n = (int)(hi - lo), held = n < EV_CAP ? n : EV_CAP;
-    const int head = (int)min((int64_t)held, (int64_t)((16 - ((reinterpret_cast<uintptr_t>(acc + lo) & 15))) % 16 / 4));
-    for (int i = tid; i < head; i += EV_THREADS) s.w[i] = acc[lo + i];
+    // this CTA's slice: entries [lo, lo + n)
+    const int64_t per = (len + csize - 1) / csize;
+    const int64_t lo = min(len, rank * per);
+    const int n = (int)(min(len, lo + per) - lo), held = n < EV_CAP ? n : EV_CAP;
+    acc += lo;
+    // protected: i < p_lo or i >= p_hi; they rank above every weight (order_key of a number is below ~0u)
+    const int p_lo = (int)max((int64_t)0, min((int64_t)n, p.sink - lo));
+    const int p_hi = (int)max((int64_t)0, min((int64_t)n, len - p.recent - lo));
+    auto weight_at = [&](int i) { return i < held ? s.w[i] : acc[i]; };
+    auto key_of = [&](int i, float w) { return i < p_lo || i >= p_hi ? ~0u : order_key(w); };
+
+    // the weights into shared memory, and the range of the unprotected keys
+    uint32_t low = ~0u, high = 0u;
+    auto seen = [&](int i, float w) {
+        const uint32_t k = key_of(i, w);
+        low = min(low, k);
+        if (k != ~0u) high = max(high, k);
+    };
+    const int head = min(held, (int)((16 - (reinterpret_cast<uintptr_t>(acc) & 15)) % 16 / 4));
+    if (tid < head) {
+        s.w[tid] = acc[tid];
+        seen(tid, s.w[tid]);
+    }
+#pragma unroll 2
     for (int i = head + 4 * tid; i < held; i += 4 * EV_THREADS) {
         if (i + 4 <= held) {
-            const float4 v = *reinterpret_cast<const float4*>(acc + lo + i);
-            s.w[i] = v.x;
-            s.w[i + 1] = v.y;
-            s.w[i + 2] = v.z;
-            s.w[i + 3] = v.w;
+            const float4 v = *reinterpret_cast<const float4*>(acc + i);
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s.w[i + j] = f[j];
+                seen(i + j, f[j]);
+            }
         } else {
-            for (int j = i; j < held; ++j) s.w[j] = acc[lo + j];
+            for (int j = i; j < held; ++j) {
+                s.w[j] = acc[j];
+                seen(j, s.w[j]);
+            }
         }
     }
+    for (int i = held + tid; i < n; i += EV_THREADS) seen(i, acc[i]);
     __syncthreads();
-    auto weight_at = [&](int i) { return i < held ? s.w[i] : acc[lo + i]; };
-    // protected entries rank above every weight: order_key of a number is below ~0u
-    auto key_at = [&](int i) {
-        const int64_t g = lo + i;
-        return g < p.sink || g >= len - p.recent ? ~0u : order_key(weight_at(i));
-    };
 
-    // the key of the last kept entry and how many entries with that key are kept
+    // thr: entries of larger keys are kept, and the first `need` of its own
     uint32_t thr = 0, need = 0;
     const bool all = n_keep >= len;
     if (!all) {
-        uint32_t want = (uint32_t)n_keep;
-        const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-        for (int pass = 0; pass < 3; ++pass) {
-            const int nb = 1 << bits[pass];
+        uint32_t want = (uint32_t)(n_keep - p.sink - p.recent);  // unprotected ones (len > budget: all protected fit)
+        low = __reduce_min_sync(~0u, low);
+        high = __reduce_max_sync(~0u, high);
+        if (lane == 0) {
+            s.scan[warp] = low;
+            s.scan2[warp] = high;
+        }
+        __syncthreads();
+        low = __reduce_min_sync(~0u, s.scan[lane]);
+        high = __reduce_max_sync(~0u, s.scan2[lane]);
+        if (csize > 1) {
+            if (tid == 0) {
+                s.low = low;
+                s.high = high;
+            }
+            cluster_sync();
+            if (lane < csize) {
+                low = dsmem_load(&s.low, lane);
+                high = dsmem_load(&s.high, lane);
+            }
+            low = __reduce_min_sync(~0u, low);
+            high = __reduce_max_sync(~0u, high);
+        }
+        // passes over the range [base, base + width]: 2048 bins of 2^shift keys
+        uint32_t base = low, width = high - low;
+        thr = ~0u - 1u;  // where no unprotected entry is wanted
+        while (want > 0) {
+            const int top = 32 - __clz(width), shift = top > 11 ? top - 11 : 0;
             for (int i = tid; i < EV_BINS; i += EV_THREADS) s.hist[i] = 0;
             __syncthreads();
-            const uint32_t mask = pass == 0 ? 0u : ~0u << (shifts[pass] + bits[pass]);
-            for (int i = tid; i < n; i += EV_THREADS) {
-                const uint32_t k = key_at(i);
-                if ((k & mask) == (thr & mask)) atomicAdd(&s.hist[(k >> shifts[pass]) & (nb - 1)], 1u);
+            auto count = [&](int i, float w) {
+                const uint32_t k = key_of(i, w);
+                if (k != ~0u && k - base <= width) atomicAdd(&s.hist[(k - base) >> shift], 1u);
+            };
+            for (int i = 4 * tid; i < held; i += 4 * EV_THREADS) {
+                if (i + 4 <= held) {
+                    const float4 v = *reinterpret_cast<const float4*>(&s.w[i]);
+                    count(i, v.x);
+                    count(i + 1, v.y);
+                    count(i + 2, v.z);
+                    count(i + 3, v.w);
+                } else {
+                    for (int j = i; j < held; ++j) count(j, s.w[j]);
+                }
             }
+            for (int i = held + tid; i < n; i += EV_THREADS) count(i, acc[i]);
             if (csize > 1) cluster_sync();
             else __syncthreads();
-            // whole-row counts; thread t takes bins nb - 1 - 2t and the one below (from the top)
+            // whole-row counts; thread t takes bins 2047 - 2t and the one below (from the top)
             uint32_t c[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int bin = nb - 1 - (2 * tid + j);
-                if (bin < 0) continue;
-                if (csize == 1) c[j] = s.hist[bin];
-                else
-                    for (int r = 0; r < csize; ++r) c[j] += dsmem_load(&s.hist[bin], r);
-            }
-            uint32_t incl = c[0] + c[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t up = __shfl_up_sync(~0u, incl, o);
-                if (lane >= o) incl += up;
-            }
-            if (lane == 31) s.scan[warp] = incl;
-            __syncthreads();
-            if (warp == 0) {
-                uint32_t v = s.scan[lane];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t up = __shfl_up_sync(~0u, v, o);
-                    if (lane >= o) v += up;
+            if (csize == 1) {
+                c[0] = s.hist[EV_BINS - 1 - 2 * tid];
+                c[1] = s.hist[EV_BINS - 2 - 2 * tid];
+            } else {
+                for (int r = 0; r < csize; ++r) {
+                    c[0] += dsmem_load(&s.hist[EV_BINS - 1 - 2 * tid], r);
+                    c[1] += dsmem_load(&s.hist[EV_BINS - 2 - 2 * tid], r);
                 }
-                s.scan[lane] = v;
             }
-            __syncthreads();
-            uint32_t above = incl - c[0] - c[1] + (warp ? s.scan[warp - 1] : 0u);
+            uint32_t above = block_before(s.scan, c[0] + c[1]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (above < want && above + c[j] >= want) {
-                    s.digit = nb - 1 - (2 * tid + j);
+                    s.digit = EV_BINS - 1 - (2 * tid + j);
                     s.above = above;
+                    s.count = c[j];
                 }
                 above += c[j];
             }
             if (csize > 1) cluster_sync();  // also: every slice's histogram has been read
             else __syncthreads();
-            thr |= s.digit << shifts[pass];
+            base += s.digit << shift;
+            width = (1u << shift) - 1u;
             want -= s.above;
+            if (shift == 0) {  // one key
+                thr = base;
+                need = want;
+                break;
+            }
+            if (s.count == want && base > 0) {  // the whole bin
+                thr = base - 1u;
+                break;
+            }
         }
-        need = want;
     }
 
-    // counts of this slice, by warp: each warp owns a run of whole turns of 32
-    const int turns = (n + 31) / 32, wt = (turns + EV_THREADS / 32 - 1) / (EV_THREADS / 32);
-    const int i0 = warp * wt * 32, i1 = min(n, i0 + wt * 32);
+    // a run of entries a thread, an odd number (so that the threads' reads spread over the banks):
+    // counted, then written behind the runs before it
+    const int run = (n + EV_THREADS - 1) / EV_THREADS | 1;
+    const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
     uint32_t gt = 0, eq = 0;
-    for (int i = i0; i < i1; i += 32) {
-        const bool live = i + lane < n;
-        const uint32_t k = live ? key_at(i + lane) : 0u;
-        gt += __popc(__ballot_sync(~0u, live && (all || k > thr)));
-        eq += __popc(__ballot_sync(~0u, live && !all && k == thr));
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key_of(i, weight_at(i));
+        gt += all || k > thr;
+        eq += !all && k == thr;
     }
-    if (lane == 0) {
-        s.warp_gt[warp] = gt;
-        s.warp_eq[warp] = eq;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, e = 0;
-        for (int i = 0; i < EV_THREADS / 32; ++i) {
-            const uint32_t tg = s.warp_gt[i], te = s.warp_eq[i];
-            s.warp_gt[i] = g;
-            s.warp_eq[i] = e;
-            g += tg;
-            e += te;
-        }
-        s.gt = g;
-        s.eq = e;
-    }
-    uint32_t g0 = 0, e0 = 0;
+    uint32_t g0 = block_before(s.scan, gt), e0 = block_before(s.scan2, eq);
     if (csize > 1) {
-        cluster_sync();
-        for (int r = 0; r < rank; ++r) {
-            g0 += dsmem_load(&s.gt, r);
-            e0 += dsmem_load(&s.eq, r);
+        if (tid == EV_THREADS - 1) {
+            s.low = g0 + gt;
+            s.high = e0 + eq;
         }
+        cluster_sync();
+        uint32_t gr = lane < rank ? dsmem_load(&s.low, lane) : 0u, er = lane < rank ? dsmem_load(&s.high, lane) : 0u;
+        g0 += __reduce_add_sync(~0u, gr);
+        e0 += __reduce_add_sync(~0u, er);
         cluster_sync();  // nobody leaves while its counts are read; every weight has been read
     } else {
         __syncthreads();
     }
-    g0 += s.warp_gt[warp];
-    e0 += s.warp_eq[warp];
-    for (int i = i0; i < i1; i += 32) {
-        const bool live = i + lane < n;
-        const uint32_t k = live ? key_at(i + lane) : 0u;
-        const uint32_t bg = __ballot_sync(~0u, live && (all || k > thr));
-        const uint32_t be = __ballot_sync(~0u, live && !all && k == thr);
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t er = e0 + __popc(be & below), gr = g0 + __popc(bg & below);
-        const bool is_g = bg >> lane & 1, is_e = (be >> lane & 1) && er < need;
-        if (is_g || is_e) {
-            const uint32_t at = gr + (er < need ? er : need);
-            keep[at] = (int32_t)(lo + i + lane);
-            if (out) out[at] = weight_at(i + lane);
+    for (int i = i0; i < i1; ++i) {
+        const float w = weight_at(i);
+        const uint32_t k = key_of(i, w);
+        const bool is_g = all || k > thr, is_e = !all && k == thr;
+        if (is_g || (is_e && e0 < need)) {
+            const uint32_t at = g0 + min(e0, need);
+            keep[at] = (int32_t)(lo + i);
+            if (out) out[at] = w;
         }
-        g0 += __popc(bg);
-        e0 += __popc(be);
+        g0 += is_g;
+        e0 += is_e;
     }
     // padding: -1 indices, zero weights
     const int64_t pad0 = n_keep + (int64_t)rank * EV_THREADS + tid, pads = (int64_t)csize * EV_THREADS;
@@ -249,24 +291,24 @@ struct CompactParams {
     int budget;
     const int32_t* dst;      // [B][ld_dst] pages of the places
     int64_t ld_dst;
+    int in_place;
 };
 
 constexpr int CP_THREADS = 256;
-constexpr int CP_ROWS = CP_THREADS / 4;  // entries of a round: four threads copy 64 bytes of each
-constexpr int CP_ROUNDS = 8;             // rounds in flight
+constexpr int CP_ROUNDS = 8;  // entries a thread has in flight
 
-__global__ void __launch_bounds__(CP_THREADS) paged_compact_kernel(CompactParams p) {
+// Blocks of a (sequence, KV head, K or V): `csize` (in place, as a cluster) or
+// gridDim.x / (2 B H) (to other pages) share its places, CP_ROUNDS times the
+// entries that 16-byte loads of CP_THREADS threads cover at a time.
+__global__ void __launch_bounds__(CP_THREADS) paged_compact_kernel(CompactParams p, int split, int csize) {
     griddep_wait();
     griddep_launch_dependents();
-    const int slices = p.kv.D * 2 / 64;
-    int id = blockIdx.x;
-    const int slice = id % slices;
-    id /= slices;
-    const int kind = id & 1;
-    id >>= 1;
-    const int h = id % p.kv.H, b = id / p.kv.H;
+    const int lanes = p.kv.D / 8, rows = CP_THREADS / lanes;  // threads of an entry, entries of a round
+    const int part = blockIdx.x % split, id = blockIdx.x / split;
+    const int kind = id & 1, h = (id >> 1) % p.kv.H, b = (id >> 1) / p.kv.H;
+    const int row = threadIdx.x / lanes;
     uint8_t* const base = static_cast<uint8_t*>(kind ? p.kv.v : p.kv.k) +
-                          ((int64_t)h * p.kv.head_stride * 2 + slice * 64 + (threadIdx.x & 3) * 16);
+                          ((int64_t)h * p.kv.head_stride * 2 + (threadIdx.x % lanes) * 16);
     const int32_t* keep = p.keep + ((int64_t)b * p.kv.H + h) * p.ld_keep;
     int n = __ldg(p.new_len + b);
     const int32_t len = paged_len(p.kv, b);
@@ -275,19 +317,19 @@ __global__ void __launch_bounds__(CP_THREADS) paged_compact_kernel(CompactParams
         n = n < 0 ? 0 : p.budget;
     }
     const int mask = (1 << p.kv.page_shift) - 1;
-    const int step = CP_ROWS * CP_ROUNDS;
-    for (int i0 = blockIdx.y * step; i0 < n; i0 += gridDim.y * step) {
+    const int step = rows * CP_ROUNDS * split;
+    for (int i0 = 0; i0 < n; i0 += step) {  // the same turns in every block of a cluster
         uint4 v[CP_ROUNDS];
         uint8_t* to[CP_ROUNDS];
         int src[CP_ROUNDS];
 #pragma unroll
         for (int u = 0; u < CP_ROUNDS; ++u) {
-            const int i = i0 + u * CP_ROWS + (threadIdx.x >> 2);
+            const int i = i0 + (part * CP_ROUNDS + u) * rows + row;
             src[u] = i < n ? __ldg(keep + i) : -2;
         }
 #pragma unroll
         for (int u = 0; u < CP_ROUNDS; ++u) {
-            const int i = i0 + u * CP_ROWS + (threadIdx.x >> 2);
+            const int i = i0 + (part * CP_ROUNDS + u) * rows + row;
             to[u] = nullptr;
             if (src[u] == -2) continue;
             if (src[u] < 0 || src[u] >= len) {
@@ -303,7 +345,10 @@ __global__ void __launch_bounds__(CP_THREADS) paged_compact_kernel(CompactParams
             v[u] = *reinterpret_cast<const uint4*>(base + 2 * (a * p.kv.page_stride + (src[u] & mask) * p.kv.token_stride));
             to[u] = base + 2 * (d * p.kv.page_stride + (i & mask) * p.kv.token_stride);
         }
-        __syncthreads();  // the rounds' reads precede their writes
+        if (p.in_place) {  // a turn's reads precede its writes
+            if (csize > 1) cluster_sync();
+            else __syncthreads();
+        }
 #pragma unroll
         for (int u = 0; u < CP_ROUNDS; ++u)
             if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];

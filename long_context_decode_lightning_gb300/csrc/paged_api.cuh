@@ -469,7 +469,11 @@ hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_
         return HSI_ERR_INVALID_ARG;
     if (acc_out && ld_out < budget) return HSI_ERR_INVALID_ARG;
     int csize = 1;
-    while (csize < EV_MAX_CLUSTER && (max_len + csize - 1) / csize > 8192) csize *= 2;
+    // slices of at most 8192 entries a CTA, and down to 2048 where the rows leave SMs idle
+    const int64_t rows = (int64_t)B * heads, sms = sm_count();
+    while (csize < EV_MAX_CLUSTER &&
+           ((max_len + csize - 1) / csize > 8192 || (max_len > 2048 * csize && 2 * csize * rows <= sms)))
+        csize *= 2;
     // past the clusters' shared memory, weights are read while others are written
     if (acc_out == acc && (max_len + csize - 1) / csize + 31 > EV_CAP) return HSI_ERR_UNSUPPORTED;
     if ((int64_t)B * heads * csize > INT32_MAX) return HSI_ERR_UNSUPPORTED;
@@ -509,17 +513,17 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     p.budget = budget;
     p.dst = dst_table;
     p.ld_dst = ld_dst;
-    const int64_t rows = (int64_t)cache->B * cache->heads * 2 * (cache->dim * 2 / 64);
-    if (rows > INT32_MAX) return HSI_ERR_UNSUPPORTED;
-    // to other pages, the places are spread until every SM has four blocks
+    p.in_place = dst_table == cache->table;
+    // blocks of a (sequence, KV head, K or V): until every SM has eight, none without a turn's entries
+    const int64_t rows = (int64_t)cache->B * cache->heads * 2, want = 8 * (int64_t)sm_count();
+    const int64_t turn = (int64_t)CP_THREADS / (cache->dim / 8) * CP_ROUNDS, most = (budget + turn - 1) / turn;
+    if (want <= 0) return HSI_ERR_CUDA;
     int64_t split = 1;
-    if (dst_table != cache->table) {
-        const int64_t steps = (budget + CP_ROWS * CP_ROUNDS - 1) / (CP_ROWS * CP_ROUNDS);
-        split = (4 * (int64_t)sm_count() + rows - 1) / rows;
-        if (split > steps) split = steps;
-        if (split < 1) split = 1;
-    }
-    return launch(paged_compact_kernel, dim3((unsigned)rows, (unsigned)split), dim3(CP_THREADS), 0, stream, p);
+    while (split * rows < want && 2 * split <= most && (!p.in_place || split < EV_MAX_CLUSTER)) split *= 2;
+    if (rows * split > INT32_MAX) return HSI_ERR_UNSUPPORTED;
+    const int csize = p.in_place ? (int)split : 1;
+    return launch_cluster(paged_compact_kernel, dim3((unsigned)(rows * split)), dim3(CP_THREADS), 0, csize, stream, p,
+                          (int)split, csize);
 }
 
 }  // extern "C"
