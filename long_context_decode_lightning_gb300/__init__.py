@@ -153,6 +153,14 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _raw_stream(stream=None) -> int:
+    """The current stream's handle without the stream object that torch.cuda.current_stream makes (a microsecond
+    of every call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _check(fn: str, st: int):
     if st != 0:
         raise HsiError(fn, st)
@@ -390,33 +398,76 @@ def reindex_layer(q_rec, g_q, w, k_rec, g_k, k_rec_off, n_visible, block_ids, n_
         _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+# The checks below run on every call of a decode step, so their messages are built only when they fail.
+
+def _bad(what: str):
+    raise ValueError(what)
 
 
 def _dtype(t: torch.Tensor) -> int:
-    _need(t.dtype in _DTYPES, f"unsupported dtype {t.dtype}")
-    return _DTYPES[t.dtype]
+    d = _DTYPES.get(t.dtype)
+    return _bad(f"unsupported dtype {t.dtype}") if d is None else d
 
 
-def _i32(t: torch.Tensor, name: str, dim: int) -> torch.Tensor:
-    _need(t.dtype == torch.int32 and t.dim() == dim and t.stride(-1) == 1, f"{name}: int32, {dim}-d, contiguous rows")
-    return t
+def _i32(t: torch.Tensor, name: str, n: int) -> int:
+    """The address of a contiguous int32 vector of n values."""
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        _bad(f"{name}: int32 [{n}], contiguous")
+    return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
-    """A [tokens, heads, dims] tensor with contiguous dims."""
-    _need(t.dim() == 3 and t.dtype == dtype and t.stride(2) == 1, f"{name}: [tokens, heads, dims] of {dtype}, dims contiguous")
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+def _table(t: torch.Tensor, name: str, B: int) -> int:
+    """The row stride of an int32 [B, pages] tensor with contiguous rows."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1:
+        _bad(f"{name}: int32 [{B}, pages], rows contiguous")
+    return t.stride(0) if B > 1 else t.shape[1]
+
+
+def _heads(t: torch.Tensor, name: str, shape, dtype):
+    """Address, token stride and head stride of a [tokens, heads, dims] tensor with contiguous dims."""
+    if t.shape != shape or t.dtype is not dtype:
+        _bad(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        _bad(f"{name}: dims must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _steps(t: torch.Tensor) -> int:
+    if t.dtype is not torch.int64 or t.dim() != 1 or not t.is_contiguous():
+        _bad("steps: int64 [pairs], contiguous")
+    return t.data_ptr()
+
+
+def _lse(t: torch.Tensor, shape) -> int:
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+        _bad(f"lse: fp32 {tuple(shape)}, contiguous")
+    return t.data_ptr()
+
+
+def _acc(t: torch.Tensor, name: str, B: int, H: int):
+    """Address and row stride of fp32 [B, H, entries] with evenly spaced rows."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != H or st[2] != 1:
+        _bad(f"{name}: fp32 [{B}, {H}, entries]")
+    ld = st[1] if H > 1 else (st[0] if B > 1 else shape[2])
+    if B > 1 and st[0] != H * ld:
+        _bad(f"{name}: rows must be evenly spaced")
+    return t.data_ptr(), ld
+
+
+def _keep(t: torch.Tensor, B: int, H: int) -> int:
+    if t.dtype is not torch.int32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != H or not t.is_contiguous():
+        _bad(f"keep: int32 [{B}, {H}, places], contiguous")
+    return t.data_ptr()
 
 
 def rope_steps(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
                beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda") -> tuple[torch.Tensor, float]:
     """The rotation of rot / 2 pairs: (steps int64 [rot / 2] on the device, in 2^-64 turns a position, gain)."""
     steps, gain = torch.empty(max(rot, 2) // 2, dtype=torch.int64), ctypes.c_float()
-    _need(scaling in ROPE_SCALING, f"unknown scaling {scaling!r}")
+    if scaling not in ROPE_SCALING:
+        _bad(f"unknown scaling {scaling!r}")
     _check("hsi_rope_steps", lib().hsi_rope_steps(rot, base, ROPE_SCALING[scaling], factor, original_len, beta_fast,
                                                   beta_slow, _ptr(steps), ctypes.byref(gain)))
     return steps.to(device), gain.value
@@ -425,14 +476,15 @@ def rope_steps(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
 def rope(x, positions, steps, out, rot_offset: int = 0, interleaved: bool = False, gain: float = 1.0,
          inverse: bool = False, stream=None):
     """x [T, H, D] (bf16, fp16 or fp32) rotated into out (may be x) at positions int32 [T]; inverse: the gradient."""
-    _heads(x, "x", x.shape, x.dtype)
-    _heads(out, "out", x.shape, x.dtype)
-    _need(_i32(positions, "positions", 1).numel() == x.shape[0], "positions: one a token")
-    _need(steps.dtype == torch.int64 and steps.is_contiguous(), "steps: int64, contiguous")
-    T, H, D = x.shape
+    shape = x.shape
+    if len(shape) != 3:
+        _bad("x: [tokens, heads, dims]")
+    T, H, D = shape
+    xp, xt, xh = _heads(x, "x", shape, x.dtype)
+    yp, yt, yh = _heads(out, "out", shape, x.dtype)
     _check("hsi_rope", lib().hsi_rope(
-        _ptr(x), x.stride(0), x.stride(1), _dtype(x), T, H, D, _ptr(positions), _ptr(steps), 2 * steps.numel(),
-        rot_offset, int(interleaved), gain, int(inverse), _ptr(out), out.stride(0), out.stride(1), _stream(stream)))
+        xp, xt, xh, _dtype(x), T, H, D, _i32(positions, "positions", T), _steps(steps), 2 * steps.shape[0], rot_offset,
+        interleaved, gain, inverse, yp, yt, yh, _raw_stream(stream)))
 
 
 class PagedKV:
@@ -441,41 +493,36 @@ class PagedKV:
     [B, pages a sequence], kv_len int32 [B] on the device. Keeps the tensors; their contents may change."""
 
     def __init__(self, k, v, table, kv_len):
-        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride(3) == 1 and v.stride() == k.stride(),
-              "k, v: [pages, page size, heads, dim], the same strides, dims contiguous")
-        _i32(table, "table", 2)
-        _need(_i32(kv_len, "kv_len", 1).numel() == table.shape[0], "kv_len: one a sequence")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride() != k.stride():
+            _bad("k, v: [pages, page size, heads, dim], the same strides, dims contiguous")
+        if table.dim() != 2:
+            _bad("table: int32 [sequences, pages]")
         self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
         self.B, self.heads, self.dim, self.page_size = table.shape[0], k.shape[2], k.shape[3], k.shape[1]
+        self.dtype = k.dtype
         self.c = _PagedKV(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[0], _ptr(table),
-                          table.stride(0) if table.shape[0] > 1 else table.shape[1], _ptr(kv_len), self.B, self.heads,
-                          self.dim, self.page_size, _dtype(k))
+                          _table(table, "table", self.B), _i32(kv_len, "kv_len", self.B), self.B, self.heads, self.dim,
+                          self.page_size, _dtype(k))
         self.ref = ctypes.byref(self.c)
-
-
-def _q_start(q_start, kv):
-    _need(_i32(q_start, "q_start", 1).numel() == kv.B + 1, "q_start: one a sequence and the end")
-    return _ptr(q_start)
 
 
 def paged_append(kv: PagedKV, k_new, v_new, q_start, max_q=None, positions=None, steps=None, rot_offset: int = 0,
                  interleaved: bool = False, gain: float = 1.0, q=None, q_out=None, stream=None):
     """k_new, v_new [T, heads, dim] into the cache's last entries of each sequence; with steps, k (and q [T,
     q heads, dim] into q_out) rotated at positions int32 [T] in the same launch. max_q is not needed here."""
-    T = k_new.shape[0]
-    _heads(k_new, "k_new", (T, kv.heads, kv.dim), kv.k.dtype)
-    _heads(v_new, "v_new", (T, kv.heads, kv.dim), kv.k.dtype)
-    _need(positions is None or _i32(positions, "positions", 1).numel() == T, "positions: one a token")
-    _need(steps is None or (steps.dtype == torch.int64 and steps.is_contiguous()), "steps: int64, contiguous")
+    T, dt = k_new.shape[0], kv.dtype
+    kp, kt, kh = _heads(k_new, "k_new", (T, kv.heads, kv.dim), dt)
+    vp, vt, vh = _heads(v_new, "v_new", (T, kv.heads, kv.dim), dt)
+    pos = None if positions is None else _i32(positions, "positions", T)
+    st, rot = (None, 0) if steps is None else (_steps(steps), 2 * steps.shape[0])
+    qp, qt, qh, op, ot, oh, Hq = None, 0, 0, None, 0, 0, 0
     if q is not None:
-        _heads(q, "q", (T, q.shape[1], kv.dim), kv.k.dtype)
-        _heads(q_out, "q_out", q.shape, kv.k.dtype)
+        Hq = q.shape[1]
+        qp, qt, qh = _heads(q, "q", (T, Hq, kv.dim), dt)
+        op, ot, oh = _heads(q_out, "q_out", (T, Hq, kv.dim), dt)
     _check("hsi_paged_append", lib().hsi_paged_append(
-        kv.ref, _ptr(k_new), k_new.stride(0), k_new.stride(1), _ptr(v_new), v_new.stride(0), v_new.stride(1),
-        _q_start(q_start, kv), T, _ptr(positions), _ptr(steps), 0 if steps is None else 2 * steps.numel(), rot_offset,
-        int(interleaved), gain, _ptr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
-        0 if q is None else q.shape[1], _ptr(q_out), 0 if q is None else q_out.stride(0),
-        0 if q is None else q_out.stride(1), _stream(stream)))
+        kv.ref, kp, kt, kh, vp, vt, vh, _i32(q_start, "q_start", kv.B + 1), T, pos, st, rot, rot_offset, interleaved,
+        gain, qp, qt, qh, Hq, op, ot, oh, _raw_stream(stream)))
 
 
 def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int) -> torch.Tensor:
@@ -487,59 +534,46 @@ def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int) -> torch.
 def paged_attention(kv: PagedKV, q, q_start, max_q: int, max_kv: int, scale: float, out, lse=None, causal: bool = True,
                     ws=None, stream=None):
     """q [T, q heads, dim] over the cache into out (and lse fp32 [T, q heads])."""
-    _heads(q, "q", (q.shape[0], q.shape[1], kv.dim), kv.k.dtype)
-    _heads(out, "out", q.shape, kv.k.dtype)
-    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == tuple(q.shape[:2])),
-          "lse: fp32 [tokens, q heads], contiguous")
+    T, Hq = q.shape[:2]
+    shape = (T, Hq, kv.dim)
+    qp, qt, qh = _heads(q, "q", shape, kv.dtype)
+    op, ot, oh = _heads(out, "out", shape, kv.dtype)
     if ws is None:
         ws = paged_attention_workspace(kv, q, max_q, max_kv)
     _check("hsi_paged_attention", lib().hsi_paged_attention(
-        kv.ref, _ptr(q), q.stride(0), q.stride(1), q.shape[1], _q_start(q_start, kv), q.shape[0], max_q, max_kv, scale,
-        int(causal), _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
-
-
-def _acc(t, name, kv_shape):
-    _need(t.dtype == torch.float32 and t.dim() == 3 and t.stride(2) == 1 and tuple(t.shape[:2]) == tuple(kv_shape),
-          f"{name}: fp32 [sequences, KV heads, entries]")
-    ld = t.stride(1) if t.shape[1] > 1 else (t.stride(0) if t.shape[0] > 1 else t.shape[2])
-    _need(t.shape[0] == 1 or t.stride(0) == t.shape[1] * ld, f"{name}: rows evenly spaced")
-    return ld
+        kv.ref, qp, qt, qh, Hq, _i32(q_start, "q_start", kv.B + 1), T, max_q, max_kv, scale, causal, op, ot, oh,
+        None if lse is None else _lse(lse, (T, Hq)), ws.data_ptr(), ws.numel(), _raw_stream(stream)))
 
 
 def attention_weights(kv: PagedKV, q, lse, q_start, max_q: int, max_kv: int, scale: float, acc_in, acc_out,
                       decay: float = 1.0, causal: bool = True, stream=None):
     """acc_out [B, heads, entries] = decay * acc_in + the attention weight of every entry, summed over the rows of
     its KV head. acc_in None: zeros; it may be acc_out."""
-    _heads(q, "q", (q.shape[0], q.shape[1], kv.dim), kv.k.dtype)
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == tuple(q.shape[:2]),
-          "lse: fp32 [tokens, q heads], contiguous")
-    shape = (kv.B, kv.heads)
+    T, Hq = q.shape[:2]
+    qp, qt, qh = _heads(q, "q", (T, Hq, kv.dim), kv.dtype)
+    ip, il = (None, 0) if acc_in is None else _acc(acc_in, "acc_in", kv.B, kv.heads)
+    op, ol = _acc(acc_out, "acc_out", kv.B, kv.heads)
     _check("hsi_attention_weights", lib().hsi_attention_weights(
-        kv.ref, _ptr(q), q.stride(0), q.stride(1), q.shape[1], _ptr(lse), _q_start(q_start, kv), q.shape[0], max_q,
-        max_kv, scale, int(causal), decay, _ptr(acc_in), 0 if acc_in is None else _acc(acc_in, "acc_in", shape),
-        _ptr(acc_out), _acc(acc_out, "acc_out", shape), _stream(stream)))
+        kv.ref, qp, qt, qh, Hq, _lse(lse, (T, Hq)), _i32(q_start, "q_start", kv.B + 1), T, max_q, max_kv, scale, causal,
+        decay, ip, il, op, ol, _raw_stream(stream)))
 
 
 def evict_select(acc, kv_len, max_len: int, budget: int, keep, new_len, sink: int = 0, recent: int = 0, acc_out=None,
                  stream=None):
     """The entries a budget keeps, per sequence and KV head: keep int32 [B, heads, >= budget], new_len int32 [B]."""
-    B, H = acc.shape[0], acc.shape[1]
-    ld = _acc(acc, "acc", (B, H))
-    _need(keep.dtype == torch.int32 and keep.is_contiguous() and keep.shape[:2] == acc.shape[:2],
-          "keep: int32 [sequences, KV heads, places], contiguous")
-    _need(_i32(kv_len, "kv_len", 1).numel() == B and _i32(new_len, "new_len", 1).numel() == B, "lengths: one a sequence")
+    B, H = acc.shape[:2]
+    ap, al = _acc(acc, "acc", B, H)
+    op, ol = (None, 0) if acc_out is None else _acc(acc_out, "acc_out", B, H)
     _check("hsi_evict_select", lib().hsi_evict_select(
-        _ptr(acc), ld, _ptr(kv_len), B, H, max_len, budget, sink, recent, _ptr(keep), keep.shape[2], _ptr(new_len),
-        _ptr(acc_out), 0 if acc_out is None else _acc(acc_out, "acc_out", (B, H)), _stream(stream)))
+        ap, al, _i32(kv_len, "kv_len", B), B, H, max_len, budget, sink, recent, _keep(keep, B, H), keep.shape[2],
+        _i32(new_len, "new_len", B), op, ol, _raw_stream(stream)))
 
 
 def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, stream=None):
     """Entry keep[b, g, i] of KV head g becomes entry i of dst_table int32 [B, pages] (None: in place).
     budget: bound of new_len (keep's width by default)."""
-    dst = kv.table if dst_table is None else _i32(dst_table, "dst_table", 2)
-    _need(keep.dtype == torch.int32 and keep.is_contiguous() and tuple(keep.shape[:2]) == (kv.B, kv.heads),
-          "keep: int32 [sequences, KV heads, places], contiguous")
-    _need(dst.shape[0] == kv.B and _i32(new_len, "new_len", 1).numel() == kv.B, "a row of dst_table and a length a sequence")
+    dst = kv.table if dst_table is None else dst_table
+    kp, places = _keep(keep, kv.B, kv.heads), keep.shape[2]
     _check("hsi_paged_compact", lib().hsi_paged_compact(
-        kv.ref, _ptr(keep), keep.shape[2], _ptr(new_len), keep.shape[2] if budget is None else budget, _ptr(dst),
-        dst.stride(0) if kv.B > 1 else dst.shape[1], _stream(stream)))
+        kv.ref, kp, places, _i32(new_len, "new_len", kv.B), places if budget is None else budget, dst.data_ptr(),
+        _table(dst, "dst_table", kv.B), _raw_stream(stream)))

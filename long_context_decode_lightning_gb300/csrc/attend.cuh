@@ -186,49 +186,42 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     griddep_wait();
     griddep_launch_dependents();
 
-    // the line: total tiles, then the sequence that holds this run's first tile
+    // the line: total tiles, then the sequence that holds this run's first tile (up to 32
+    // sequences, a lane each, are looked at once)
     if (warp == 0) {
-        int64_t total = 0;
-        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+        auto tiles_of = [&](int b) {
+            if (b >= p.kv.B) return (int64_t)0;
             LineWalk w;
-            w.b = b0 + lane;
-            int64_t n = 0;
-            if (w.b < p.kv.B) {
-                walk_load<WEIGHTS>(p, w);
-                n = walk_tiles(w);
-            }
+            w.b = b;
+            walk_load<WEIGHTS>(p, w);
+            return walk_tiles(w);
+        };
+        auto upto = [&](int64_t n) {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t up = __shfl_up_sync(~0u, n, o);
                 if (lane >= o) n += up;
             }
-            if (!WEIGHTS && blockIdx.x == 0 && w.b < p.kv.B) p.base[w.b + 1] = total + n;
-            total += __shfl_sync(~0u, n, 31);
+            return n;
+        };
+        int64_t total = 0, n = 0;
+        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+            n = tiles_of(b0 + lane);
+            const int64_t sum = upto(n);
+            if (!WEIGHTS && blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + sum;
+            total += __shfl_sync(~0u, sum, 31);
         }
         if (!WEIGHTS && blockIdx.x == 0 && lane == 0) p.base[0] = 0;
         const int64_t lo = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
         int64_t before = 0;
-        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
-            LineWalk w;
-            w.b = b0 + lane;
-            int64_t n = 0;
-            if (w.b < p.kv.B) {
-                walk_load<WEIGHTS>(p, w);
-                n = walk_tiles(w);
-            }
-            int64_t upto = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(~0u, upto, o);
-                if (lane >= o) upto += up;
-            }
-            const int64_t f = before + upto - n;
+        for (int b0 = 0; b0 < p.kv.B && before <= lo; b0 += 32) {
+            if (p.kv.B > 32) n = tiles_of(b0 + lane);
+            const int64_t sum = upto(n), f = before + sum - n;
             if (n && lo >= f && lo < f + n) {
-                s_b = w.b;
+                s_b = b0 + lane;
                 s_first = f;
             }
-            before += __shfl_sync(~0u, upto, 31);
-            if (before > lo) break;
+            before += __shfl_sync(~0u, sum, 31);
         }
         if (lane == 0) s_total = total;
     }

@@ -83,16 +83,21 @@ hsi_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, 
     return e == cudaSuccess ? HSI_OK : HSI_ERR_CUDA;
 }
 
+constexpr int kMaxDevices = 64;
+
+// Multiprocessors of the current device, asked for once per device.
 int sm_count() {
+    static std::atomic<int> known[kMaxDevices];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool slot = dev >= 0 && dev < kMaxDevices;
+    if (slot && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (slot) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-constexpr int kMaxDevices = 64;
 
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device, once per device: the attribute is a property of the kernel on one
