@@ -8,6 +8,8 @@
 //    entries, form one line of tiles that is cut into equal runs, one per CTA, two CTAs
 //    an SM. Long and short sequences mix freely and no SM waits for another; a
 //    unit that spans CTAs is joined from their partial sums by a second kernel.
+//    Short sequences go without the line and the second kernel: a cluster a unit,
+//    its tiles in equal parts, joined through distributed shared memory.
 //  - A producer warp fetches tiles with one TMA box per page (or 64 entries of
 //    it) into a ring of shared-memory stages, a lane per box.
 //  - Each of four warps owns 16 entries of a tile: S = Q K^T by mma.sync
@@ -31,6 +33,7 @@ namespace hsi {
 
 constexpr int AT_ROWS = 16;      // rows of a unit
 constexpr int AT_KT = 64;        // entries of a tile
+constexpr int AT_CLUSTER = 8;    // most blocks of a short unit
 constexpr int AT_WARPS = 4;      // consumer warps, 16 entries of a tile each
 constexpr int AT_THREADS = 32 * (AT_WARPS + 1);
 
@@ -56,6 +59,22 @@ struct AttendParams {
     int64_t ld_acc_in, ld_acc_out;
     float decay;
 };
+
+// A value of rank c's part (this block's own where there is no cluster).
+__device__ __forceinline__ float cluster_load(const float* mine, int c, int csize) {
+    return csize > 1 ? __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(mine), c)) : *mine;
+}
+__device__ __forceinline__ float4 cluster_load4(const float* mine, int c, int csize) {
+    if (csize <= 1) return *reinterpret_cast<const float4*>(mine);
+    uint32_t addr;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(c));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 
 template <int D>
 __host__ __device__ constexpr int attend_slot_floats(int rows) { return rows * (D + 2); }
@@ -162,7 +181,7 @@ __device__ __forceinline__ int64_t walk_tiles(const LineWalk& w) { return (int64
 template <typename T, int D, bool WEIGHTS>
 __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     attend_token_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap) {
+                        const __grid_constant__ CUtensorMap vmap, int csize) {
     using C = AttendCfg<D, WEIGHTS>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
@@ -186,55 +205,76 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     griddep_wait();
     griddep_launch_dependents();
 
-    // the line: total tiles, then the sequence that holds this run's first tile (up to 32
-    // sequences, a lane each, are looked at once)
-    if (warp == 0) {
-        auto tiles_of = [&](int b) {
-            if (b >= p.kv.B) return (int64_t)0;
-            LineWalk w;
-            w.b = b;
-            walk_load<WEIGHTS>(p, w);
-            return walk_tiles(w);
-        };
-        auto upto = [&](int64_t n) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(~0u, n, o);
-                if (lane >= o) n += up;
-            }
-            return n;
-        };
-        int64_t total = 0, n = 0;
-        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
-            n = tiles_of(b0 + lane);
-            const int64_t sum = upto(n);
-            if (!WEIGHTS && blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + sum;
-            total += __shfl_sync(~0u, sum, 31);
-        }
-        if (!WEIGHTS && blockIdx.x == 0 && lane == 0) p.base[0] = 0;
-        const int64_t lo = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.kv.B && before <= lo; b0 += 32) {
-            if (p.kv.B > 32) n = tiles_of(b0 + lane);
-            const int64_t sum = upto(n), f = before + sum - n;
-            if (n && lo >= f && lo < f + n) {
-                s_b = b0 + lane;
-                s_first = f;
-            }
-            before += __shfl_sync(~0u, sum, 31);
-        }
-        if (lane == 0) s_total = total;
-    }
-    __syncthreads();
-    const int64_t total = s_total;
-    const int64_t G = min((int64_t)gridDim.x, total);
-    if (blockIdx.x >= G) return;
-    int64_t x = line_cut(total, blockIdx.x, G);
-    const int64_t hi = line_cut(total, blockIdx.x + 1, G);
     LineWalk w;
-    w.b = s_b;
-    w.first = s_first;
-    walk_load<WEIGHTS>(p, w);
+    int64_t x, hi;  // the tiles of this block: of the line, or (short) of its unit
+    if (!WEIGHTS && csize) {
+        // short: a cluster of csize blocks a unit, the unit's tiles in equal parts
+        const int u = blockIdx.x / csize, rank = csize > 1 ? (int)cluster_ctarank() : 0;
+        const int rts = (p.max_q * p.group + AT_ROWS - 1) / AT_ROWS;
+        w.b = u / (rts * p.kv.H);
+        w.first = -(int64_t)(u % (rts * p.kv.H));
+        walk_load<WEIGHTS>(p, w);
+        const int per = (w.nt + csize - 1) / csize;
+        const int t0 = min(w.nt, rank * per), t1 = min(w.nt, t0 + per);
+        const bool there = -w.first < w.units;  // the row tile has rows
+        w.first *= w.nt;
+        x = there ? t0 : 0;
+        hi = there ? t1 : 0;
+        if (x == hi && threadIdx.x < AT_ROWS) {
+            float* slot = reinterpret_cast<float*>(stage0);
+            slot[AT_ROWS * D + threadIdx.x] = -INFINITY;
+            slot[AT_ROWS * (D + 1) + threadIdx.x] = 0.f;
+        }
+        __syncthreads();
+    } else {
+        // the line: total tiles, then the sequence that holds this run's first tile (up to 32
+        // sequences, a lane each, are looked at once)
+        if (warp == 0) {
+            auto tiles_of = [&](int b) {
+                if (b >= p.kv.B) return (int64_t)0;
+                LineWalk w;
+                w.b = b;
+                walk_load<WEIGHTS>(p, w);
+                return walk_tiles(w);
+            };
+            auto upto = [&](int64_t n) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(~0u, n, o);
+                    if (lane >= o) n += up;
+                }
+                return n;
+            };
+            int64_t total = 0, n = 0;
+            for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+                n = tiles_of(b0 + lane);
+                const int64_t sum = upto(n);
+                if (!WEIGHTS && blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + sum;
+                total += __shfl_sync(~0u, sum, 31);
+            }
+            if (!WEIGHTS && blockIdx.x == 0 && lane == 0) p.base[0] = 0;
+            const int64_t lo = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
+            int64_t before = 0;
+            for (int b0 = 0; b0 < p.kv.B && before <= lo; b0 += 32) {
+                if (p.kv.B > 32) n = tiles_of(b0 + lane);
+                const int64_t sum = upto(n), f = before + sum - n;
+                if (n && lo >= f && lo < f + n) {
+                    s_b = b0 + lane;
+                    s_first = f;
+                }
+                before += __shfl_sync(~0u, sum, 31);
+            }
+            if (lane == 0) s_total = total;
+        }
+        __syncthreads();
+        const int64_t total = s_total, G = min((int64_t)gridDim.x, total);
+        if (blockIdx.x >= G) return;
+        x = line_cut(total, blockIdx.x, G);
+        hi = line_cut(total, blockIdx.x + 1, G);
+        w.b = s_b;
+        w.first = s_first;
+        walk_load<WEIGHTS>(p, w);
+    }
     int stage = 0, fills = 0;
     uint32_t phase = 0;
     bool ok = true;  // false once a wait has run out: no more copies or results, but every barrier is kept
@@ -264,10 +304,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                 int page = 0;
                 if (mine) page = paged_page(p.kv, w.b, (e0 + e) >> p.kv.page_shift);
                 ok = wait_bounded(&empty[stage], phase ^ 1, &s_abort);
-                if (!__all_sync(~0u, ok)) {  // let the copies in flight land before the block goes
+                ok = __all_sync(~0u, ok);
+                if (!ok) {  // let the copies in flight land before the block goes
                     for (int k = fills > C::STAGES ? fills - C::STAGES : 0; k < fills; ++k)
                         wait_drain(&full[k % C::STAGES], (k / C::STAGES) & 1);
-                    return;
+                    break;
                 }
                 ++fills;
                 if (fills == 1 && *(volatile int*)&g_hsi_skip_first_copy) goto next;
@@ -285,6 +326,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                     phase ^= 1;
                 }
             }
+            if (!ok) break;
             continue;
         }
 
@@ -476,8 +518,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                 float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
                 f[j] = m2[j] == -INFINITY ? 0.f : ex2(m2[j] - m);
             }
-            const bool whole = tile0 == 0 && n_tiles == w.nt;
-            float* slot = p.part + (int64_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * attend_slot_floats<D>(AT_ROWS);
+            const bool whole = !csize && tile0 == 0 && n_tiles == w.nt;
+            float* slot = csize ? reinterpret_cast<float*>(stage0)  // every tile has been read
+                                : p.part + (int64_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * attend_slot_floats<D>(AT_ROWS);
             // 32 dims at a time: thread -> row tid / 8, dims (tid % 8) * 4 .. + 3
             const int orow = threadIdx.x >> 3, od = (threadIdx.x & 7) * 4;
             const float rm = fmaxf(fmaxf(s_m[0][orow], s_m[1][orow]), fmaxf(s_m[2][orow], s_m[3][orow]));
@@ -525,6 +568,48 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                 }
             }
         }
+    }
+
+    if constexpr (!WEIGHTS) {
+        if (!csize) return;
+        // short: the cluster's parts are joined through distributed shared memory, each block a
+        // share of the outputs
+        if (csize > 1) cluster_sync();
+        else __syncthreads();
+        const int rank = csize > 1 ? (int)cluster_ctarank() : 0;
+        const int rts = (p.max_q * p.group + AT_ROWS - 1) / AT_ROWS, unit = blockIdx.x / csize % (rts * p.kv.H);
+        const int head = unit % p.kv.H, rt = unit / p.kv.H;
+        const float* slot = reinterpret_cast<const float*>(stage0);
+        for (int i = rank * AT_THREADS + threadIdx.x; i < AT_ROWS * (D / 4); i += csize * AT_THREADS) {
+            const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = rt * AT_ROWS + row;
+            if (r >= w.m * p.group) break;
+            float mc[AT_CLUSTER], m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int c = 0; c < AT_CLUSTER; ++c) {
+                mc[c] = -INFINITY;
+                if (c < csize) mc[c] = cluster_load(slot + AT_ROWS * D + row, c, csize);
+                m = fmaxf(m, mc[c]);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < AT_CLUSTER; ++c) {
+                if (mc[c] == -INFINITY) continue;  // a part without tiles has no sums
+                const float f = ex2(mc[c] - m);
+                const float4 v = cluster_load4(slot + row * D + d, c, csize);
+                o.x += f * v.x;
+                o.y += f * v.y;
+                o.z += f * v.z;
+                o.w += f * v.w;
+                l += f * cluster_load(slot + AT_ROWS * (D + 1) + row, c, csize);
+            }
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const int64_t tok = w.at + r / p.group;
+            const int h = head * p.group + r % p.group;
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + d) =
+                make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+            if (d == 0 && p.lse) p.lse[tok * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        }
+        if (csize > 1) cluster_sync();  // nobody leaves while its part is read
     }
 }
 

@@ -57,23 +57,6 @@ struct EvictSmem {
     float w[EV_CAP];               // the slice's weights
 };
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A 32-bit word of another CTA of the cluster, at the address it has in this one.
-__device__ __forceinline__ uint32_t dsmem_load(const uint32_t* mine, uint32_t rank) {
-    uint32_t addr, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // The sum of v over the threads before this one. Whole block; scan: a word a warp.
 __device__ __forceinline__ uint32_t block_before(uint32_t* scan, uint32_t v) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

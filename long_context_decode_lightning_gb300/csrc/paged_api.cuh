@@ -167,16 +167,30 @@ int64_t attend_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int6
 // Workspace of the attention: the line's prefix, then the partial sums' slots.
 size_t attend_base_bytes(int32_t B) { return align_up(((size_t)B + 1) * 8, 256); }
 
+// Blocks of a unit in the short form (0: the line). A unit's tiles go to up to
+// eight blocks, four tiles each at most: past that the line's finer cut is
+// quicker. All units at once, or the line evens them out better.
+int attend_short(const AttendParams& p) {
+    const int64_t rt = ((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS, units = rt * p.kv.H * p.kv.B;
+    const int64_t tiles = (p.max_kv + AT_KT - 1) / AT_KT, room = 2 * (int64_t)sm_count();
+    int csize = 1;
+    while (csize < AT_CLUSTER && 2 * csize <= tiles && 2 * csize * units <= room) csize *= 2;
+    return csize * units <= room && tiles <= 4 * csize ? csize : 0;
+}
+
 template <typename T, int D, bool WEIGHTS>
 hsi_status launch_attend_token(const AttendParams& p, const CUtensorMap& km, const CUtensorMap& vm, int64_t grid,
                                cudaStream_t s) {
     using C = AttendCfg<D, WEIGHTS>;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(attend_token_kernel<T, D, WEIGHTS>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
-    hsi_status st = launch(attend_token_kernel<T, D, WEIGHTS>, dim3((unsigned)grid), dim3(AT_THREADS), C::SMEM_BYTES, s, p,
-                           km, vm);
-    if (st != HSI_OK || WEIGHTS) return st;
     const unsigned rt = (unsigned)(((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS);
+    if (const int csize = WEIGHTS ? 0 : attend_short(p))
+        return launch_cluster(attend_token_kernel<T, D, WEIGHTS>, dim3(rt * p.kv.H * p.kv.B * csize), dim3(AT_THREADS),
+                              C::SMEM_BYTES, csize, s, p, km, vm, csize);
+    const hsi_status st = launch(attend_token_kernel<T, D, WEIGHTS>, dim3((unsigned)grid), dim3(AT_THREADS),
+                                 C::SMEM_BYTES, s, p, km, vm, 0);
+    if (st != HSI_OK || WEIGHTS) return st;
     return launch(attend_join_kernel<T, D>, dim3(rt, p.kv.H, p.kv.B), dim3(128), 0, s, p, (int)grid);
 }
 
