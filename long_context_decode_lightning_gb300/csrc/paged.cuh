@@ -6,12 +6,43 @@
 // coordinate past the tensor), a store is skipped.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <cstdint>
 
 #include "common.cuh"
 
 namespace hsi {
+
+template <typename T>
+constexpr bool is_bf16 = false;
+template <>
+constexpr bool is_bf16<__nv_bfloat16> = true;
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
 
 struct PagedView {
     void *k, *v;
@@ -47,23 +78,18 @@ __device__ __forceinline__ int32_t paged_new(const int32_t* q_start, int b, int3
     return e - a;
 }
 
-// The sequence of new token t: the last b with q_start[b] <= t.
-__device__ __forceinline__ int paged_seq_of(const int32_t* q_start, int B, int64_t t) {
-    int lo = 0, hi = B;  // q_start[lo] <= t < q_start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(q_start + mid) <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Element offset (head 0) of the place of new token t: entry kv_len - (new
 // tokens of its sequence) + its index among them. PAGED_NO_TOKEN where t lies
 // outside every sequence, PAGED_NO_ENTRY (reported) where it has no valid place.
-__device__ __forceinline__ int64_t paged_new_row(const PagedView& kv, const int32_t* q_start, int64_t t) {
-    if (t < __ldg(q_start) || t >= __ldg(q_start + kv.B)) return PAGED_NO_TOKEN;
-    const int b = paged_seq_of(q_start, kv.B, t);
+// Whole warp; the sequence is the number of those that end at or before t, so
+// that its lookup is one round of loads (for up to 32 sequences) and no chain.
+__device__ __forceinline__ int64_t paged_new_row_warp(const PagedView& kv, const int32_t* q_start, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    int b = 0;
+#pragma unroll 4
+    for (int i = lane; i < kv.B; i += 32) b += __ldg(q_start + i + 1) <= t;
+    b = __reduce_add_sync(~0u, b);
+    if (b >= kv.B || t < __ldg(q_start + b)) return PAGED_NO_TOKEN;
     const int32_t a = __ldg(q_start + b), e1 = __ldg(q_start + b + 1);
     const int32_t n = paged_len(kv, b);
     const int64_t e = (int64_t)n - (e1 - a) + (t - a);

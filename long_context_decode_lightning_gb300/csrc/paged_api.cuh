@@ -378,9 +378,15 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
     p.vh = v_head_stride;
     p.T = T;
     p.Hq = q_heads;
+    // as many tokens a block as leave every SM the blocks that it holds at once
+    const int64_t room = APPEND_CTAS * (int64_t)sm_count();
+    if (room <= 0) return HSI_ERR_CUDA;
+    const int64_t tb = (T + room - 1) / room;
+    p.tb = (int)(tb > APPEND_TOKENS ? APPEND_TOKENS : tb);
+    const dim3 grid((unsigned)((T + p.tb - 1) / p.tb));
     if (cache->dtype == HSI_BF16)
-        return launch(paged_append_kernel<__nv_bfloat16>, dim3((unsigned)T), dim3(ROPE_THREADS), 0, stream, p);
-    return launch(paged_append_kernel<__half>, dim3((unsigned)T), dim3(ROPE_THREADS), 0, stream, p);
+        return launch(paged_append_kernel<__nv_bfloat16>, grid, dim3(ROPE_THREADS), 0, stream, p);
+    return launch(paged_append_kernel<__half>, grid, dim3(ROPE_THREADS), 0, stream, p);
 }
 
 size_t hsi_paged_attention_ws(int32_t B, int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t max_q, int64_t max_kv) {

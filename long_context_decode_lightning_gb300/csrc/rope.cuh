@@ -96,25 +96,48 @@ __host__ __device__ constexpr int rope_spans(int D, int rot, int pairs) {
     return pairs ? D / V : (D - rot / 2) / V;
 }
 
+// cs: the token's (cos, sin) pairs, 16-byte aligned where a vector's pairs start.
 template <typename T>
 __device__ __forceinline__ void rope_rotate(const RopeSpan& s, bool pairs, const float2* cs, Vec16<T>& a, Vec16<T>& b) {
-    constexpr int V = Vec16<T>::N;
     if (s.pair < 0) return;
-    if (pairs) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 c = cs[s.pair + i];
-            const float u = to_f(a.v[2 * i]), v = to_f(a.v[2 * i + 1]);
-            a.v[2 * i] = from_f<T>(u * c.x - v * c.y);
-            a.v[2 * i + 1] = from_f<T>(u * c.y + v * c.x);
+    if constexpr (sizeof(T) == 4) {
+        if (pairs) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + s.pair);
+            const float u0 = a.v[0], v0 = a.v[1], u1 = a.v[2], v1 = a.v[3];
+            a.v[0] = u0 * c.x - v0 * c.y;
+            a.v[1] = u0 * c.y + v0 * c.x;
+            a.v[2] = u1 * c.z - v1 * c.w;
+            a.v[3] = u1 * c.w + v1 * c.z;
+            return;
         }
-    } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float2 c = cs[s.pair + i];
-            const float u = to_f(a.v[i]), v = to_f(b.v[i]);
-            a.v[i] = from_f<T>(u * c.x - v * c.y);
-            b.v[i] = from_f<T>(u * c.y + v * c.x);
+        for (int i = 0; i < 4; i += 2) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + s.pair + i);
+            const float u0 = a.v[i], u1 = a.v[i + 1], v0 = b.v[i], v1 = b.v[i + 1];
+            a.v[i] = u0 * c.x - v0 * c.y;
+            b.v[i] = u0 * c.y + v0 * c.x;
+            a.v[i + 1] = u1 * c.z - v1 * c.w;
+            b.v[i + 1] = u1 * c.w + v1 * c.z;
+        }
+    } else {  // 32-bit words of two values
+        uint32_t* x = &a.raw.x;
+        uint32_t* y = &b.raw.x;
+        if (pairs) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float4 c = *reinterpret_cast<const float4*>(cs + s.pair + i);
+                const float2 p = unpack2<T>(x[i]), q = unpack2<T>(x[i + 1]);
+                x[i] = pack2<T>(p.x * c.x - p.y * c.y, p.x * c.y + p.y * c.x);
+                x[i + 1] = pack2<T>(q.x * c.z - q.y * c.w, q.x * c.w + q.y * c.z);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 c = *reinterpret_cast<const float4*>(cs + s.pair + 2 * i);
+                const float2 u = unpack2<T>(x[i]), v = unpack2<T>(y[i]);
+                x[i] = pack2<T>(u.x * c.x - v.x * c.y, u.y * c.z - v.y * c.w);
+                y[i] = pack2<T>(u.x * c.y + v.x * c.x, u.y * c.w + v.y * c.z);
+            }
         }
     }
 }
@@ -126,7 +149,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeParams p) {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int V = Vec16<T>::N;
-    __shared__ float2 cs[ROPE_CS];
+    __shared__ __align__(16) float2 cs[ROPE_CS];
     const T* x = static_cast<const T*>(p.x);
     T* y = static_cast<T*>(p.y);
     const int64_t t0 = (int64_t)blockIdx.x * p.tb;
@@ -206,55 +229,78 @@ struct PagedAppendParams {
     void* q_out;
     int64_t qt, qh, ot, oh, kt, kh, vt, vh;
     int64_t T;
-    int Hq;
+    int Hq, tb;  // query heads; tokens per block
 };
 
-// A block per new token: its query heads are rotated (when given), its key
-// heads are rotated into their page, its value heads copied there. One launch
-// in place of four, each of which would be little but its ramp at one token
-// per sequence.
+// Blocks of up to sixteen new tokens: their query heads are rotated (when given),
+// their key heads are rotated into their pages, their value heads copied there.
+// One launch in place of four, each of which would be little but its ramp at
+// one token per sequence. A thread keeps its vectors' places in a token and
+// goes from token to token, so that what finding them costs (two divisions) is
+// shared; the first vectors are loaded at once, and the tokens' places in the
+// pages (three dependent lookups, a warp a token) and cosines come in the
+// loads' shadow.
+constexpr int APPEND_UNROLL = 4, APPEND_TOKENS = 16, APPEND_CTAS = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(ROPE_THREADS) paged_append_kernel(PagedAppendParams p) {
+__global__ void __launch_bounds__(ROPE_THREADS, APPEND_CTAS) paged_append_kernel(PagedAppendParams p) {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int V = Vec16<T>::N;
-    __shared__ float2 cs[64];  // heads of at most 128 dims
-    __shared__ int64_t s_row;  // element offset of the token's place in the pages, -1: none
-    const int64_t t = blockIdx.x;
+    __shared__ __align__(16) float2 cs[APPEND_TOKENS * 64];   // heads of at most 128 dims
+    __shared__ int64_t s_row[APPEND_TOKENS];    // element offset of a token's place in the pages, or why it has none
+    const int64_t t0 = (int64_t)blockIdx.x * p.tb;
+    const int nt = (int)(p.T - t0 < p.tb ? p.T - t0 : p.tb);
     const int half = p.r.steps ? p.r.rot / 2 : 0;
-    if (threadIdx.x == ROPE_THREADS - 1) s_row = paged_new_row(p.kv, p.q_start, t);
-    for (int i = threadIdx.x; i < half; i += ROPE_THREADS) cs[i] = rope_turn(p.r, i, __ldg(p.r.pos + t));
-    __syncthreads();
-    const int64_t row = s_row;
-    if (row == PAGED_NO_TOKEN) return;
     const int D = p.kv.D, Hkv = p.kv.H;
     const int W = half ? rope_spans<V>(D, p.r.rot, p.r.pairs) : D / V, Wv = D / V;
-    const int nq = p.q ? p.Hq * W : 0, nk = Hkv * W, items = nq + nk + Hkv * Wv;
-    for (int i = threadIdx.x; i < items; i += ROPE_THREADS) {
-        const T* in;
-        T* out;
-        RopeSpan sp;
-        if (i < nq + nk) {
-            const bool is_q = i < nq;
-            const int r = is_q ? i : i - nq, h = r / W;
-            sp = half ? rope_span<V>(r - h * W, p.r.rot, p.r.off, p.r.pairs) : RopeSpan{(r - h * W) * V, -1, -1};
-            if (!is_q && row < 0) continue;
-            in = is_q ? static_cast<const T*>(p.q) + t * p.qt + h * p.qh : static_cast<const T*>(p.k) + t * p.kt + h * p.kh;
-            out = is_q ? static_cast<T*>(p.q_out) + t * p.ot + h * p.oh
-                       : static_cast<T*>(p.kv.k) + row + h * p.kv.head_stride;
-        } else {
-            const int r = i - nq - nk, h = r / Wv;
-            if (row < 0) continue;
-            sp = RopeSpan{(r - h * Wv) * V, -1, -1};
-            in = static_cast<const T*>(p.v) + t * p.vt + h * p.vh;
-            out = static_cast<T*>(p.kv.v) + row + h * p.kv.head_stride;
+    const int nq = p.q ? p.Hq * W : 0, nk = Hkv * W, per = nq + nk + Hkv * Wv;
+    bool first = true;
+    for (int i0 = 0; i0 < per; i0 += ROPE_THREADS) {
+        const int i = i0 + threadIdx.x;
+        const int kind = i >= per ? -1 : i < nq ? 0 : i < nq + nk ? 1 : 2;  // q, k, v
+        const int r = i - (kind == 1 ? nq : kind == 2 ? nq + nk : 0), wide = kind == 2 ? Wv : W, h = r / wide;
+        const RopeSpan sp = half && kind < 2 ? rope_span<V>(r - h * wide, p.r.rot, p.r.off, p.r.pairs)
+                                             : RopeSpan{(r - h * wide) * V, -1, -1};
+        const int64_t in_step = kind == 0 ? p.qt : kind == 1 ? p.kt : p.vt;
+        const T* in = kind == 0   ? static_cast<const T*>(p.q) + h * p.qh
+                      : kind == 1 ? static_cast<const T*>(p.k) + h * p.kh
+                                  : static_cast<const T*>(p.v) + h * p.vh;
+        in += t0 * in_step + sp.m;
+        T* out = kind == 0   ? static_cast<T*>(p.q_out) + t0 * p.ot + h * p.oh
+                 : kind == 1 ? static_cast<T*>(p.kv.k) + h * p.kv.head_stride
+                             : static_cast<T*>(p.kv.v) + h * p.kv.head_stride;
+        out += sp.m;
+        const int pair_step = sp.n - sp.m;  // to a half's partner
+        for (int k0 = 0; k0 < nt; k0 += APPEND_UNROLL) {
+            Vec16<T> a[APPEND_UNROLL], b[APPEND_UNROLL];
+#pragma unroll
+            for (int u = 0; u < APPEND_UNROLL; ++u) {
+                if (kind < 0 || k0 + u >= nt) continue;
+                a[u].raw = *reinterpret_cast<const uint4*>(in + (k0 + u) * in_step);
+                if (sp.n >= 0) b[u].raw = *reinterpret_cast<const uint4*>(in + (k0 + u) * in_step + pair_step);
+            }
+            if (first) {
+                for (int j = threadIdx.x >> 5; j < nt; j += ROPE_THREADS / 32) {
+                    const int64_t row = paged_new_row_warp(p.kv, p.q_start, t0 + j);
+                    if ((threadIdx.x & 31) == 0) s_row[j] = row;
+                }
+                for (int j = threadIdx.x; j < nt * half; j += ROPE_THREADS)
+                    cs[j] = rope_turn(p.r, j % half, __ldg(p.r.pos + t0 + j / half));
+                __syncthreads();
+                first = false;
+            }
+#pragma unroll
+            for (int u = 0; u < APPEND_UNROLL; ++u) {
+                if (kind < 0 || k0 + u >= nt) continue;
+                const int64_t row = s_row[k0 + u];
+                if (row == PAGED_NO_TOKEN || (kind > 0 && row < 0)) continue;
+                T* to = out + (kind == 0 ? (k0 + u) * p.ot : row);
+                rope_rotate<T>(sp, p.r.pairs, cs + (k0 + u) * half, a[u], b[u]);
+                *reinterpret_cast<uint4*>(to) = a[u].raw;
+                if (sp.n >= 0) *reinterpret_cast<uint4*>(to + pair_step) = b[u].raw;
+            }
         }
-        Vec16<T> a, b;
-        a.raw = *reinterpret_cast<const uint4*>(in + sp.m);
-        if (sp.n >= 0) b.raw = *reinterpret_cast<const uint4*>(in + sp.n);
-        rope_rotate<T>(sp, p.r.pairs, cs, a, b);
-        *reinterpret_cast<uint4*>(out + sp.m) = a.raw;
-        if (sp.n >= 0) *reinterpret_cast<uint4*>(out + sp.n) = b.raw;
     }
 }
 
