@@ -440,13 +440,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             const uint32_t id_s = idesc_f16(is_bf16<T>, 128, CH_KEYS, false) | (p.negate ? 1u << 13 : 0u);  // of -Q
             constexpr uint32_t TILE16 = C::TILE_BYTES >> 4;
             const uint32_t tm = uniform(tmem);
-            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_ring)), k_desc = smem_desc_sw128(smem_u32(kv_ring)),
+            const uint32_t q_desc = smem_desc_sw128(smem_u32(q_ring)), k_desc = smem_desc_sw128(smem_u32(kv_ring)),
                            v_desc = smem_desc_sw128(smem_u32(kv_ring), C::HALF_BYTES);
             int qst = 0, st = 0;          // the query stage, the stage of the next K or V
             uint32_t qph = 0, ph = 0;     // and their phases
             uint32_t it = 0, seg = 0;     // of row tile w, in bit w: parities of its key tiles and segments so far
             auto product_s = [&](int w) {
-                const uint64_t a = uniform(q_desc + (qst * 2 + w) * TILE16), b = uniform(k_desc + st * TILE16);
+                const uint32_t a = uniform(q_desc + (qst * 2 + w) * TILE16), b = uniform(k_desc + st * TILE16);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 next();
                 for (int i = 0; i < k.n; ++i) {
                     const int vst = st;
-                    const uint64_t v = uniform(v_desc + vst * TILE16);
+                    const uint32_t v = uniform(v_desc + vst * TILE16);
                     const uint32_t more = uniform((uint32_t)i);
                     ok = wait_bounded(&s.kv_full[st], ph, &s.abort);
                     next();  // to the next K

@@ -346,22 +346,21 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// A value that is the same in every lane, in a form the compiler knows to be:
-// operands of the tensor-core instructions live in the warp's uniform
-// registers, and what is not known to be uniform is moved there one by one.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(~0u, v, 0); }
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-    return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
-}
+// A value that is the same in every lane, put into a uniform register by a
+// reduction: operands of the tensor-core instructions live there, and what the
+// compiler does not know to be uniform it moves there one by one.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(~0u, v); }
 
 // Shared-memory matrix descriptor of rows of 128 bytes, 128-byte swizzle,
 // 8-row groups 1024 bytes apart. K-major operands (rows along M or N, 64
 // values of K each): a step of 16 along K starts 32 bytes further. MN-major
 // (rows along K, 64 values of N each): `lbo` is the distance between
 // 64-value columns of N and a step of 16 along K starts 2048 bytes further.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo = 16) {
-    return smem_desc(saddr, lbo, 1024) | (uint64_t)2 << 61;
+// The upper half is the same for all: only the lower one is passed around.
+__device__ __forceinline__ uint32_t smem_desc_sw128(uint32_t saddr, uint32_t lbo = 16) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) & 0x3FFFu) << 16;
 }
+constexpr uint32_t SMEM_DESC_SW128_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulators, A and B
 // both fp16 or both bf16, A K-major, B K-major or (b_mn) MN-major.
@@ -371,40 +370,45 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, uint32_t M, uint32_t
 }
 
 // D[tmem] = A[smem] * B[smem]^T, one thread issues; mma_f16_ss_add adds to D.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+// adesc, bdesc: lower halves of smem_desc_sw128 descriptors.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc)
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "n"(SMEM_DESC_SW128_HI)
         : "memory");
 }
-__device__ __forceinline__ void mma_f16_ss_add(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+__device__ __forceinline__ void mma_f16_ss_add(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc)
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "n"(SMEM_DESC_SW128_HI)
         : "memory");
 }
 
 // The same with A in tensor memory (two 16-bit values of K to a column), D
 // added to where `accumulate` is not 0.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "n"(SMEM_DESC_SW128_HI)
         : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts_add(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+__device__ __forceinline__ void mma_f16_ts_add(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
         "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc)
+        "mov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(bdesc), "r"(idesc), "n"(SMEM_DESC_SW128_HI)
         : "memory");
 }
 

@@ -13,8 +13,7 @@
 // bound it together. A CTA keeps 256 entries of K in shared memory and streams
 // the query tiles past them (one 32 KB tile per 1024 tensor cycles; 128 entries
 // would ask twice the L2 rate), two accumulators per 128 entries, and
-// four warpgroups: one per 128 entries and half of the columns, so that four warps a
-// scheduler hide the latencies of loads and exponentials (two: 204 us against 165).
+// four warpgroups, each for every other tile of its 128 entries.
 // Few entries: a cluster shares a unit's query tiles and adds up the partial
 // sums through distributed shared memory, in rank order.
 #pragma once
@@ -39,11 +38,13 @@ struct WeightsCfg {
     static constexpr int K_BYTES = 2 * Q_BYTES;             // of a unit
     static constexpr int K_STAGES = 2;
     static constexpr int Q_STAGES = D == 128 ? 3 : 6;
+    static constexpr int NL_STAGES = 3;
     static constexpr int RING_BYTES = K_STAGES * K_BYTES + Q_STAGES * Q_BYTES;
     struct Tail {
-        float nl[4][2][WC_ROWS / 2];  // -lse (base 2) of a warpgroup's columns, double-buffered
+        float nl[NL_STAGES][WC_ROWS];  // -lse (base 2) of a tile's rows
+        float part[2][128];            // per 128 entries: one warpgroup's sums, then the block's
         uint64_t k_full[K_STAGES], k_empty[K_STAGES], q_full[Q_STAGES], q_empty[Q_STAGES];
-        uint64_t s_full[2][2], s_empty[2][2], done;
+        uint64_t nl_full[NL_STAGES], nl_empty[NL_STAGES], s_full[2][2], s_empty[2][2], done;
         uint32_t tmem;
         int abort;
     };
@@ -85,7 +86,8 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::K_STAGES; ++i) mbar_init(&s.k_full[i], 1), mbar_init(&s.k_empty[i], 1);
         for (int i = 0; i < C::Q_STAGES; ++i) mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&s.s_full[i >> 1][i & 1], 1), mbar_init(&s.s_empty[i >> 1][i & 1], 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&s.s_full[i >> 1][i & 1], 1), mbar_init(&s.s_empty[i >> 1][i & 1], 4);
+        for (int i = 0; i < C::NL_STAGES; ++i) mbar_init(&s.nl_full[i], 1), mbar_init(&s.nl_empty[i], 8);
         mbar_init(&s.done, 1);
         fence_mbar_init();
         s.abort = 0;
@@ -114,6 +116,13 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
     w.load(p);
     bool ok = true;
     int kf = 0, qf = 0;  // fills (or uses) of the key and query rings so far
+    int row_tok[4], row_head[4];  // the query producer's rows of a tile: token (-1: none) and head
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = lane + 32 * i;
+        row_tok[i] = row < rpt ? row / p.group : -1;
+        row_head[i] = row % p.group;
+    }
     int q_st = 0;        // the products' query stage and its phase
     uint32_t q_ph = 0;
     for (int64_t u = blockIdx.x / csize; w.seek(p, u); u += step) {
@@ -144,50 +153,68 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                     ++kf;
                 }
             }
-        } else if (warp == 17) {  // query tiles
-            if (lane == 0) {
-                for (int j = j0; j < j1 && ok; j += csize) {
-                    const int st = qf % C::Q_STAGES;
-                    ok = wait_bounded(&s.q_empty[st], (qf / C::Q_STAGES & 1) ^ 1, &s.abort);
-                    if (!ok) break;
-                    ++qf;
-                    if (qf == 1 && *(volatile int*)&g_hsi_skip_first_copy) continue;
+        } else if (warp == 17) {  // query tiles, and their rows' lse
+            const float* lse = p.lse_in + (int64_t)w.at * p.Hq + head * p.group;
+            for (int j = j0; j < j1; j += csize) {
+                const int st = qf % C::Q_STAGES, nst = qf % C::NL_STAGES;
+                float v[4];  // of rows lane, lane + 32, ..
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = j * tpt + row_tok[i];
+                    v[i] = -INFINITY;
+                    if (row_tok[i] >= 0 && t < w.m) v[i] = __ldg(lse + (int64_t)t * p.Hq + row_head[i]);
+                }
+                ok = __all_sync(~0u, ok && wait_bounded(&s.q_empty[st], (qf / C::Q_STAGES & 1) ^ 1, &s.abort));
+                if (!ok) break;
+                if (lane == 0 && !(qf == 0 && *(volatile int*)&g_hsi_skip_first_copy)) {
                     mbar_arrive_expect_tx(&s.q_full[st], rpt * 128 * (D / 64));
                     for (int half = 0; half < D / 64; ++half)
                         tma_rows_box(q_ring + st * C::Q_BYTES + half * C::HALF_BYTES, &qmap, half * 64, head * p.group,
                                      w.at + j * tpt, &s.q_full[st]);
                 }
+                ++qf;
+                ok = __all_sync(~0u, wait_bounded(&s.nl_empty[nst], ((qf - 1) / C::NL_STAGES & 1) ^ 1, &s.abort));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s.nl[nst][lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * LOG2E;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.nl_full[nst]);
             }
         } else if (warp == 16) {  // products: the warp waits, one lane issues
             if (j0 < j1) {
                 constexpr uint32_t idesc = idesc_f16(is_bf16<T>, 128, WC_ROWS, false);
                 const int kst = kf % C::K_STAGES;
                 const uint32_t tm = uniform(tmem);
-                const uint64_t kd = uniform(smem_desc_sw128(smem_u32(k_ring + kst * C::K_BYTES)));
+                const uint32_t kd = uniform(smem_desc_sw128(smem_u32(k_ring + kst * C::K_BYTES)));
                 ok = ok && wait_bounded(&s.k_full[kst], kf / C::K_STAGES & 1, &s.abort);
                 for (int j = j0; j < j1 && __all_sync(~0u, ok); j += csize) {
                     const int buf = qf & 1;
                     ok = wait_bounded(&s.q_full[q_st], q_ph, &s.abort);
-                    const uint64_t qd = uniform(smem_desc_sw128(smem_u32(q_ring + q_st * C::Q_BYTES)));
+                    const uint32_t qd = uniform(smem_desc_sw128(smem_u32(q_ring + q_st * C::Q_BYTES)));
                     const uint32_t d0 = uniform(tm + buf * 128);
+                    ok = ok && wait_bounded(&s.s_empty[0][buf], (qf >> 1 & 1) ^ 1, &s.abort) &&
+                         wait_bounded(&s.s_empty[1][buf], (qf >> 1 & 1) ^ 1, &s.abort);
+                    if (!__all_sync(~0u, ok)) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        // step by step for both accumulators in turn: a chain into one of them waits for
+                        // itself (104 cycles a product in two groups, 81 in turn, 64 at the tensor rate)
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) {
-                        ok = ok && wait_bounded(&s.s_empty[kt][buf], (qf >> 1 & 1) ^ 1, &s.abort);
-                        if (!__all_sync(~0u, ok)) break;
-                        tc_fence_after();
-                        if (elect_one()) {
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = ((ks >> 2) * C::HALF_BYTES + (ks & 3) * 32) >> 4;
 #pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t off = ((ks >> 2) * C::HALF_BYTES + (ks & 3) * 32) >> 4;
-                                const uint64_t a = kd + kt * (C::Q_BYTES >> 4) + off;
+                            for (int kt = 0; kt < 2; ++kt) {
+                                const uint32_t a = kd + kt * (C::Q_BYTES >> 4) + off;
                                 if (ks == 0) mma_f16_ss(d0 + kt * 256, a, qd, idesc);
                                 else mma_f16_ss_add(d0 + kt * 256, a, qd + off, idesc);
                             }
-                            tc_commit(&s.s_full[kt][buf]);
-                            if (kt == 1) tc_commit(&s.q_empty[q_st]);
                         }
-                        __syncwarp();
+                        tc_commit(&s.s_full[0][buf]);
+                        tc_commit(&s.s_full[1][buf]);
+                        tc_commit(&s.q_empty[q_st]);
                     }
+                    __syncwarp();
                     ++qf;
                     if (++q_st == C::Q_STAGES) {
                         q_st = 0;
@@ -198,65 +225,51 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                 __syncwarp();
                 ++kf;
             }
-        } else {  // weights: a thread per entry and half of the columns
-            const int wg = warp >> 2, kt = wg >> 1, half = wg & 1;
-            const int key = k0 + kt * 128 + (threadIdx.x & 127), row = half * 64 + (threadIdx.x & 63);
-            const bool loads = (threadIdx.x & 127) < 64;
-            const int rtok = row / p.group, rhead = head * p.group + row % p.group;
+        } else {  // weights: a thread per entry, a warpgroup for every other tile of it
+            const int wg = warp >> 2, kt = wg >> 1, par = wg & 1, tid = threadIdx.x & 127;
+            const int key = k0 + kt * 128 + tid;
             // first token that sees this entry
             const int t_min = p.causal ? key - past : 0;
             const uint64_t sl2 = f2_pack(p.sl2, p.sl2);
+            const uint32_t ta = tmem + (uint32_t)((warp & 3) * 32 << 16) + (kt * 2 + par) * 128;
             float total = 0.f;
-            // the lse of this thread's row in tile j, loaded a tile ahead; nothing is computed from it
-            // before the next tile, which would wait for the load
-            const float* lse = p.lse_in + (int64_t)w.at * p.Hq + rhead;
-            auto load_lse = [&](int j) {
-                const int t = j * tpt + rtok;
-                float v = -INFINITY;
-                if (loads && j < j1 && row < rpt && t < w.m) v = __ldg(lse + (int64_t)t * p.Hq);
-                return v;
-            };
-            float next = load_lse(j0);
-            for (int j = j0; j < j1; j += csize, ++qf) {
-                const int buf = qf & 1;
-                if (loads) s.nl[wg][buf][threadIdx.x & 63] = next == -INFINITY ? -INFINITY : -next * LOG2E;
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-                next = load_lse(j + csize);
-                ok = ok && __all_sync(~0u, wait_bounded(&s.s_full[kt][buf], qf >> 1 & 1, &s.abort));
-                if (!ok) continue;
+            for (int j = j0; j < j1 && ok; j += csize, ++qf) {
+                if ((qf & 1) != par) continue;
+                const int nst = qf % C::NL_STAGES;
+                ok = wait_bounded(&s.nl_full[nst], qf / C::NL_STAGES & 1, &s.abort);
+                ok = __all_sync(~0u, ok && wait_bounded(&s.s_full[kt][par], qf >> 1 & 1, &s.abort));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t ta = tmem + (uint32_t)((warp & 3) * 32 << 16) + (kt * 2 + buf) * 128 + half * 64;
-                // columns [c_lo, c_hi) of this half count; tiles where all do need no comparison
-                const int rows = min(rpt, (w.m - j * tpt) * p.group), c_hi = rows - half * 64;
-                const int c_lo = (t_min - j * tpt) * p.group - half * 64;
+                // columns [c_lo, rows) count; tiles where all do need no comparison
+                const int rows = min(rpt, (w.m - j * tpt) * p.group);
+                const int c_lo = (t_min - j * tpt) * p.group;
                 const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + kt * 128 + 127 - past);
                 uint64_t add[4] = {0, 0, 0, 0};
                 auto columns = [&](auto masked) {
                     uint32_t r[2][32];
                     tmem_ld32_issue(ta, r[0]);
-                    tmem_ld32_issue(ta + 32, r[1]);
-                    tmem_ld_wait(r[0]);
-                    tmem_ld_waited(r[1]);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const ulonglong2* nlv = reinterpret_cast<const ulonglong2*>(&s.nl[wg][buf][c * 32]);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait(r[c & 1]);
+                        if (c < 3) tmem_ld32_issue(ta + (c + 1) * 32, r[(c + 1) & 1]);
+                        const ulonglong2* nlv = reinterpret_cast<const ulonglong2*>(&s.nl[nst][c * 32]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const ulonglong2 l2 = nlv[i];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int n = 4 * i + 2 * h;
-                                const uint64_t x =
-                                    f2_fma(f2_pack(__uint_as_float(r[c][n]), __uint_as_float(r[c][n + 1])), sl2,
-                                           h ? l2.y : l2.x);
+                                const uint64_t x = f2_fma(
+                                    f2_pack(__uint_as_float(r[c & 1][n]), __uint_as_float(r[c & 1][n + 1])), sl2,
+                                    h ? l2.y : l2.x);
                                 float a, b;
                                 f2_unpack(x, a, b);
                                 a = ex2(a);
                                 b = ex2(b);
                                 if (masked.value) {
                                     const int col = c * 32 + n;
-                                    a = col >= c_lo && col < c_hi ? a : 0.f;
-                                    b = col + 1 >= c_lo && col + 1 < c_hi ? b : 0.f;
+                                    a = col >= c_lo && col < rows ? a : 0.f;
+                                    b = col + 1 >= c_lo && col + 1 < rows ? b : 0.f;
                                 }
                                 add[n / 2 & 3] = f2_add(add[n / 2 & 3], f2_pack(a, b));
                             }
@@ -267,31 +280,33 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                 else columns(std::true_type{});
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.s_empty[kt][buf]);
+                if (lane == 0) {
+                    mbar_arrive(&s.s_empty[kt][par]);
+                    mbar_arrive(&s.nl_empty[nst]);
+                }
                 float a, b, c, d;
                 f2_unpack(f2_add(add[0], add[1]), a, b);
                 f2_unpack(f2_add(add[2], add[3]), c, d);
                 total += (a + b) + (c + d);
             }
-            // the two halves' sums, then the ranks', through the -lse buffers (128 values a
-            // warpgroup), which nobody reads past the barrier
-            const int tid = threadIdx.x & 127;
-            float* part = &s.nl[wg][0][0] + tid;
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-            if (half == 1) *part = total;
-            asm volatile("bar.sync %0, 256;" ::"r"(5 + kt) : "memory");
-            if (half == 0) total += (&s.nl[wg + 1][0][0])[tid];
-            asm volatile("bar.sync %0, 256;" ::"r"(5 + kt) : "memory");
+            // the two warpgroups' sums, then the ranks'
+            float* part = &s.part[kt][tid];
+            if (par == 1) *part = total;
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");
+            if (par == 0) total += *part;
             if (csize > 1) {
-                if (half == 0) *part = total;
+                asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");
+                if (par == 0) *part = total;
                 cluster_sync();
-                if (rank == 0 && half == 0) {
+                if (rank == 0 && par == 0) {
                     total = 0.f;
                     for (int r = 0; r < csize; ++r)
                         total += __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(part), r));
                 }
+            } else {
+                asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");  // read, before the next unit's
             }
-            if (rank == 0 && half == 0 && key < w.len && ok) {
+            if (rank == 0 && par == 0 && key < w.len && ok) {
                 const int64_t at = (int64_t)w.b * p.kv.H + head;
                 const float old = p.acc_in ? p.decay * p.acc_in[at * p.ld_acc_in + key] : 0.f;
                 p.acc_out[at * p.ld_acc_out + key] = old + total;
