@@ -627,8 +627,10 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
  * The products run on the tensor cores with fp32 sums; p is rounded to the
  * cache's type for the second one.
  *  q, out  (dev) [T][q_heads][dim] of the cache's type, strides in elements
- *          (multiples of 8, 16-byte aligned); distinct. Entries that a row sees
- *          must be finite for the row to be.
+ *          (multiples of 8, 16-byte aligned); distinct. v_e of an entry below
+ *          kv_len must be finite for every new token of its sequence, also
+ *          where a row does not see it yet (0 times a NaN is a NaN); k_e of an
+ *          entry that a row does not see may be anything.
  *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
  *  lse     (dev) fp32 [T][q_heads], may be NULL.
  *  ws      (dev) hsi_paged_attention_ws(...) bytes.
@@ -663,7 +665,7 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
  *          up to `budget`.
  *  new_len (dev) out int32 [B]: min(kv_len[b], budget). Distinct from kv_len.
  *  acc_out (dev, may be NULL) fp32 [B][heads][ld_out]: the kept entries' acc in
- *          the order of keep, zeros up to `budget`. It may be acc (up to 393000
+ *          the order of keep, zeros up to `budget`; not overlapping acc. It may be acc (up to 393000
  *          entries, UNSUPPORTED beyond): then zeros up to max_len.
  * Errors: INVALID_ARG (sink + recent > budget among them).
  */

@@ -411,22 +411,22 @@ def _dtype(t: torch.Tensor) -> int:
 
 def _i32(t: torch.Tensor, name: str, n: int) -> int:
     """The address of a contiguous int32 vector of n values."""
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
-        _bad(f"{name}: int32 [{n}], contiguous")
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
+        _bad(f"{name}: int32 [{n}], contiguous, on the GPU")
     return t.data_ptr()
 
 
 def _table(t: torch.Tensor, name: str, B: int) -> int:
     """The row stride of an int32 [B, pages] tensor with contiguous rows."""
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1:
-        _bad(f"{name}: int32 [{B}, pages], rows contiguous")
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1 or not t.is_cuda:
+        _bad(f"{name}: int32 [{B}, pages], rows contiguous, on the GPU")
     return t.stride(0) if B > 1 else t.shape[1]
 
 
 def _heads(t: torch.Tensor, name: str, shape, dtype):
     """Address, token stride and head stride of a [tokens, heads, dims] tensor with contiguous dims."""
-    if t.shape != shape or t.dtype is not dtype:
-        _bad(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _bad(f"{name}: {dtype} {tuple(shape)} on the GPU expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
     st = t.stride()
     if st[2] != 1:
         _bad(f"{name}: dims must be contiguous")
@@ -434,22 +434,22 @@ def _heads(t: torch.Tensor, name: str, shape, dtype):
 
 
 def _steps(t: torch.Tensor) -> int:
-    if t.dtype is not torch.int64 or t.dim() != 1 or not t.is_contiguous():
-        _bad("steps: int64 [pairs], contiguous")
+    if t.dtype is not torch.int64 or t.dim() != 1 or not t.is_contiguous() or not t.is_cuda:
+        _bad("steps: int64 [pairs], contiguous, on the GPU")
     return t.data_ptr()
 
 
 def _lse(t: torch.Tensor, shape) -> int:
-    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
-        _bad(f"lse: fp32 {tuple(shape)}, contiguous")
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _bad(f"lse: fp32 {tuple(shape)}, contiguous, on the GPU")
     return t.data_ptr()
 
 
 def _acc(t: torch.Tensor, name: str, B: int, H: int):
     """Address and row stride of fp32 [B, H, entries] with evenly spaced rows."""
     shape, st = t.shape, t.stride()
-    if t.dtype is not torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != H or st[2] != 1:
-        _bad(f"{name}: fp32 [{B}, {H}, entries]")
+    if t.dtype is not torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != H or st[2] != 1 or not t.is_cuda:
+        _bad(f"{name}: fp32 [{B}, {H}, entries] on the GPU")
     ld = st[1] if H > 1 else (st[0] if B > 1 else shape[2])
     if B > 1 and st[0] != H * ld:
         _bad(f"{name}: rows must be evenly spaced")
@@ -457,8 +457,8 @@ def _acc(t: torch.Tensor, name: str, B: int, H: int):
 
 
 def _keep(t: torch.Tensor, B: int, H: int) -> int:
-    if t.dtype is not torch.int32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != H or not t.is_contiguous():
-        _bad(f"keep: int32 [{B}, {H}, places], contiguous")
+    if t.dtype is not torch.int32 or t.dim() != 3 or t.shape[:2] != (B, H) or not t.is_contiguous() or not t.is_cuda:
+        _bad(f"keep: int32 [{B}, {H}, places], contiguous, on the GPU")
     return t.data_ptr()
 
 
@@ -493,8 +493,9 @@ class PagedKV:
     [B, pages a sequence], kv_len int32 [B] on the device. Keeps the tensors; their contents may change."""
 
     def __init__(self, k, v, table, kv_len):
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride() != k.stride():
-            _bad("k, v: [pages, page size, heads, dim], the same strides, dims contiguous")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride() != k.stride() or \
+                not (k.is_cuda and v.is_cuda):
+            _bad("k, v: [pages, page size, heads, dim] on the GPU, the same strides, dims contiguous")
         if table.dim() != 2:
             _bad("table: int32 [sequences, pages]")
         self.k, self.v, self.table, self.kv_len = k, v, table, kv_len

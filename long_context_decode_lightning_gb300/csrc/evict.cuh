@@ -54,7 +54,7 @@ struct EvictSmem {
     uint32_t scan[EV_THREADS / 32], scan2[EV_THREADS / 32];
     uint32_t low, high;            // of this slice: the range of the unprotected keys; later its two counts
     uint32_t digit, above, count;  // the pass's bin, the entries above it and in it
-    float w[EV_CAP];               // the slice's weights
+    alignas(16) float w[EV_CAP];   // the slice's weights
 };
 
 // The sum of v over the threads before this one. Whole block; scan: a word a warp.

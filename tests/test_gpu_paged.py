@@ -250,6 +250,63 @@ def test_attention_layouts_strides_streams(layout, kv_lens, q_lens, group):
             within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
 
 
+@pytest.mark.parametrize("Hq,Hkv,kv_lens,q_lens", [(130, 1, [300, 90], [3, 2]), (256, 2, [140], [1]), (96, 1, [500], [5])])
+def test_attention_of_wide_groups(Hq, Hkv, kv_lens, q_lens):
+    """Groups past the 128 rows of a tile, and groups that leave part of one empty."""
+    c = Case(43, kv_lens, q_lens, Hq, Hkv, 64, 32, BF)
+    out, lse = torch.full_like(c.q, math.nan), torch.empty(c.T, Hq, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.125, out, lse=lse)
+    want, want_lse, tol, tol_lse = c.attention(0.125, True)
+    within(out, want, tol, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    acc = torch.zeros(c.B, Hkv, c.max_kv, device=DEV)
+    hsi.attention_weights(c.kv, c.q, lse, c.q_start, c.max_q, c.max_kv, 0.125, None, acc)
+    w, wt = c.weights(0.125, True, lse, 1.0, None)
+    for b, n in enumerate(kv_lens):
+        for g in range(Hkv):
+            within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
+
+
+@pytest.mark.parametrize("m", [1, 40])
+def test_attention_of_broadcast_queries(m):
+    """One query row expanded over heads and tokens (strides of 0)."""
+    c = Case(47, [333, 64], [m, m], 4, 2, 64, 16, BF)
+    q = c.q[:1, :1].expand(c.T, 4, 64)
+    out, lse = torch.empty_like(c.q), torch.empty(c.T, 4, device=DEV)
+    hsi.paged_attention(c.kv, q, c.q_start, c.max_q, c.max_kv, 0.125, out, lse=lse)
+    c.q = q.contiguous()
+    want, want_lse, tol, tol_lse = c.attention(0.125, True)
+    within(out, want, tol, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    acc = torch.zeros(c.B, 2, c.max_kv, device=DEV)
+    hsi.attention_weights(c.kv, q, lse, c.q_start, c.max_q, c.max_kv, 0.125, None, acc)
+    w, wt = c.weights(0.125, True, lse, 1.0, None)
+    for b, n in enumerate(c.kv_lens):
+        for g in range(2):
+            within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
+
+
+@pytest.mark.parametrize("m", [1, 3])
+@pytest.mark.parametrize("B,longest", [(40, 900), (70, 5000), (300, 40)])
+def test_attention_of_many_sequences(m, B, longest):
+    """More sequences than a warp has lanes, of lengths from none on: the line, and the short form."""
+    lens = [(i * 7919) % (longest + 1) for i in range(B)]
+    lens = [max(n, m) if i % 5 else n for i, n in enumerate(lens)]
+    new = [m if n else 0 for n in lens]
+    c = Case(53, lens, new, 4, 2, 64, 32, BF)
+    out, lse = torch.full_like(c.q, math.nan), torch.empty(c.T, 4, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.125, out, lse=lse)
+    assert hsi.device_error() == 0
+    want, want_lse, tol, tol_lse = c.attention(0.125, True)
+    within(out, want, tol, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    acc = torch.zeros(c.B, 2, c.max_kv, device=DEV)
+    hsi.attention_weights(c.kv, c.q, lse, c.q_start, c.max_q, c.max_kv, 0.125, None, acc)
+    w, wt = c.weights(0.125, True, lse, 1.0, None)
+    for b in range(0, B, 9):
+        within(acc[b, 1, :lens[b]], w[b][1], wt[b][1], "weights")
+
+
 @pytest.mark.parametrize("q_lens", [[1, 1], [200, 140]])
 def test_attention_of_a_cache_past_32_bit_offsets(q_lens):
     """The sequences' pages lie behind 2^31 elements of K."""
@@ -395,10 +452,8 @@ def test_evict_select(lens, budget, sink, recent, kind):
             assert (k[b, h, m:budget] == -1).all() and (k[b, h, budget:] == -9).all()
             assert np.array_equal(o[b, h, :m].view(np.int32), acc[b, h][want].view(np.int32))
             assert (o[b, h, m:budget] == 0).all() and (o[b, h, budget:] == 7).all()
-    # in place: the kept weights in front, zeros behind them
-    hsi.evict_select(t, kv_len, max(lens), budget, keep, new_len, sink=sink, recent=recent, acc_out=t) \
-        if ld >= budget else None
-    if ld >= budget:
+    if ld >= budget:  # in place: the kept weights in front, zeros behind them
+        hsi.evict_select(t, kv_len, max(lens), budget, keep, new_len, sink=sink, recent=recent, acc_out=t)
         got = t.cpu().numpy()
         for b, n in enumerate(lens):
             m = min(n, budget)
