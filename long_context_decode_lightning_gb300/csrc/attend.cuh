@@ -33,7 +33,7 @@ namespace hsi {
 
 constexpr int AT_ROWS = 16;      // rows of a unit
 constexpr int AT_KT = 64;        // entries of a tile
-constexpr int AT_CLUSTER = 8;    // most blocks of a short unit
+constexpr int AT_CLUSTER = 16;   // most blocks of a short unit
 constexpr int AT_WARPS = 4;      // consumer warps, 16 entries of a tile each
 constexpr int AT_THREADS = 32 * (AT_WARPS + 1);
 
@@ -51,7 +51,7 @@ struct AttendParams {
     float* lse;      // [T][Hq] or null
     // partial sums: slot s holds AT_ROWS x D accumulators, AT_ROWS maxima (base 2), AT_ROWS sums
     float* part;
-    int64_t* base;   // [B + 1] first tile of each sequence on the line
+    uint32_t* base;  // attend_chunk_kernel: [B + 1] first tile of each sequence on the line
     // weights only
     const float* lse_in;
     const float* acc_in;
@@ -79,13 +79,22 @@ __device__ __forceinline__ float4 cluster_load4(const float* mine, int c, int cs
 template <int D>
 __host__ __device__ constexpr int attend_slot_floats(int rows) { return rows * (D + 2); }
 
-// A line of `total` tiles is cut into G <= total runs, so that none is empty.
-// First tile of run `c`:
-__device__ __forceinline__ int64_t line_cut(int64_t total, int64_t c, int64_t G) { return G ? c * total / G : 0; }
-// The run that holds tile x.
-__device__ __forceinline__ int64_t line_run(int64_t total, int64_t x, int64_t G) {
-    return ((x + 1) * G + total - 1) / total - 1;
-}
+// A line of `total` tiles (below 2^31, the host's bound) cut into at most
+// `grid` runs, none empty: the first `rest` of them one tile longer.
+struct Line {
+    uint32_t total, G, q, rest;
+    __device__ __forceinline__ Line(uint32_t total_, uint32_t grid) : total(total_), G(min(grid, total_)) {
+        q = G ? total / G : 0u;
+        rest = total - q * G;
+    }
+    // first tile of run c
+    __device__ __forceinline__ uint32_t cut(uint32_t c) const { return c * q + min(c, rest); }
+    // the run that holds tile x
+    __device__ __forceinline__ uint32_t run(uint32_t x) const {
+        const uint32_t longer = rest * (q + 1);
+        return x < longer ? x / (q + 1) : rest + (x - longer) / q;
+    }
+};
 
 // ---------------------------------------------------------------- mma.sync --
 
@@ -145,7 +154,7 @@ struct AttendCfg {
 // Where a walk along the line stands: the sequence, its tiles and what is left.
 struct LineWalk {
     int b;
-    int64_t first;    // first tile of sequence b
+    int first;        // first tile of sequence b
     int32_t len, m, at;  // entries, new tokens, first new token
     int nt, units;    // tiles of a unit, units of the sequence (row tiles x KV heads)
 };
@@ -158,7 +167,7 @@ __device__ __forceinline__ void walk_load(const AttendParams& p, LineWalk& w) {
     const int rt = (w.m * p.group + AT_ROWS - 1) / AT_ROWS;
     w.units = (WEIGHTS ? 1 : rt) * p.kv.H;  // the weights' units take every row of a KV head
 }
-__device__ __forceinline__ int64_t walk_tiles(const LineWalk& w) { return (int64_t)w.nt * w.units; }
+__device__ __forceinline__ int walk_tiles(const LineWalk& w) { return w.nt * w.units; }
 
 template <typename T, int D, bool WEIGHTS>
 __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
@@ -167,8 +176,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     using C = AttendCfg<D, WEIGHTS>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
-    __shared__ int64_t s_total, s_first;
-    __shared__ int s_b, s_abort;
+    __shared__ uint32_t s_lo, s_hi;
+    __shared__ int s_b, s_first, s_abort;
     __shared__ float s_m[AT_WARPS][AT_ROWS], s_l[AT_WARPS][AT_ROWS];
     uint8_t* const stage0 = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float* const red = reinterpret_cast<float*>(stage0 + C::STAGES * C::STAGE_BYTES);
@@ -188,13 +197,13 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     griddep_launch_dependents();
 
     LineWalk w;
-    int64_t x, hi;  // the tiles of this block: of the line, or (short) of its unit
+    int x, hi;  // the tiles of this block: of the line, or (short) of its unit
     if (!WEIGHTS && csize) {
         // short: a cluster of csize blocks a unit, the unit's tiles in equal parts
         const int u = blockIdx.x / csize, rank = csize > 1 ? (int)cluster_ctarank() : 0;
         const int rts = (p.max_q * p.group + AT_ROWS - 1) / AT_ROWS;
         w.b = u / (rts * p.kv.H);
-        w.first = -(int64_t)(u % (rts * p.kv.H));
+        w.first = -(u % (rts * p.kv.H));
         walk_load<WEIGHTS>(p, w);
         const int per = (w.nt + csize - 1) / csize;
         const int t0 = min(w.nt, rank * per), t1 = min(w.nt, t0 + per);
@@ -213,46 +222,46 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
         // sequences, a lane each, are looked at once)
         if (warp == 0) {
             auto tiles_of = [&](int b) {
-                if (b >= p.kv.B) return (int64_t)0;
+                if (b >= p.kv.B) return 0u;
                 LineWalk w;
                 w.b = b;
                 walk_load<WEIGHTS>(p, w);
-                return walk_tiles(w);
+                return (uint32_t)walk_tiles(w);
             };
-            auto upto = [&](int64_t n) {
+            auto upto = [&](uint32_t n) {
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t up = __shfl_up_sync(~0u, n, o);
+                    const uint32_t up = __shfl_up_sync(~0u, n, o);
                     if (lane >= o) n += up;
                 }
                 return n;
             };
-            int64_t total = 0, n = 0;
+            uint32_t total = 0, n = 0;
             for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
                 n = tiles_of(b0 + lane);
-                const int64_t sum = upto(n);
-                if (!WEIGHTS && blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + sum;
-                total += __shfl_sync(~0u, sum, 31);
+                total += __reduce_add_sync(~0u, n);
             }
-            if (!WEIGHTS && blockIdx.x == 0 && lane == 0) p.base[0] = 0;
-            const int64_t lo = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
-            int64_t before = 0;
+            const Line line(total, gridDim.x);
+            const uint32_t lo = line.cut(blockIdx.x);
+            uint32_t before = 0;
             for (int b0 = 0; b0 < p.kv.B && before <= lo; b0 += 32) {
                 if (p.kv.B > 32) n = tiles_of(b0 + lane);
-                const int64_t sum = upto(n), f = before + sum - n;
-                if (n && lo >= f && lo < f + n) {
+                const uint32_t sum = upto(n), f = before + sum - n;
+                if (lo >= f && lo < f + n) {
                     s_b = b0 + lane;
                     s_first = f;
                 }
                 before += __shfl_sync(~0u, sum, 31);
             }
-            if (lane == 0) s_total = total;
+            if (lane == 0) {
+                s_lo = blockIdx.x < line.G ? lo : 0u;
+                s_hi = blockIdx.x < line.G ? line.cut(blockIdx.x + 1) : 0u;
+            }
         }
         __syncthreads();
-        const int64_t total = s_total, G = min((int64_t)gridDim.x, total);
-        if (blockIdx.x >= G) return;
-        x = line_cut(total, blockIdx.x, G);
-        hi = line_cut(total, blockIdx.x + 1, G);
+        x = s_lo;
+        hi = s_hi;
+        if (x >= hi) return;  // more blocks than tiles
         w.b = s_b;
         w.first = s_first;
         walk_load<WEIGHTS>(p, w);
@@ -267,9 +276,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
             ++w.b;
             walk_load<WEIGHTS>(p, w);
         }
-        const int64_t local = x - w.first;
-        const int unit = (int)(local / w.nt), tile0 = (int)(local % w.nt);
-        const int n_tiles = (int)(hi - x < w.nt - tile0 ? hi - x : w.nt - tile0);
+        const int unit = (x - w.first) / w.nt, tile0 = (x - w.first) % w.nt;
+        const int n_tiles = min(hi - x, w.nt - tile0);
         const int head = unit % p.kv.H, rt = unit / p.kv.H;
         x += n_tiles;
 
@@ -595,55 +603,135 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
     }
 }
 
-// Joins the units that several runs hold: a block per (sequence, row tile, KV
-// head), a thread per output value. Runs of a unit lie side by side: the first
-// wrote its CTA's slot 1, the others their slots 0. Sequences without entries
-// get zeros and lse -inf here.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int grid) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int b = blockIdx.z, head = blockIdx.y, rt = blockIdx.x;
-    LineWalk w;
+// Where unit `unit` of sequence b lies on the line: its first run, and how many
+// runs hold it. Whole warp; sets w to sequence b.
+__device__ __forceinline__ int line_runs_of(const AttendParams& p, int b, int unit, int grid, LineWalk& w, int& c0) {
+    const int lane = threadIdx.x & 31;
+    uint32_t total = 0, before = 0;
+    for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+        uint32_t n = 0;
+        if (b0 + lane < p.kv.B) {
+            w.b = b0 + lane;
+            walk_load<false>(p, w);
+            n = walk_tiles(w);
+        }
+        total += __reduce_add_sync(~0u, n);
+        before += __reduce_add_sync(~0u, b0 + lane < b ? n : 0u);
+    }
     w.b = b;
     walk_load<false>(p, w);
-    const int rows = w.m * p.group;
-    if (rt * AT_ROWS >= rows) return;
-    const int64_t total = p.base[p.kv.B];
-    const int64_t G = min((int64_t)grid, total);
-    const int64_t s0 = p.base[b] + ((int64_t)rt * p.kv.H + head) * w.nt;
-    int64_t c0 = 0, c1 = -1;
-    if (w.nt) {
-        c0 = line_run(total, s0, G);
-        c1 = line_run(total, s0 + w.nt - 1, G);
-        if (c0 == c1) return;  // written whole
-    }
+    c0 = 0;
+    if (!w.nt || unit >= w.units) return 0;
+    const Line line(total, grid);
+    const uint32_t s0 = before + (uint32_t)unit * w.nt;
+    c0 = line.run(s0);
+    return (int)line.run(s0 + w.nt - 1) - c0 + 1;
+}
+
+// Joins the units that several runs hold: a block per (sequence, row tile, KV
+// head) and DIMS dims (all where there are many units). Runs of a unit lie side by side: the first wrote
+// its CTA's slot 1, the others their slots 0. A warp takes a row's maxima and
+// sums, a lane a run, and leaves each run's factor in shared memory; then
+// groups of threads, one per four output values, add up every so many runs (a
+// long sequence alone has up to 304 runs a unit) and the groups' sums are added.
+// Which runs those are needs only
+// the lengths, which were there before the kernel that writes the parts: that
+// comes before the wait for it. Sequences without entries get zeros and lse -inf
+// here.
+constexpr int AT_MAX_RUNS = 512;  // CTAs of the kernel above
+constexpr int AT_JOIN_THREADS = 256;
+
+template <typename T, int D, int DIMS>
+__global__ void __launch_bounds__(AT_JOIN_THREADS) attend_join_kernel(const __grid_constant__ AttendParams p, int grid) {
+    __shared__ float s_f[AT_ROWS][AT_MAX_RUNS];  // a run's factor for a row, over the row's sum
+    __shared__ float4 s_o[AT_JOIN_THREADS];
+    const int b = blockIdx.z, head = blockIdx.y, rt = blockIdx.x / (D / DIMS);
+    const int d0 = blockIdx.x % (D / DIMS) * DIMS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    LineWalk w;
+    int c0;
+    const int runs = line_runs_of(p, b, rt * p.kv.H + head, grid, w, c0);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rows = min(AT_ROWS, w.m * p.group - rt * AT_ROWS);
+    if (rows <= 0 || runs == 1) return;  // no rows, or written whole
     constexpr int SLOT = attend_slot_floats<D>(AT_ROWS);
-    for (int i = threadIdx.x; i < AT_ROWS * (D / 4); i += 128) {
-        const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = rt * AT_ROWS + row;
-        if (r >= rows) break;
-        float m = -INFINITY;
-        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part[(2 * c + (c == c0)) * SLOT + AT_ROWS * D + row]);
+    const float* first = p.part + (int64_t)(2 * c0 + 1) * SLOT;
+    const float* rest = p.part + (int64_t)2 * c0 * SLOT;  // run i > 0: rest + 2 i SLOT
+    for (int row = warp; row < rows; row += AT_JOIN_THREADS / 32) {
+        float mc[AT_MAX_RUNS / 32], lc[AT_MAX_RUNS / 32], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < AT_MAX_RUNS / 32; ++k) {  // all loads at once
+            const int i = lane + 32 * k;
+            mc[k] = -INFINITY;
+            lc[k] = 0.f;
+            if (i < runs) {
+                const float* slot = i ? rest + 2 * i * SLOT : first;
+                mc[k] = slot[AT_ROWS * D + row];
+                lc[k] = slot[AT_ROWS * (D + 1) + row];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < AT_MAX_RUNS / 32; ++k) m = fmaxf(m, mc[k]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+#pragma unroll
+        for (int k = 0; k < AT_MAX_RUNS / 32; ++k) {
+            mc[k] = mc[k] == -INFINITY ? 0.f : ex2(mc[k] - m);
+            l += mc[k] * lc[k];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+        for (int k = 0; k < AT_MAX_RUNS / 32; ++k)
+            if (lane + 32 * k < runs) s_f[row][lane + 32 * k] = mc[k] * inv;
+        if (lane == 0 && p.lse && d0 == 0) {
+            const int r = rt * AT_ROWS + row;
+            p.lse[(w.at + r / p.group) * (int64_t)p.Hq + head * p.group + r % p.group] =
+                l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        }
+    }
+    __syncthreads();
+    const int items = rows * (DIMS / 4);
+    const int groups = items < AT_JOIN_THREADS ? min(AT_JOIN_THREADS / items, 32) : 1;
+    const int group = items < AT_JOIN_THREADS ? threadIdx.x / items : 0;
+    for (int i = threadIdx.x - group * items; group < groups && i < items; i += AT_JOIN_THREADS) {
+        const int row = i / (DIMS / 4), d = d0 + (i % (DIMS / 4)) * 4, r = rt * AT_ROWS + row;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float* slot = p.part + (2 * c + (c == c0)) * SLOT;
-            const float mc = slot[AT_ROWS * D + row];
-            const float f = mc == -INFINITY ? 0.f : ex2(mc - m);
-            const float4 v = *reinterpret_cast<const float4*>(slot + row * D + d);
+#pragma unroll 8
+        for (int c = group; c < runs; c += groups) {
+            const float f = s_f[row][c];
+            const float4 v = *reinterpret_cast<const float4*>((c ? rest + 2 * c * SLOT : first) + row * D + d);
             o.x += f * v.x;
             o.y += f * v.y;
             o.z += f * v.z;
             o.w += f * v.w;
-            l += f * slot[AT_ROWS * D + AT_ROWS + row];
         }
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        if (groups > 1) {
+            s_o[group * items + i] = o;
+            break;
+        }
         const int64_t tok = w.at + r / p.group;
         const int h = head * p.group + r % p.group;
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + d) =
-            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-        if (d == 0 && p.lse) p.lse[tok * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+            make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
     }
+    if (groups == 1) return;
+    __syncthreads();
+    if (group) return;
+    const int i = threadIdx.x, row = i / (DIMS / 4), d = d0 + (i % (DIMS / 4)) * 4, r = rt * AT_ROWS + row;
+    float4 o = s_o[i];
+    for (int c = 1; c < groups; ++c) {
+        const float4 v = s_o[c * items + i];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+    }
+    const int64_t tok = w.at + r / p.group;
+    const int h = head * p.group + r % p.group;
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + d) =
+        make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
 }
 
 }  // namespace hsi

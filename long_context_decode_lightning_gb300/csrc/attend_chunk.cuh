@@ -34,27 +34,6 @@ constexpr int CH_KEYS = 128;               // entries of a key tile
 constexpr int CH_THREADS = 32 * 12;        // two softmax warpgroups; one of MMA, copies and two idle warps
 constexpr float CH_LAZY = 8.f;             // growth of a maximum (base 2) that O takes without rescaling
 
-template <int D>
-struct ChunkCfg {
-    static constexpr int HALF_BYTES = 128 * 128;
-    static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // 128 rows of Q, K or V
-    static constexpr int Q_STAGES = D == 128 ? 1 : 2;
-    static constexpr int KV_STAGES = D == 128 ? 5 : 8;
-    static constexpr int RING_BYTES = (2 * Q_STAGES + KV_STAGES) * TILE_BYTES;
-    struct Tail {
-        uint64_t q_full[Q_STAGES], q_empty[Q_STAGES], kv_full[KV_STAGES], kv_empty[KV_STAGES];
-        uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], done;
-        uint32_t tmem;
-        int abort;
-        int64_t total;
-        int b, g, rt, tile;  // where this block's run starts
-    };
-    static constexpr int SMEM_BYTES = RING_BYTES + (int)sizeof(Tail);
-    static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
-};
-
-__host__ __device__ constexpr int64_t chunk_slot_floats(int D) { return 2 * CH_ROWS * (int64_t)(D + 2); }
-
 // Lengths of sequence b and what follows from them.
 struct ChunkSeq {
     int len, m, at, past, n_rt;
@@ -69,17 +48,39 @@ struct ChunkSeq {
         const int seen = p.causal ? min(len, past + min(m, (rt + 1) * 2 * tpt)) : len;
         return seen > 0 ? (seen + CH_KEYS - 1) / CH_KEYS : 0;
     }
-    __device__ __forceinline__ int64_t all_tiles(const AttendParams& p, int tpt) const {
-        int64_t n = 0;
-        for (int rt = 0; rt < n_rt; ++rt) n += tiles(p, rt, tpt);
-        return n;
-    }
 };
+
+template <int D>
+struct ChunkCfg {
+    static constexpr int HALF_BYTES = 128 * 128;
+    static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // 128 rows of Q, K or V
+    static constexpr int Q_STAGES = D == 128 ? 1 : 2;
+    static constexpr int KV_STAGES = D == 128 ? 5 : 8;
+    static constexpr int RING_BYTES = (2 * Q_STAGES + KV_STAGES) * TILE_BYTES;
+    struct Tail {
+        uint64_t q_full[Q_STAGES], q_empty[Q_STAGES], kv_full[KV_STAGES], kv_empty[KV_STAGES];
+        uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], done;
+        uint32_t tmem;
+        int abort;
+        int left, b, g, rt, tile;  // this block's run: key tiles, and where it starts
+        ChunkSeq q;
+    };
+    static constexpr int SMEM_BYTES = RING_BYTES + (int)sizeof(Tail);
+    static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
+};
+
+// A cut of the line this near to a unit's end moves there. A part of a unit
+// costs its own start and end and two partial sums, some four tiles' time; a
+// longer run costs its tiles. So it pays where runs are short, a few units
+// each: 2048 tokens over themselves (14 tiles a run, 8 a unit) 62 us against 73;
+// runs of 73 tiles lost 4% by it.
+__device__ __forceinline__ uint32_t chunk_snap(const Line& line) { return line.q < 32 ? min(4u, line.q / 4) : 0u; }
+
+__host__ __device__ constexpr int64_t chunk_slot_floats(int D) { return 2 * CH_ROWS * (int64_t)(D + 2); }
 
 // A walk along a block's run of the line: segment by segment, each a unit or the part of one that the run holds.
 struct ChunkWalk {
-    int64_t left;
-    int b, g, rt, tile0;
+    int left, b, g, rt, tile0;
     ChunkSeq q;
     int n, tok0, tiles;  // key tiles of the segment, the unit's first token, row tiles that hold tokens
     bool whole;
@@ -100,7 +101,7 @@ struct ChunkWalk {
             step(p, tpt);
             nt = q.tiles(p, rt, tpt);
         }
-        n = (int)(left < nt - tile0 ? left : nt - tile0);
+        n = min(left, nt - tile0);
         whole = tile0 == 0 && n == nt;
         tok0 = rt * 2 * tpt;
         tiles = q.m - tok0 > tpt ? 2 : 1;
@@ -169,66 +170,114 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     fence_proxy_async_smem();
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 0) {  // the line, a lane per sequence: its length, then where this block's run starts
-        int64_t total = 0;
-        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
-            int64_t n = 0;
-            if (b0 + lane < p.kv.B) {
-                ChunkSeq q;
-                q.load(p, b0 + lane, tpt);
-                n = q.all_tiles(p, tpt) * p.kv.H;
+    if (warp == 0) {  // the line: its length, then this block's run
+        // tiles of a KV head's units of sequence b0 + lane: few sequences one by one with a lane per
+        // unit, many with a lane each
+        ChunkSeq mine;  // sequence b0 + lane: loaded at once, handed around by shuffles
+        auto load = [&](int b0) {
+            mine.len = mine.m = mine.at = mine.past = mine.n_rt = 0;
+            if (b0 + lane < p.kv.B) mine.load(p, b0 + lane, tpt);
+        };
+        auto seq = [&](int l) {
+            ChunkSeq q;
+            q.len = __shfl_sync(~0u, mine.len, l);
+            q.m = __shfl_sync(~0u, mine.m, l);
+            q.past = q.len - q.m;
+            q.n_rt = __shfl_sync(~0u, mine.n_rt, l);
+            return q;
+        };
+        auto tiles_of = [&](int b0) {
+            load(b0);
+            uint32_t n = 0;
+            if (p.kv.B >= 32) {
+                for (int rt = 0; rt < mine.n_rt; ++rt) n += mine.tiles(p, rt, tpt);
+                return n;
             }
+            for (int i = 0; i < p.kv.B; ++i) {
+                const ChunkSeq q = seq(i);
+                uint32_t sum = 0;
+                for (int rt = lane; rt < q.n_rt; rt += 32) sum += q.tiles(p, rt, tpt);
+                sum = __reduce_add_sync(~0u, sum);
+                if (lane == i) n = sum;
+            }
+            return n;
+        };
+        auto upto = [&](uint32_t n) {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(~0u, n, o);
+                const uint32_t up = __shfl_up_sync(~0u, n, o);
                 if (lane >= o) n += up;
             }
-            if (blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + n;
-            total += __shfl_sync(~0u, n, 31);
+            return n;
+        };
+        uint32_t total = 0, n = 0;
+        for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+            n = tiles_of(b0);
+            const uint32_t sum = upto(n * p.kv.H);
+            if (blockIdx.x == 0 && b0 + lane < p.kv.B) p.base[b0 + lane + 1] = total + sum;
+            total += __shfl_sync(~0u, sum, 31);
         }
         if (blockIdx.x == 0 && lane == 0) p.base[0] = 0;
-        const int64_t x = line_cut(total, blockIdx.x, min((int64_t)gridDim.x, total));
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.kv.B && before <= x; b0 += 32) {
-            int64_t n = 0;
-            ChunkSeq q;
-            if (b0 + lane < p.kv.B) {
-                q.load(p, b0 + lane, tpt);
-                n = q.all_tiles(p, tpt);
+        const Line line(total, gridDim.x);
+        const uint32_t snap = chunk_snap(line);
+        int cut[2] = {0, 0};  // the run's start and end
+        for (int e = 0; e < 2 && blockIdx.x < line.G; ++e) {
+            const uint32_t x = line.cut(blockIdx.x + e);
+            cut[e] = (int)x;
+            uint32_t before = 0;
+            bool found = e == 1 && (x == total || snap == 0);  // as it is
+            for (int b0 = 0; b0 < p.kv.B && !found; b0 += 32) {
+                if (p.kv.B > 32) n = tiles_of(b0);
+                const uint32_t sum = upto(n * p.kv.H), f = before + sum - n * p.kv.H;
+                const uint32_t has = __ballot_sync(~0u, x >= f && x < f + n * p.kv.H);
+                before += __shfl_sync(~0u, sum, 31);
+                if (!has) continue;
+                found = true;
+                // the sequence, its KV head, then the unit, a lane per unit
+                const int at = __ffs(has) - 1;
+                const uint32_t nb = __shfl_sync(~0u, n, at), off = x - __shfl_sync(~0u, f, at);
+                uint32_t rem = off % nb;
+                const ChunkSeq q = seq(at);
+                for (int r0 = 0; r0 < q.n_rt; r0 += 32) {
+                    const uint32_t t = r0 + lane < q.n_rt ? q.tiles(p, r0 + lane, tpt) : 0;
+                    const uint32_t u = upto(t), all = __shfl_sync(~0u, u, 31);
+                    if (rem >= all) {
+                        rem -= all;
+                        continue;
+                    }
+                    const int l = __ffs(__ballot_sync(~0u, rem < u)) - 1;
+                    const uint32_t nt = __shfl_sync(~0u, t, l), tile = rem - __shfl_sync(~0u, u - t, l);
+                    const uint32_t to = tile <= snap ? 0 : nt - tile <= snap ? nt : tile;
+                    cut[e] = (int)(x + to - tile);
+                    if (e == 0 && lane == at) {
+                        s.q = mine;
+                        s.b = b0 + at;
+                        s.g = off / nb;
+                        s.rt = r0 + l;
+                        s.tile = to;
+                    }
+                    break;
+                }
             }
-            int64_t upto = n * p.kv.H;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(~0u, upto, o);
-                if (lane >= o) upto += up;
-            }
-            const int64_t f = before + upto - n * p.kv.H;
-            if (n && x >= f && x < f + n * p.kv.H) {
-                int64_t rem = (x - f) % n;
-                int rt = 0;
-                for (int t = q.tiles(p, 0, tpt); rem >= t; t = q.tiles(p, ++rt, tpt)) rem -= t;
-                s.b = b0 + lane;
-                s.g = (int)((x - f) / n);
-                s.rt = rt;
-                s.tile = (int)rem;
-            }
-            before += __shfl_sync(~0u, upto, 31);
         }
-        if (lane == 0) s.total = total;
+        if (lane == 0) s.left = cut[1] - cut[0];
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
-    const int64_t total = s.total, G = min((int64_t)gridDim.x, total);
     ChunkWalk k;
-    k.left = blockIdx.x < G ? line_cut(total, blockIdx.x + 1, G) - line_cut(total, blockIdx.x, G) : 0;
-    if (k.left) {
+    k.left = s.left;
+    if (k.left > 0) {
         k.b = s.b;
         k.g = s.g;
         k.rt = s.rt;
         k.tile0 = s.tile;
-        k.q.load(p, k.b, tpt);
+        k.q = s.q;
+        if (k.tile0 == k.q.tiles(p, k.rt, tpt)) {  // the cut moved to the unit's end
+            k.tile0 = 0;
+            k.step(p, tpt);
+        }
     }
     bool ok = true;  // false once a wait has run out: the role ends, after what it has in flight
 
@@ -357,10 +406,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     uint32_t o[32];
                     tmem_ld32_issue(to + c * 32, o);
                     tmem_ld_wait(o);
-                    if (!k.whole) {  // four dims of 32 rows lie side by side
+                    if (!k.whole) {  // four dims of 32 rows lie side by side; rows that hold nothing are not read
+                        if (valid)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            reinterpret_cast<uint4*>(slot)[(c * 8 + j) * 2 * CH_ROWS + w * CH_ROWS + row] =
+                            for (int j = 0; j < 8; ++j)
+                                reinterpret_cast<uint4*>(slot)[(c * 8 + j) * 2 * CH_ROWS + w * CH_ROWS + row] =
                                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     } else if (valid) {
 #pragma unroll
@@ -545,52 +595,52 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 }
 
 // Joins the units that several runs hold, as attend_join_kernel does: a block
-// per unit and 16 dims, a thread per row. Rows that see no entry get zeros and
-// lse -inf here.
-template <typename T, int D>
+// per unit and DIMS dims (fewer where there are few units), a thread per row. Rows that see no entry get
+// zeros and lse -inf here.
+template <typename T, int D, int DIMS>
 __global__ void __launch_bounds__(2 * CH_ROWS)
     attend_chunk_join_kernel(const __grid_constant__ AttendParams p, int grid, int tpt) {
+    const int b = blockIdx.z, g = blockIdx.y, row = threadIdx.x, lane = row & 31;
+    const int rt = blockIdx.x / (D / DIMS), d0 = blockIdx.x % (D / DIMS) * DIMS;
     griddep_wait();
     griddep_launch_dependents();
-    const int b = blockIdx.z, g = blockIdx.y, rt = blockIdx.x / (D / 16), d0 = blockIdx.x % (D / 16) * 16;
     ChunkSeq q;
     q.load(p, b, tpt);
     if (rt >= q.n_rt) return;
-    const int nt = q.tiles(p, rt, tpt), row = threadIdx.x;
-    int64_t c0 = 0, c1 = -1;
+    const int nt = q.tiles(p, rt, tpt);
+    int c0 = 0, c1 = -1;
     if (nt) {
-        // the unit's first tile on the line
-        __shared__ int s_before[2 * CH_ROWS / 32];
-        int before = 0;
-        for (int i = row; i < rt; i += 2 * CH_ROWS) before += q.tiles(p, i, tpt);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
-        if ((row & 31) == 0) s_before[row >> 5] = before;
-        __syncthreads();
-        int64_t x = 0;
-#pragma unroll
-        for (int i = 0; i < 2 * CH_ROWS / 32; ++i) x += s_before[i];
-        const int64_t total = p.base[p.kv.B], G = min((int64_t)grid, total);
-        x += p.base[b] + (p.base[b + 1] - p.base[b]) / p.kv.H * g;
-        c0 = line_run(total, x, G);
-        c1 = line_run(total, x + nt - 1, G);
-        if (c0 == c1) return;  // written whole
+        uint32_t before = 0;
+        for (int i = lane; i < rt; i += 32) before += q.tiles(p, i, tpt);
+        before = __reduce_add_sync(~0u, before);
+        const Line line(p.base[p.kv.B], grid);
+        const uint32_t s0 = p.base[b] + (p.base[b + 1] - p.base[b]) / p.kv.H * g + before;
+        // the runs that the cuts which stayed inside the unit make of it
+        const uint32_t snap = chunk_snap(line);
+        c0 = line.run(min(s0 + snap, line.total - 1));
+        c1 = line.run(max(s0, s0 + nt - min((uint32_t)nt, snap + 1)));
+        if (c0 >= c1) return;  // written whole
     }
     const int w = row / CH_ROWS, r = row % CH_ROWS;
     const int tok = rt * 2 * tpt + w * tpt + r / p.group, h = g * p.group + r % p.group;
     if (r >= tpt * p.group || tok >= q.m) return;
-    constexpr int64_t SLOT = chunk_slot_floats(D);
-    auto slot = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * SLOT; };
+    constexpr int SLOT = (int)chunk_slot_floats(D), V = DIMS / 4;
+    const int runs = c1 - c0 + 1;
+    const float* first = p.part + (int64_t)(2 * c0 + 1) * SLOT;
+    const float* rest = p.part + (int64_t)2 * c0 * SLOT;  // run i > 0: rest + 2 i SLOT
+    auto slot = [&](int i) { return i ? rest + (int64_t)2 * i * SLOT : first; };
     float m = -INFINITY, l = 0.f;
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, slot(c)[2 * CH_ROWS * D + row]);
-    float4 o[4] = {};
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float mc = slot(c)[2 * CH_ROWS * D + row];
+#pragma unroll 8
+    for (int i = 0; i < runs; ++i) m = fmaxf(m, slot(i)[2 * CH_ROWS * D + row]);
+    float4 o[V] = {};
+#pragma unroll 4
+    for (int i = 0; i < runs; ++i) {
+        const float mc = slot(i)[2 * CH_ROWS * D + row];
         const float f = mc == -INFINITY ? 0.f : ex2(mc - m);
-        l += f * slot(c)[2 * CH_ROWS * (D + 1) + row];
+        l += f * slot(i)[2 * CH_ROWS * (D + 1) + row];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 v = reinterpret_cast<const float4*>(slot(c))[(d0 / 4 + j) * 2 * CH_ROWS + row];
+        for (int j = 0; j < V; ++j) {
+            const float4 v = reinterpret_cast<const float4*>(slot(i))[(d0 / 4 + j) * 2 * CH_ROWS + row];
             o[j].x += f * v.x;
             o[j].y += f * v.y;
             o[j].z += f * v.z;
@@ -598,15 +648,15 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
         }
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    uint32_t v[8];
+    uint32_t v[2 * V];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < V; ++j) {
         v[2 * j] = pack2<T>(o[j].x * inv, o[j].y * inv);
         v[2 * j + 1] = pack2<T>(o[j].z * inv, o[j].w * inv);
     }
     uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)(q.at + tok) * p.ot + (int64_t)h * p.oh + d0);
-    out[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    out[1] = make_uint4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) out[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     if (d0 == 0 && p.lse) p.lse[(int64_t)(q.at + tok) * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 

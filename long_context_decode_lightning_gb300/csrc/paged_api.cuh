@@ -160,22 +160,26 @@ hsi_status launch_rope(const RopeParams& p0, cudaStream_t s) {
 int64_t attend_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int64_t max_kv, bool weights) {
     const int64_t rt = weights ? 1 : ((int64_t)max_q * group + AT_ROWS - 1) / AT_ROWS;
     const int64_t tiles = (int64_t)B * heads * rt * ((max_kv + AT_KT - 1) / AT_KT);
+    static_assert(AttendCfg<64, false>::CTAS * 160 <= AT_MAX_RUNS, "the join's runs");
     const int64_t most = (weights ? AttendCfg<64, true>::CTAS : AttendCfg<64, false>::CTAS) * (int64_t)sm_count();
     return tiles < most ? tiles : most;
 }
 
-// Workspace of the attention: the line's prefix, then the partial sums' slots.
-size_t attend_base_bytes(int32_t B) { return align_up(((size_t)B + 1) * 8, 256); }
+// Workspace of the attention: the chunks' line, then the partial sums' slots.
+size_t attend_base_bytes(int32_t B) { return align_up(((size_t)B + 1) * 4, 256); }
 
 // Blocks of a unit in the short form (0: the line). A unit's tiles go to up to
-// eight blocks, four tiles each at most: past that the line's finer cut is
+// sixteen blocks, AT_SHORT_TILES each at most: past that the line's finer cut is
 // quicker. All units at once, or the line evens them out better.
+#ifndef AT_SHORT_TILES
+#define AT_SHORT_TILES 12
+#endif
 int attend_short(const AttendParams& p) {
     const int64_t rt = ((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS, units = rt * p.kv.H * p.kv.B;
     const int64_t tiles = (p.max_kv + AT_KT - 1) / AT_KT, room = 2 * (int64_t)sm_count();
     int csize = 1;
     while (csize < AT_CLUSTER && 2 * csize <= tiles && 2 * csize * units <= room) csize *= 2;
-    return csize * units <= room && tiles <= 4 * csize ? csize : 0;
+    return csize * units <= room && tiles <= AT_SHORT_TILES * csize ? csize : 0;
 }
 
 template <typename T, int D, bool WEIGHTS>
@@ -185,13 +189,28 @@ hsi_status launch_attend_token(const AttendParams& p, const CUtensorMap& km, con
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(attend_token_kernel<T, D, WEIGHTS>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
     const unsigned rt = (unsigned)(((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS);
-    if (const int csize = WEIGHTS ? 0 : attend_short(p))
+    const int csize = WEIGHTS ? 0 : attend_short(p);
+    if (csize > 8) {  // more than the portable size
+        static std::atomic<bool> wide_set[kMaxDevices];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return HSI_ERR_CUDA;
+        if (!wide_set[dev].load(std::memory_order_acquire)) {
+            if (cudaFuncSetAttribute(attend_token_kernel<T, D, WEIGHTS>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                     1) != cudaSuccess)
+                return HSI_ERR_CUDA;
+            wide_set[dev].store(true, std::memory_order_release);
+        }
+    }
+    if (csize)
         return launch_cluster(attend_token_kernel<T, D, WEIGHTS>, dim3(rt * p.kv.H * p.kv.B * csize), dim3(AT_THREADS),
                               C::SMEM_BYTES, csize, s, p, km, vm, csize);
     const hsi_status st = launch(attend_token_kernel<T, D, WEIGHTS>, dim3((unsigned)grid), dim3(AT_THREADS),
                                  C::SMEM_BYTES, s, p, km, vm, 0);
     if (st != HSI_OK || WEIGHTS) return st;
-    return launch(attend_join_kernel<T, D>, dim3(rt, p.kv.H, p.kv.B), dim3(128), 0, s, p, (int)grid);
+    if ((int64_t)rt * p.kv.H * p.kv.B * 2 >= grid)  // blocks for every SM without splitting a unit's dims
+        return launch(attend_join_kernel<T, D, D>, dim3(rt, p.kv.H, p.kv.B), dim3(AT_JOIN_THREADS), 0, s, p, (int)grid);
+    return launch(attend_join_kernel<T, D, 16>, dim3(rt * (D / 16), p.kv.H, p.kv.B), dim3(AT_JOIN_THREADS), 0, s, p,
+                  (int)grid);
 }
 
 template <bool WEIGHTS>
@@ -213,8 +232,12 @@ hsi_status launch_attend_chunk(const AttendParams& p, const CUtensorMap& km, con
     const hsi_status st = launch(attend_chunk_kernel<T, D>, dim3((unsigned)grid), dim3(CH_THREADS), C::SMEM_BYTES, s, p, km,
                                  vm, qm, tpt);
     if (st != HSI_OK) return st;
-    const unsigned rt = (unsigned)((p.max_q + 2 * tpt - 1) / (2 * tpt)) * (D / 16);
-    return launch(attend_chunk_join_kernel<T, D>, dim3(rt, p.kv.H, p.kv.B), dim3(2 * CH_ROWS), 0, s, p, (int)grid, tpt);
+    const unsigned rt = (unsigned)((p.max_q + 2 * tpt - 1) / (2 * tpt));
+    if ((int64_t)rt * p.kv.H * p.kv.B >= grid)
+        return launch(attend_chunk_join_kernel<T, D, 32>, dim3(rt * (D / 32), p.kv.H, p.kv.B), dim3(2 * CH_ROWS), 0, s, p,
+                      (int)grid, tpt);
+    return launch(attend_chunk_join_kernel<T, D, 8>, dim3(rt * (D / 8), p.kv.H, p.kv.B), dim3(2 * CH_ROWS), 0, s, p,
+                  (int)grid, tpt);
 }
 
 // CTAs of the chunk kernel: one an SM, no more than there can be key tiles.
@@ -265,8 +288,9 @@ hsi_status attend_params(const hsi_paged_kv* cache, const void* q, int64_t qt, i
     p->group = q_heads / cache->heads;
     p->sl2 = scale * LOG2E;
     p->causal = causal != 0;
-    // units are counted in 32 bits
-    if ((int64_t)p->max_q * p->group > (int64_t(1) << 30) / cache->heads) return HSI_ERR_UNSUPPORTED;
+    // tiles are counted in 31 bits
+    const int64_t units = ((int64_t)p->max_q * p->group + AT_ROWS - 1) / AT_ROWS * cache->heads;
+    if (units > INT32_MAX || units * cache->B > INT32_MAX / ((p->max_kv + AT_KT - 1) / AT_KT)) return HSI_ERR_UNSUPPORTED;
     return HSI_OK;
 }
 
@@ -417,7 +441,7 @@ hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t
     p.ot = o_token_stride;
     p.oh = o_head_stride;
     p.lse = lse;
-    p.base = static_cast<int64_t*>(ws);
+    p.base = static_cast<uint32_t*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attend_base_bytes(cache->B));
     CUtensorMap km, vm;
     if (chunk_rows(p)) {
