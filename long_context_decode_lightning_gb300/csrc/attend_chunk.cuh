@@ -602,17 +602,18 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
     attend_chunk_join_kernel(const __grid_constant__ AttendParams p, int grid, int tpt) {
     const int b = blockIdx.z, g = blockIdx.y, row = threadIdx.x, lane = row & 31;
     const int rt = blockIdx.x / (D / DIMS), d0 = blockIdx.x % (D / DIMS) * DIMS;
-    griddep_wait();
-    griddep_launch_dependents();
+    // the lengths were there before the kernel that is waited for
     ChunkSeq q;
     q.load(p, b, tpt);
+    const int nt = rt < q.n_rt ? q.tiles(p, rt, tpt) : 0;
+    uint32_t before = 0;
+    for (int i = lane; i < rt; i += 32) before += q.tiles(p, i, tpt);
+    before = __reduce_add_sync(~0u, before);
+    griddep_wait();
+    griddep_launch_dependents();
     if (rt >= q.n_rt) return;
-    const int nt = q.tiles(p, rt, tpt);
     int c0 = 0, c1 = -1;
     if (nt) {
-        uint32_t before = 0;
-        for (int i = lane; i < rt; i += 32) before += q.tiles(p, i, tpt);
-        before = __reduce_add_sync(~0u, before);
         const Line line(p.base[p.kv.B], grid);
         const uint32_t s0 = p.base[b] + (p.base[b + 1] - p.base[b]) / p.kv.H * g + before;
         // the runs that the cuts which stayed inside the unit make of it
@@ -624,27 +625,52 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
     const int w = row / CH_ROWS, r = row % CH_ROWS;
     const int tok = rt * 2 * tpt + w * tpt + r / p.group, h = g * p.group + r % p.group;
     if (r >= tpt * p.group || tok >= q.m) return;
-    constexpr int SLOT = (int)chunk_slot_floats(D), V = DIMS / 4;
+    constexpr int SLOT = (int)chunk_slot_floats(D), V = DIMS / 4, AT_ONCE = 16 / V;  // runs whose loads are in flight
     const int runs = c1 - c0 + 1;
     const float* first = p.part + (int64_t)(2 * c0 + 1) * SLOT;
     const float* rest = p.part + (int64_t)2 * c0 * SLOT;  // run i > 0: rest + 2 i SLOT
-    auto slot = [&](int i) { return i ? rest + (int64_t)2 * i * SLOT : first; };
     float m = -INFINITY, l = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < runs; ++i) m = fmaxf(m, slot(i)[2 * CH_ROWS * D + row]);
     float4 o[V] = {};
-#pragma unroll 4
-    for (int i = 0; i < runs; ++i) {
-        const float mc = slot(i)[2 * CH_ROWS * D + row];
-        const float f = mc == -INFINITY ? 0.f : ex2(mc - m);
-        l += f * slot(i)[2 * CH_ROWS * (D + 1) + row];
+    for (int i0 = 0; i0 < runs; i0 += AT_ONCE) {
+        float mc[AT_ONCE], lc[AT_ONCE];
+        float4 oc[AT_ONCE][V];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int i = i0 + k;
+            const float* slot = i ? rest + (int64_t)2 * i * SLOT : first;
+            mc[k] = -INFINITY;
+            if (i >= runs) continue;
+            mc[k] = slot[2 * CH_ROWS * D + row];
+            lc[k] = slot[2 * CH_ROWS * (D + 1) + row];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                oc[k][j] = reinterpret_cast<const float4*>(slot)[(d0 / 4 + j) * 2 * CH_ROWS + row];
+        }
+        float m_new = m;
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) m_new = fmaxf(m_new, mc[k]);
+        const float keep = m == -INFINITY ? 0.f : ex2(m - m_new);
+        m = m_new;
+        l *= keep;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float4 v = reinterpret_cast<const float4*>(slot(i))[(d0 / 4 + j) * 2 * CH_ROWS + row];
-            o[j].x += f * v.x;
-            o[j].y += f * v.y;
-            o[j].z += f * v.z;
-            o[j].w += f * v.w;
+            o[j].x *= keep;
+            o[j].y *= keep;
+            o[j].z *= keep;
+            o[j].w *= keep;
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            if (mc[k] == -INFINITY) continue;  // past the runs, or a part that this row does not see
+            const float f = ex2(mc[k] - m);
+            l += f * lc[k];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                o[j].x += f * oc[k][j].x;
+                o[j].y += f * oc[k][j].y;
+                o[j].z += f * oc[k][j].z;
+                o[j].w += f * oc[k][j].w;
+            }
         }
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
