@@ -113,22 +113,23 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
         s.w[tid] = acc[tid];
         seen(tid, s.w[tid]);
     }
-#pragma unroll 2
-    for (int i = head + 4 * tid; i < held; i += 4 * EV_THREADS) {
-        if (i + 4 <= held) {
-            const float4 v = *reinterpret_cast<const float4*>(acc + i);
-            const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s.w[i + j] = f[j];
-                seen(i + j, f[j]);
-            }
-        } else {
-            for (int j = i; j < held; ++j) {
-                s.w[j] = acc[j];
-                seen(j, s.w[j]);
-            }
-        }
+    const int vecs = (held - head) / 4, tail = head + 4 * vecs;
+#pragma unroll 4
+    for (int v = tid; v < vecs; v += EV_THREADS) {
+        const int i = head + 4 * v;
+        const float4 f = *reinterpret_cast<const float4*>(acc + i);
+        s.w[i] = f.x;
+        s.w[i + 1] = f.y;
+        s.w[i + 2] = f.z;
+        s.w[i + 3] = f.w;
+        seen(i, f.x);
+        seen(i + 1, f.y);
+        seen(i + 2, f.z);
+        seen(i + 3, f.w);
+    }
+    if (tid < held - tail) {
+        s.w[tail + tid] = acc[tail + tid];
+        seen(tail + tid, s.w[tail + tid]);
     }
     for (int i = held + tid; i < n; i += EV_THREADS) seen(i, acc[i]);
     __syncthreads();
@@ -167,22 +168,23 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
             const int top = 32 - __clz(width), shift = top > 11 ? top - 11 : 0;
             for (int i = tid; i < EV_BINS; i += EV_THREADS) s.hist[i] = 0;
             __syncthreads();
-            auto count = [&](int i, float w) {
-                const uint32_t k = key_of(i, w);
-                if (k != ~0u && k - base <= width) atomicAdd(&s.hist[(k - base) >> shift], 1u);
+            auto count = [&](float w) {  // of the unprotected [p_lo, p_hi)
+                const uint32_t k = order_key(w) - base;
+                if (k <= width) atomicAdd(&s.hist[k >> shift], 1u);
             };
-            for (int i = 4 * tid; i < held; i += 4 * EV_THREADS) {
-                if (i + 4 <= held) {
-                    const float4 v = *reinterpret_cast<const float4*>(&s.w[i]);
-                    count(i, v.x);
-                    count(i + 1, v.y);
-                    count(i + 2, v.z);
-                    count(i + 3, v.w);
-                } else {
-                    for (int j = i; j < held; ++j) count(j, s.w[j]);
-                }
+            // whole vectors between v_lo and v_hi, single entries before and behind
+            const int last = min(p_hi, held), v_lo = min(last, (p_lo + 3) & ~3), v_hi = max(v_lo, last & ~3);
+            if (tid < v_lo - p_lo) count(s.w[p_lo + tid]);
+            if (tid < last - v_hi) count(s.w[v_hi + tid]);
+#pragma unroll 2
+            for (int i = v_lo + 4 * tid; i < v_hi; i += 4 * EV_THREADS) {
+                const float4 v = *reinterpret_cast<const float4*>(&s.w[i]);
+                count(v.x);
+                count(v.y);
+                count(v.z);
+                count(v.w);
             }
-            for (int i = held + tid; i < n; i += EV_THREADS) count(i, acc[i]);
+            for (int i = max(held, p_lo) + tid; i < p_hi; i += EV_THREADS) count(acc[i]);
             if (csize > 1) cluster_sync();
             else __syncthreads();
             // whole-row counts; thread t takes bins 2047 - 2t and the one below (from the top)
@@ -223,17 +225,25 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
         }
     }
 
-    // a run of entries a thread, an odd number (so that the threads' reads spread over the banks):
-    // counted, then written behind the runs before it
-    const int run = (n + EV_THREADS - 1) / EV_THREADS | 1;
-    const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
+    // turns of 32 entries, a run of them a warp: counted, then written side by side behind the
+    // runs before (a run of entries a thread would store them apart: 16000 cycles against 4000)
+    const int turns = (n + 31) / 32, run = (turns + EV_THREADS / 32 - 1) / (EV_THREADS / 32) * 32;
+    const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
     uint32_t gt = 0, eq = 0;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = key_of(i, weight_at(i));
-        gt += all || k > thr;
-        eq += !all && k == thr;
+#pragma unroll 4
+    for (int i = i0; i < i1; i += 32) {
+        const bool live = i + lane < i1;
+        const uint32_t k = live ? key_of(i + lane, weight_at(i + lane)) : 0u;
+        gt += __popc(__ballot_sync(~0u, live && (all || k > thr)));
+        eq += __popc(__ballot_sync(~0u, live && !all && k == thr));
     }
-    uint32_t g0 = block_before(s.scan, gt), e0 = block_before(s.scan2, eq);
+    if (lane == 0) {
+        s.scan[warp] = gt;
+        s.scan2[warp] = eq;
+    }
+    __syncthreads();
+    uint32_t g0 = __reduce_add_sync(~0u, lane < warp ? s.scan[lane] : 0u);
+    uint32_t e0 = __reduce_add_sync(~0u, lane < warp ? s.scan2[lane] : 0u);
     if (csize > 1) {
         if (tid == EV_THREADS - 1) {
             s.low = g0 + gt;
@@ -244,20 +254,23 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
         g0 += __reduce_add_sync(~0u, gr);
         e0 += __reduce_add_sync(~0u, er);
         cluster_sync();  // nobody leaves while its counts are read; every weight has been read
-    } else {
-        __syncthreads();
     }
-    for (int i = i0; i < i1; ++i) {
-        const float w = weight_at(i);
-        const uint32_t k = key_of(i, w);
-        const bool is_g = all || k > thr, is_e = !all && k == thr;
-        if (is_g || (is_e && e0 < need)) {
-            const uint32_t at = g0 + min(e0, need);
-            keep[at] = (int32_t)(lo + i);
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 2
+    for (int i = i0; i < i1; i += 32) {
+        const bool live = i + lane < i1;
+        const float w = live ? weight_at(i + lane) : 0.f;
+        const uint32_t k = key_of(i + lane, w);
+        const uint32_t bg = __ballot_sync(~0u, live && (all || k > thr));
+        const uint32_t be = __ballot_sync(~0u, live && !all && k == thr);
+        const uint32_t er = e0 + __popc(be & below);
+        if ((bg >> lane & 1) || ((be >> lane & 1) && er < need)) {
+            const uint32_t at = g0 + __popc(bg & below) + min(er, need);
+            keep[at] = (int32_t)(lo + i + lane);
             if (out) out[at] = w;
         }
-        g0 += is_g;
-        e0 += is_e;
+        g0 += __popc(bg);
+        e0 += __popc(be);
     }
     // padding: -1 indices, zero weights
     const int64_t pad0 = n_keep + (int64_t)rank * EV_THREADS + tid, pads = (int64_t)csize * EV_THREADS;
@@ -283,7 +296,7 @@ constexpr int CP_ROUNDS = 8;  // entries a thread has in flight
 // Blocks of a (sequence, KV head, K or V): `csize` (in place, as a cluster) or
 // gridDim.x / (2 B H) (to other pages) share its places, CP_ROUNDS times the
 // entries that 16-byte loads of CP_THREADS threads cover at a time.
-__global__ void __launch_bounds__(CP_THREADS) paged_compact_kernel(CompactParams p, int split, int csize) {
+__global__ void __launch_bounds__(CP_THREADS, 4) paged_compact_kernel(CompactParams p, int split, int csize) {
     griddep_wait();
     griddep_launch_dependents();
     const int lanes = p.kv.D / 8, rows = CP_THREADS / lanes;  // threads of an entry, entries of a round

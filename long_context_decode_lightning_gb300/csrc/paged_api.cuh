@@ -513,13 +513,11 @@ hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_
         return HSI_ERR_INVALID_ARG;
     if (acc_out && ld_out < budget) return HSI_ERR_INVALID_ARG;
     int csize = 1;
-    // slices of at most 8192 entries a CTA, and down to 2048 where the rows leave SMs idle
-    const int64_t rows = (int64_t)B * heads, sms = sm_count();
-    while (csize < EV_MAX_CLUSTER &&
-           ((max_len + csize - 1) / csize > 8192 || (max_len > 2048 * csize && 2 * csize * rows <= sms)))
-        csize *= 2;
+    // a CTA a row up to 16384 entries: a cluster's barriers and remote counts, 10000 cycles in all,
+    // cost two CTAs what they save there; slices of 16384 beyond
+    while (csize < EV_MAX_CLUSTER && max_len > (int64_t)csize * 16384) csize *= 2;
     // past the clusters' shared memory, weights are read while others are written
-    if (acc_out == acc && (max_len + csize - 1) / csize + 31 > EV_CAP) return HSI_ERR_UNSUPPORTED;
+    if (acc_out == acc && (max_len + csize - 1) / csize > EV_CAP) return HSI_ERR_UNSUPPORTED;
     if ((int64_t)B * heads * csize > INT32_MAX) return HSI_ERR_UNSUPPORTED;
     EvictParams p{};
     p.acc = acc;
@@ -558,8 +556,9 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     p.dst = dst_table;
     p.ld_dst = ld_dst;
     p.in_place = dst_table == cache->table;
-    // blocks of a (sequence, KV head, K or V): until every SM has eight, none without a turn's entries
-    const int64_t rows = (int64_t)cache->B * cache->heads * 2, want = 8 * (int64_t)sm_count();
+    // blocks of a (sequence, KV head, K or V): until every SM has sixteen (four at a time), none
+    // without a turn's entries
+    const int64_t rows = (int64_t)cache->B * cache->heads * 2, want = 16 * (int64_t)sm_count();
     const int64_t turn = (int64_t)CP_THREADS / (cache->dim / 8) * CP_ROUNDS, most = (budget + turn - 1) / turn;
     if (want <= 0) return HSI_ERR_CUDA;
     int64_t split = 1;
