@@ -665,8 +665,9 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
  *          up to `budget`.
  *  new_len (dev) out int32 [B]: min(kv_len[b], budget). Distinct from kv_len.
  *  acc_out (dev, may be NULL) fp32 [B][heads][ld_out]: the kept entries' acc in
- *          the order of keep, zeros up to `budget`; not overlapping acc. It may be acc (up to 393216
- *          entries, UNSUPPORTED beyond): then zeros up to max_len.
+ *          the order of keep, zeros up to `budget`. It may be acc itself (up to
+ *          393216 entries, UNSUPPORTED beyond): then zeros up to max_len; it
+ *          must not overlap acc otherwise.
  * Errors: INVALID_ARG (sink + recent > budget among them).
  */
 hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_len, int32_t B, int32_t heads,

@@ -558,15 +558,18 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     p.in_place = dst_table == cache->table;
     // blocks of a (sequence, KV head, K or V): until every SM has sixteen (four at a time), none
     // without a turn's entries
-    const int64_t rows = (int64_t)cache->B * cache->heads * 2, want = 16 * (int64_t)sm_count();
-    const int64_t turn = (int64_t)CP_THREADS / (cache->dim / 8) * CP_ROUNDS, most = (budget + turn - 1) / turn;
-    if (want <= 0) return HSI_ERR_CUDA;
+    const int64_t rows = (int64_t)cache->B * cache->heads * 2, sms = sm_count();
+    if (sms <= 0) return HSI_ERR_CUDA;
+    const int64_t round = CP_THREADS / (cache->dim / 8);
+    const bool few = rows * ((budget + 8 * round - 1) / (8 * round)) < 2 * sms;
+    const int64_t turn = round * (few ? 2 : 8), most = (budget + turn - 1) / turn;
     int64_t split = 1;
-    while (split * rows < want && 2 * split <= most && (!p.in_place || split < EV_MAX_CLUSTER)) split *= 2;
+    while (split * rows < 16 * sms && 2 * split <= most && (!p.in_place || split < EV_MAX_CLUSTER)) split *= 2;
     if (rows * split > INT32_MAX) return HSI_ERR_UNSUPPORTED;
     const int csize = p.in_place ? (int)split : 1;
-    return launch_cluster(paged_compact_kernel, dim3((unsigned)(rows * split)), dim3(CP_THREADS), 0, csize, stream, p,
-                          (int)split, csize);
+    const dim3 grid((unsigned)(rows * split));
+    if (few) return launch_cluster(paged_compact_kernel<2>, grid, dim3(CP_THREADS), 0, csize, stream, p, (int)split, csize);
+    return launch_cluster(paged_compact_kernel<8>, grid, dim3(CP_THREADS), 0, csize, stream, p, (int)split, csize);
 }
 
 }  // extern "C"
