@@ -482,9 +482,11 @@ def rope(x, positions, steps, out, rot_offset: int = 0, interleaved: bool = Fals
     T, H, D = shape
     xp, xt, xh = _heads(x, "x", shape, x.dtype)
     yp, yt, yh = _heads(out, "out", shape, x.dtype)
-    _check("hsi_rope", lib().hsi_rope(
+    st = (_lib or lib()).hsi_rope(
         xp, xt, xh, _dtype(x), T, H, D, _i32(positions, "positions", T), _steps(steps), 2 * steps.shape[0], rot_offset,
-        interleaved, gain, inverse, yp, yt, yh, _raw_stream(stream)))
+        interleaved, gain, inverse, yp, yt, yh, _raw_stream(stream))
+    if st:
+        _check("hsi_rope", st)
 
 
 class PagedKV:
@@ -515,15 +517,17 @@ def paged_append(kv: PagedKV, k_new, v_new, q_start, max_q=None, positions=None,
     kp, kt, kh = _heads(k_new, "k_new", (T, kv.heads, kv.dim), dt)
     vp, vt, vh = _heads(v_new, "v_new", (T, kv.heads, kv.dim), dt)
     pos = None if positions is None else _i32(positions, "positions", T)
-    st, rot = (None, 0) if steps is None else (_steps(steps), 2 * steps.shape[0])
+    sp, rot = (None, 0) if steps is None else (_steps(steps), 2 * steps.shape[0])
     qp, qt, qh, op, ot, oh, Hq = None, 0, 0, None, 0, 0, 0
     if q is not None:
         Hq = q.shape[1]
         qp, qt, qh = _heads(q, "q", (T, Hq, kv.dim), dt)
         op, ot, oh = _heads(q_out, "q_out", (T, Hq, kv.dim), dt)
-    _check("hsi_paged_append", lib().hsi_paged_append(
-        kv.ref, kp, kt, kh, vp, vt, vh, _i32(q_start, "q_start", kv.B + 1), T, pos, st, rot, rot_offset, interleaved,
-        gain, qp, qt, qh, Hq, op, ot, oh, _raw_stream(stream)))
+    st = (_lib or lib()).hsi_paged_append(
+        kv.ref, kp, kt, kh, vp, vt, vh, _i32(q_start, "q_start", kv.B + 1), T, pos, sp, rot, rot_offset, interleaved,
+        gain, qp, qt, qh, Hq, op, ot, oh, _raw_stream(stream))
+    if st:
+        _check("hsi_paged_append", st)
 
 
 def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int) -> torch.Tensor:
@@ -541,9 +545,13 @@ def paged_attention(kv: PagedKV, q, q_start, max_q: int, max_kv: int, scale: flo
     op, ot, oh = _heads(out, "out", shape, kv.dtype)
     if ws is None:
         ws = paged_attention_workspace(kv, q, max_q, max_kv)
-    _check("hsi_paged_attention", lib().hsi_paged_attention(
+    elif not ws.is_cuda:
+        _bad("ws: on the GPU")
+    st = (_lib or lib()).hsi_paged_attention(
         kv.ref, qp, qt, qh, Hq, _i32(q_start, "q_start", kv.B + 1), T, max_q, max_kv, scale, causal, op, ot, oh,
-        None if lse is None else _lse(lse, (T, Hq)), ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+        None if lse is None else _lse(lse, (T, Hq)), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if st:
+        _check("hsi_paged_attention", st)
 
 
 def attention_weights(kv: PagedKV, q, lse, q_start, max_q: int, max_kv: int, scale: float, acc_in, acc_out,
@@ -554,9 +562,11 @@ def attention_weights(kv: PagedKV, q, lse, q_start, max_q: int, max_kv: int, sca
     qp, qt, qh = _heads(q, "q", (T, Hq, kv.dim), kv.dtype)
     ip, il = (None, 0) if acc_in is None else _acc(acc_in, "acc_in", kv.B, kv.heads)
     op, ol = _acc(acc_out, "acc_out", kv.B, kv.heads)
-    _check("hsi_attention_weights", lib().hsi_attention_weights(
+    st = (_lib or lib()).hsi_attention_weights(
         kv.ref, qp, qt, qh, Hq, _lse(lse, (T, Hq)), _i32(q_start, "q_start", kv.B + 1), T, max_q, max_kv, scale, causal,
-        decay, ip, il, op, ol, _raw_stream(stream)))
+        decay, ip, il, op, ol, _raw_stream(stream))
+    if st:
+        _check("hsi_attention_weights", st)
 
 
 def evict_select(acc, kv_len, max_len: int, budget: int, keep, new_len, sink: int = 0, recent: int = 0, acc_out=None,
@@ -565,9 +575,11 @@ def evict_select(acc, kv_len, max_len: int, budget: int, keep, new_len, sink: in
     B, H = acc.shape[:2]
     ap, al = _acc(acc, "acc", B, H)
     op, ol = (None, 0) if acc_out is None else _acc(acc_out, "acc_out", B, H)
-    _check("hsi_evict_select", lib().hsi_evict_select(
+    st = (_lib or lib()).hsi_evict_select(
         ap, al, _i32(kv_len, "kv_len", B), B, H, max_len, budget, sink, recent, _keep(keep, B, H), keep.shape[2],
-        _i32(new_len, "new_len", B), op, ol, _raw_stream(stream)))
+        _i32(new_len, "new_len", B), op, ol, _raw_stream(stream))
+    if st:
+        _check("hsi_evict_select", st)
 
 
 def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, stream=None):
@@ -575,6 +587,8 @@ def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, strea
     budget: bound of new_len (keep's width by default)."""
     dst = kv.table if dst_table is None else dst_table
     kp, places = _keep(keep, kv.B, kv.heads), keep.shape[2]
-    _check("hsi_paged_compact", lib().hsi_paged_compact(
+    st = (_lib or lib()).hsi_paged_compact(
         kv.ref, kp, places, _i32(new_len, "new_len", kv.B), places if budget is None else budget, dst.data_ptr(),
-        _table(dst, "dst_table", kv.B), _raw_stream(stream)))
+        _table(dst, "dst_table", kv.B), _raw_stream(stream))
+    if st:
+        _check("hsi_paged_compact", st)

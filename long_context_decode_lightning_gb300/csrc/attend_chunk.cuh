@@ -14,12 +14,20 @@
 // The running maximum is lazy: O is rescaled only where a row's maximum has
 // grown by more than 2^8 since the last time (p stays below 256, exact enough
 // in either type), which after the first tiles hardly happens; the row sum
-// is taken from the fp32 p in the shadow of the exponentials.
+// is taken from the fp32 p in the shadow of the exponentials (the exponentials of
+// half a tile by the old maximum, before the new one is known, were no faster).
 //
 // The units' key tiles (causal: only those that some row of the unit sees)
 // form one line that is cut into equal runs, one per SM, as for single tokens;
 // a unit that spans runs is joined by a second kernel from fp32 partial sums.
-// Bound: the tensor cores.
+//
+// Measured (32 query and 8 KV heads of 128, bf16): 2048 tokens over 32768 entries
+// 735 us alone, 1450 TFLOP/s or 75% of the measured burst rate, and 780 us back to
+// back under the power limit, 80% of the sustained rate. A pair of tiles takes 3300
+// cycles, 2200 of products: the rest is the chain of a tile's S, softmax and P V
+// (1250 cycles from S to P) and the issuing warp's waits. Short units add 8000
+// cycles of start and end each: four chunks of up to 1001 tokens over 5003 entries
+// (28 / 4 heads) 165 us for a floor of 92.
 #pragma once
 #include <cstdint>
 
@@ -473,7 +481,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                         __syncwarp();
                         if (lane < nbox && e0 < have)
                             tma_page_box(kv_ring + st * C::TILE_BYTES + (lane % halves) * C::HALF_BYTES + e0 * 128,
-                                         kind ? &vmap : &kmap, (lane % halves) * 64, (k0 + e0) & ((1 << p.kv.page_shift) - 1), k.g,
+                                         kind ? &vmap : &kmap, (lane % halves) * 64,
+                                         (k0 + e0) & ((1 << p.kv.page_shift) - 1), k.g,
                                          page, &s.kv_full[st]);
                         ++kvn;
                     }

@@ -568,8 +568,10 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     if (rows * split > INT32_MAX) return HSI_ERR_UNSUPPORTED;
     const int csize = p.in_place ? (int)split : 1;
     const dim3 grid((unsigned)(rows * split));
-    if (few) return launch_cluster(paged_compact_kernel<2>, grid, dim3(CP_THREADS), 0, csize, stream, p, (int)split, csize);
-    return launch_cluster(paged_compact_kernel<8>, grid, dim3(CP_THREADS), 0, csize, stream, p, (int)split, csize);
+    const auto kernel = few                                        ? paged_compact_kernel<2, false>
+                        : p.in_place && rows * split <= 2 * sms ? paged_compact_kernel<8, true>
+                                                                : paged_compact_kernel<8, false>;
+    return launch_cluster(kernel, grid, dim3(CP_THREADS), 0, csize, stream, p, (int)split, csize);
 }
 
 }  // extern "C"

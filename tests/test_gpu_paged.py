@@ -509,6 +509,34 @@ def test_compact(lens, budget, page, D, Hkv, layout, in_place):
         assert torch.equal(pages.contiguous().view(torch.int16), want.contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("lens,budget,D,Hkv", [([60000], 50000, 64, 1), ([40000, 33000], 30001, 128, 1)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_of_long_sequences(lens, budget, D, Hkv, in_place):
+    page, B = 64, len(lens)
+    need = -(-budget // page)
+    c = Case(59, lens, [0] * B, Hkv, Hkv, D, page, BF, spare=need * B)
+    acc = torch.rand(B, Hkv, max(lens), device=DEV)
+    keep = torch.empty(B, Hkv, budget, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(B, dtype=torch.int32, device=DEV)
+    hsi.evict_select(acc, c.kv_len, max(lens), budget, keep, new_len)
+    dst = c.table
+    if not in_place:
+        used = set(c.table[(c.table >= 0) & (c.table < c.k.shape[0])].tolist())
+        free = [p for p in range(c.k.shape[0]) if p not in used]
+        dst = torch.tensor(free[:need * B], dtype=torch.int32, device=DEV).view(B, need)
+    want = [c.k.clone(), c.v.clone()]
+    for pages, src in zip(want, (c.K, c.V)):
+        for b in range(B):
+            n = int(new_len[b])
+            i = torch.arange(n, device=DEV)
+            for h in range(Hkv):
+                pages[dst[b, i // page].long(), i % page, h] = src[b][keep[b, h, :n].long(), h]
+    hsi.paged_compact(c.kv, keep, new_len, None if in_place else dst)
+    assert hsi.device_error() == 0
+    for pages, w in zip((c.k, c.v), want):
+        assert torch.equal(pages.view(torch.int16), w.view(torch.int16))
+
+
 def test_compact_skips_what_is_wrong():
     c = Case(31, [100], [0], 1, 1, 64, 16, BF)
     before = c.k.clone()
