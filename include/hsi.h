@@ -660,7 +660,8 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
  * Which entries a budget keeps, per (sequence, KV head): all of them when
  * kv_len[b] <= budget; otherwise the first `sink`, the last `recent` and the
  * largest acc among the rest, ties to the lowest index, `budget` in all.
- *  acc     (dev) fp32 [B][heads][ld_acc], not NaN; max_len (host) bounds kv_len.
+ *  acc     (dev) fp32 [B][heads][ld_acc] (a NaN ranks above +inf or, with its
+ *          sign set, below -inf); max_len (host) bounds kv_len.
  *  keep    (dev) out int32 [B][heads][ld_keep]: the kept entries ascending, -1
  *          up to `budget`.
  *  new_len (dev) out int32 [B]: min(kv_len[b], budget). Distinct from kv_len.

@@ -22,7 +22,7 @@
 // in bf16, averaged by the sum); maxima, sums and the output stay in fp32.
 //
 // Measured (32 query and 8 KV heads of 128, bf16): one token over 16 sequences of
-// up to 65536 entries 485 to 497 us, 98 to 100% of the measured copy rate; over one
+// up to 65536 entries 475 to 497 us, 98 to 102% of the measured copy rate; over one
 // of 8000 entries 17 us (floor 5), the start, a tile's chain of 700 cycles and the
 // join; three short sequences of up to 777 entries (16 / 2 heads of 64) 7.1 us.
 #pragma once

@@ -99,11 +99,13 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
     const int64_t lo = min(len, rank * per);
     const int n = (int)(min(len, lo + per) - lo), held = n < EV_CAP ? n : EV_CAP;
     acc += lo;
-    // protected: i < p_lo or i >= p_hi; they rank above every weight (order_key of a number is below ~0u)
+    // protected: i < p_lo or i >= p_hi; they rank above every weight (whose keys are held below ~0u, so that
+    // even a NaN's, which has no place of its own, is counted like any other)
     const int p_lo = (int)max((int64_t)0, min((int64_t)n, p.sink - lo));
     const int p_hi = (int)max((int64_t)0, min((int64_t)n, len - p.recent - lo));
     auto weight_at = [&](int i) { return i < held ? s.w[i] : acc[i]; };
-    auto key_of = [&](int i, float w) { return i < p_lo || i >= p_hi ? ~0u : order_key(w); };
+    auto rank_of = [&](float w) { return min(order_key(w), ~0u - 1u); };
+    auto key_of = [&](int i, float w) { return i < p_lo || i >= p_hi ? ~0u : rank_of(w); };
 
     // the weights into shared memory, and the range of the unprotected keys
     uint32_t low = ~0u, high = 0u;
@@ -167,13 +169,13 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
         }
         // passes over the range [base, base + width]: 2048 bins of 2^shift keys
         uint32_t base = low, width = high - low;
-        thr = ~0u - 1u;  // where no unprotected entry is wanted
+        thr = ~0u - 1u;  // where no unprotected entry is wanted: above every rank
         while (want > 0) {
             const int top = 32 - __clz(width), shift = top > 11 ? top - 11 : 0;
             for (int i = tid; i < EV_BINS; i += EV_THREADS) s.hist[i] = 0;
             __syncthreads();
             auto count = [&](float w) {  // of the unprotected [p_lo, p_hi)
-                const uint32_t k = order_key(w) - base;
+                const uint32_t k = rank_of(w) - base;
                 if (k <= width) atomicAdd(&s.hist[k >> shift], 1u);
             };
             // whole vectors between v_lo and v_hi, single entries before and behind
@@ -270,8 +272,10 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictParams
         const uint32_t er = e0 + __popc(be & below);
         if ((bg >> lane & 1) || ((be >> lane & 1) && er < need)) {
             const uint32_t at = g0 + __popc(bg & below) + min(er, need);
-            keep[at] = (int32_t)(lo + i + lane);
-            if (out) out[at] = w;
+            if (at < (uint32_t)n_keep) {  // (always, unless somebody writes the weights meanwhile)
+                keep[at] = (int32_t)(lo + i + lane);
+                if (out) out[at] = w;
+            }
         }
         g0 += __popc(bg);
         e0 += __popc(be);

@@ -461,6 +461,25 @@ def test_evict_select(lens, budget, sink, recent, kind):
             assert (got[b, :, m:max(lens)] == 0).all()
 
 
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, 0xFFC00000, 0xFFFFFFFF])
+@pytest.mark.parametrize("n,budget", [(700, 300), (40000, 20000)])
+def test_evict_select_with_nans(bits, n, budget):
+    """NaNs rank as numbers past +inf or -inf; the budget is kept exactly, nothing is written outside it."""
+    rng = np.random.default_rng(bits % 1000 + n)
+    acc = rng.random(n).astype(np.float32)
+    bad = np.flatnonzero(rng.random(n) < 0.3)
+    acc.view(np.uint32)[bad] = bits
+    t = torch.from_numpy(acc).view(1, 1, n).to(DEV)
+    keep = torch.full((1, 1, budget + 64), -9, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(1, dtype=torch.int32, device=DEV)
+    hsi.evict_select(t, torch.tensor([n], dtype=torch.int32, device=DEV), n, budget, keep, new_len, sink=3, recent=10)
+    assert hsi.device_error() == 0 and int(new_len) == budget
+    rank = acc.copy()
+    rank[bad] = np.inf if bits < 1 << 31 else -1.0
+    k = keep.cpu().numpy()[0, 0]
+    assert np.array_equal(k[:budget], _kept(rank, n, budget, 3, 10)) and (k[budget:] == -9).all()
+
+
 def test_evict_select_of_rows_past_the_shared_memory():
     n, budget = 500_000, 123_457
     rng = np.random.default_rng(3)
@@ -548,22 +567,42 @@ def test_compact_skips_what_is_wrong():
 
 # ------------------------------------------------------------------ refusals --
 
-def test_wait_that_runs_out_is_reported():
-    c = Case(37, [900, 500], [1, 1], 8, 2, 128, 16, BF)
-    out = torch.empty_like(c.q)
+# short form, line, chunk kernels; few entries for many rows (clusters share the weights' units)
+@pytest.mark.parametrize("kv_lens,q_lens", [([900, 500], [1, 1]), ([20000, 12000], [1, 1]), ([3000, 1000], [150, 90]),
+                                            ([300], [300])])
+def test_wait_that_runs_out_is_reported(kv_lens, q_lens):
+    """A copy that is never made: the waits for it end, the status says so, and the next calls are right."""
+    c = Case(37, kv_lens, q_lens, 8, 2, 128, 16, BF)
+    out, lse = torch.empty_like(c.q), torch.empty(c.T, 8, device=DEV)
+    acc = torch.zeros(c.B, 2, c.max_kv, device=DEV)
+
+    def attend():
+        hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.1, out, lse=lse)
+
+    def weights():
+        hsi.attention_weights(c.kv, c.q, lse, c.q_start, c.max_q, c.max_kv, 0.1, None, acc)
+
+    attend()
     assert hsi.device_error() == 0
-    try:
-        hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 20_000_000)
-        hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 1)
-        hsi.paged_attention(c.kv, c.q, c.q_start, 1, 900, 0.1, out)
-        assert hsi.device_error() == -4
-    finally:
-        hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 0)
-        hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
-    hsi.paged_attention(c.kv, c.q, c.q_start, 1, 900, 0.1, out)
+    for call in (attend, weights):
+        try:
+            hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 20_000_000)
+            hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 1)
+            call()
+            assert hsi.device_error() == -4
+        finally:
+            hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 0)
+            hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
+    attend()
+    weights()
     assert hsi.device_error() == 0
-    want, _, tol, _ = c.attention(0.1, True)
+    want, want_lse, tol, tol_lse = c.attention(0.1, True)
     within(out, want, tol, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    w, wt = c.weights(0.1, True, lse, 1.0, None)
+    for b, n in enumerate(kv_lens):
+        for g in range(2):
+            within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
 
 
 def test_refusals():
