@@ -23,7 +23,7 @@
 //
 // Measured (32 query and 8 KV heads of 128, bf16): one token over 16 sequences of
 // up to 65536 entries 475 to 497 us, 98 to 102% of the measured copy rate; over one
-// of 8000 entries 17 us (floor 5), the start, a tile's chain of 700 cycles and the
+// of 8000 entries 15 us (floor 5), the start, a tile's chain of 700 cycles and the
 // join; three short sequences of up to 777 entries (16 / 2 heads of 64) 7.1 us.
 #pragma once
 #include <cuda_bf16.h>
@@ -38,7 +38,7 @@ namespace hsi {
 
 constexpr int AT_ROWS = 16;      // rows of a unit
 constexpr int AT_KT = 64;        // entries of a tile
-constexpr int AT_CLUSTER = 16;   // most blocks of a short unit
+constexpr int AT_CLUSTER = 8;    // most blocks of a short unit
 constexpr int AT_WARPS = 4;      // consumer warps, 16 entries of a tile each
 constexpr int AT_THREADS = 32 * (AT_WARPS + 1);
 

@@ -168,18 +168,23 @@ int64_t attend_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int6
 // Workspace of the attention: the chunks' line, then the partial sums' slots.
 size_t attend_base_bytes(int32_t B) { return align_up(((size_t)B + 1) * 4, 256); }
 
-// Blocks of a unit in the short form (0: the line). A unit's tiles go to up to
-// sixteen blocks, AT_SHORT_TILES each at most: past that the line's finer cut is
-// quicker. All units at once, or the line evens them out better.
-#ifndef AT_SHORT_TILES
-#define AT_SHORT_TILES 12
-#endif
+// Blocks of a unit in the short form (0: the line): up to eight while all units'
+// blocks run at once, each with at most AT_SHORT_TILES tiles, as ragged lengths
+// leave the blocks uneven and the line does not. Units so few that twice the
+// blocks would still run at once leave SMs idle that the line would use: they
+// take it past AT_FEW_TILES. Measured, one token, 8 KV heads of 128, short
+// against line: 16 sequences of 1500 entries 21 and 27 us, four of 6000 22 and
+// 24; two of 1100 9.9 and 10.1, of 5100 17.3 and 15.4; one of 4600 15.1 and 11.8.
+// Clusters of sixteen: two of 1100 17.2 (they do not seem to run all at once),
+// one of 3000 11.7 against the line's 12.4.
+constexpr int AT_SHORT_TILES = 12, AT_FEW_TILES = 4;
 int attend_short(const AttendParams& p) {
     const int64_t rt = ((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS, units = rt * p.kv.H * p.kv.B;
     const int64_t tiles = (p.max_kv + AT_KT - 1) / AT_KT, room = 2 * (int64_t)sm_count();
     int csize = 1;
     while (csize < AT_CLUSTER && 2 * csize <= tiles && 2 * csize * units <= room) csize *= 2;
-    return csize * units <= room && tiles <= AT_SHORT_TILES * csize ? csize : 0;
+    const int most = 2 * csize * units <= room ? AT_FEW_TILES : AT_SHORT_TILES;
+    return csize * units <= room && tiles <= most * csize ? csize : 0;
 }
 
 template <typename T, int D, bool WEIGHTS>
@@ -190,17 +195,6 @@ hsi_status launch_attend_token(const AttendParams& p, const CUtensorMap& km, con
     if (smem_attr_once(attend_token_kernel<T, D, WEIGHTS>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
     const unsigned rt = (unsigned)(((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS);
     const int csize = WEIGHTS ? 0 : attend_short(p);
-    if (csize > 8) {  // more than the portable size
-        static std::atomic<bool> wide_set[kMaxDevices];
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return HSI_ERR_CUDA;
-        if (!wide_set[dev].load(std::memory_order_acquire)) {
-            if (cudaFuncSetAttribute(attend_token_kernel<T, D, WEIGHTS>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                     1) != cudaSuccess)
-                return HSI_ERR_CUDA;
-            wide_set[dev].store(true, std::memory_order_release);
-        }
-    }
     if (csize)
         return launch_cluster(attend_token_kernel<T, D, WEIGHTS>, dim3(rt * p.kv.H * p.kv.B * csize), dim3(AT_THREADS),
                               C::SMEM_BYTES, csize, s, p, km, vm, csize);
