@@ -170,10 +170,19 @@ def workspace_size(kind: int, B: int, max_n: int, k: int = 0) -> int:
     return int(lib().hsi_workspace_size(kind, B, max_n, k))
 
 
-def workspace(kind: int, B: int, max_n: int, k: int = 0, device="cuda") -> torch.Tensor | None:
-    """A caller-owned scratch buffer for one call (256-byte aligned by torch)."""
+def _scratch(n: int, device, stream=None, fill=torch.empty, dtype=torch.uint8) -> torch.Tensor:
+    """n values for a call on `stream` (None: the current one), made on it: memory of the current stream would be
+    handed out again there while kernels on `stream` still use it."""
+    if stream is None:
+        return fill(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return fill(n, dtype=dtype, device=device)
+
+
+def workspace(kind: int, B: int, max_n: int, k: int = 0, device="cuda", stream=None) -> torch.Tensor | None:
+    """A caller-owned scratch buffer for one call on `stream` (256-byte aligned by torch)."""
     n = workspace_size(kind, B, max_n, k)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return _scratch(n, device, stream) if n else None
 
 
 def kernel_launches() -> int:
@@ -199,13 +208,13 @@ def device_error(stream=None) -> int:
 
 
 def calib_read(buf: torch.Tensor, method: int = 0, chunk: int = 9216, stages: int = 12, sink=None, stream=None):
-    sink = torch.zeros(1, dtype=torch.int64, device=buf.device) if sink is None else sink
+    sink = _scratch(1, buf.device, stream, torch.zeros, torch.int64) if sink is None else sink
     _check("hsi_calib_read", lib().hsi_calib_read(_ptr(buf), buf.numel() * buf.element_size(), method, chunk,
                                                   stages, _ptr(sink), _stream(stream)))
 
 
 def calib_mma(n: int, iters: int, sink=None, device="cuda", stream=None):
-    sink = torch.zeros(1, dtype=torch.int64, device=device) if sink is None else sink
+    sink = _scratch(1, device, stream, torch.zeros, torch.int64) if sink is None else sink
     _check("hsi_calib_mma", lib().hsi_calib_mma(n, iters, _ptr(sink), _stream(stream)))
 
 
@@ -218,7 +227,7 @@ def quantize_nvfp4(x: torch.Tensor, n_tensors: int, rows_per_tensor: int, signs,
     """x: bf16 (or its int16 bits) [n_tensors*rows_per_tensor, 128] on the device."""
     s8 = (ctypes.c_int8 * 128)(*[int(v) for v in signs])
     if mode == 0 and ws is None:
-        ws = workspace(WS_QUANTIZE, n_tensors, 0, device=x.device)
+        ws = workspace(WS_QUANTIZE, n_tensors, 0, device=x.device, stream=stream)
     _check("hsi_quantize_nvfp4", lib().hsi_quantize_nvfp4(
         _ptr(x), n_tensors, rows_per_tensor, s8, mode, _ptr(g), _ptr(rec), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream)))
@@ -291,7 +300,7 @@ def topk(scores, n_valid, B, max_valid, k, out_idx, out_val, ld=None, block_ids=
          block_size=8, ws=None, stream=None):
     ld = scores.shape[-1] if ld is None else ld
     if ws is None:
-        ws = workspace(WS_TOPK, B, max_valid, k, device=scores.device)
+        ws = workspace(WS_TOPK, B, max_valid, k, device=scores.device, stream=stream)
     if block_ids is not None and not ld_blocks:
         ld_blocks = block_ids.shape[-1]
     _check("hsi_topk", lib().hsi_topk(
@@ -321,7 +330,7 @@ def candidate_pool(n_visible, B, max_visible, block_ids, n_kept, n_pool, scores=
         ld_bits = pool_bits.shape[-1]
     if ws is None:
         dev = (scores if scores is not None else block_max).device
-        ws = workspace(WS_POOL, B, max_visible, block_size, device=dev)
+        ws = workspace(WS_POOL, B, max_visible, block_size, device=dev, stream=stream)
     _check("hsi_candidate_pool", lib().hsi_candidate_pool(
         _ptr(scores), ld, _ptr(block_max), ldb, _ptr(n_visible), B, max_visible, block_size, n_keep,
         _ptr(block_ids), _ptr(n_kept), _ptr(n_pool), _ptr(pool_bits), ld_bits, _ptr(ws),
@@ -347,7 +356,7 @@ def full_layer(q_rec, g_q, w, k_rec, g_k, k_rec_off, n_visible, B, max_visible, 
     if pool_bits is not None and not ld_bits:
         ld_bits = pool_bits.shape[-1]
     if ws is None:
-        ws = workspace(WS_FULL_LAYER, B, max_visible, k, device=top_idx.device)
+        ws = workspace(WS_FULL_LAYER, B, max_visible, k, device=top_idx.device, stream=stream)
     _check("hsi_full_layer", lib().hsi_full_layer(
         _ptr(q_rec), _ptr(g_q), _ptr(w), _ptr(k_rec), _ptr(g_k), _ptr(k_rec_off), _ptr(n_visible), B, max_visible,
         _ptr(scores), ld, k, _ptr(top_idx), _ptr(top_val), n_keep, _ptr(block_ids), _ptr(n_kept), _ptr(n_pool),
@@ -364,7 +373,7 @@ def prefill_layer(q_rec, g_q, w, k_rec, g_k, k_rec_off, n_visible, B, max_visibl
     if pool_bits is not None and not ld_bits:
         ld_bits = pool_bits.shape[-1]
     if ws is None:
-        ws = workspace(WS_PREFILL_LAYER, B, max_visible, k, device=scores.device)
+        ws = workspace(WS_PREFILL_LAYER, B, max_visible, k, device=scores.device, stream=stream)
     _check("hsi_prefill_layer", lib().hsi_prefill_layer(
         _ptr(q_rec), _ptr(g_q), _ptr(w), _ptr(k_rec), _ptr(g_k), _ptr(k_rec_off), _ptr(n_visible), B, max_visible,
         group, _ptr(scores), ld, k, _ptr(top_idx), _ptr(top_val), n_keep, _ptr(block_ids), _ptr(n_kept),
@@ -389,7 +398,7 @@ def reindex_layer(q_rec, g_q, w, k_rec, g_k, k_rec_off, n_visible, block_ids, n_
     compacted pool left in pool_rec."""
     ld = pool_scores.shape[-1] if ld is None else ld
     if ws is None:
-        ws = workspace(WS_REINDEX_LAYER, B, 8 * n_keep, k, device=pool_scores.device)
+        ws = workspace(WS_REINDEX_LAYER, B, 8 * n_keep, k, device=pool_scores.device, stream=stream)
     _check("hsi_reindex_layer", lib().hsi_reindex_layer(
         _ptr(q_rec), _ptr(g_q), _ptr(w), _ptr(k_rec), _ptr(g_k), _ptr(k_rec_off), _ptr(pool_rec),
         1 if pool_rec_ready else 0, _ptr(n_visible),
@@ -530,10 +539,10 @@ def paged_append(kv: PagedKV, k_new, v_new, q_start, max_q=None, positions=None,
         _check("hsi_paged_append", st)
 
 
-def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int) -> torch.Tensor:
-    """A caller-owned scratch buffer for paged_attention."""
+def paged_attention_workspace(kv: PagedKV, q, max_q: int, max_kv: int, stream=None) -> torch.Tensor:
+    """A caller-owned scratch buffer for paged_attention on `stream`."""
     n = int(lib().hsi_paged_attention_ws(kv.B, kv.heads, q.shape[1], kv.dim, max_q, max_kv))
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    return _scratch(max(n, 1), q.device, stream)
 
 
 def paged_attention(kv: PagedKV, q, q_start, max_q: int, max_kv: int, scale: float, out, lse=None, causal: bool = True,
@@ -544,7 +553,7 @@ def paged_attention(kv: PagedKV, q, q_start, max_q: int, max_kv: int, scale: flo
     qp, qt, qh = _heads(q, "q", shape, kv.dtype)
     op, ot, oh = _heads(out, "out", shape, kv.dtype)
     if ws is None:
-        ws = paged_attention_workspace(kv, q, max_q, max_kv)
+        ws = paged_attention_workspace(kv, q, max_q, max_kv, stream)
     elif not ws.is_cuda:
         _bad("ws: on the GPU")
     st = (_lib or lib()).hsi_paged_attention(

@@ -1,0 +1,68 @@
+"""The paged-cache calls where they are easily wrong: NaN that comes in with the inputs, weights far below a row's
+largest, positions and counts near the ends of their ranges, views, streams, and every path of a move in place."""
+import math
+
+import pytest
+import torch
+
+from paged_cases import DEV, UNIT, Case, within
+
+import long_context_decode_lightning_gb300 as hsi
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    hsi.build()
+    hsi.device_check()
+    yield
+    assert hsi.device_error() == 0
+
+
+# -------------------------------------------------------------------- streams --
+
+class _Calls:
+    """In the library's place: takes every call, asks for a megabyte of scratch, and knows the addresses it was given."""
+
+    def __init__(self):
+        self.args = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name in ("hsi_workspace_size", "hsi_paged_attention_ws"):
+                return 1 << 20
+            self.args.append([a for a in args if isinstance(a, int)])
+            return 0
+        return call
+
+
+def test_scratch_that_a_call_makes_belongs_to_its_stream(monkeypatch):
+    """Without a workspace the wrappers make one and drop it at return, while its kernels may still wait: its memory
+    may go back to the given stream only, never to the current one."""
+    c = Case(61, [100], [1], 4, 2, 64, 16, BF)
+    out, lib, s = torch.empty_like(c.q), _Calls(), torch.cuda.Stream()
+    x, i = torch.zeros(64, 128, device=DEV), torch.zeros(64, 128, dtype=torch.int32, device=DEV)
+    monkeypatch.setattr(hsi, "_lib", lib)
+    calls = [
+        lambda: hsi.paged_attention(c.kv, c.q, c.q_start, 1, 100, 0.1, out, stream=s),
+        lambda: hsi.quantize_nvfp4(x, 1, 64, [1] * 128, x, x, stream=s),
+        lambda: hsi.topk(x, i, 64, 128, 8, i, x, stream=s),
+        lambda: hsi.candidate_pool(i, 64, 128, i, i, i, scores=x, stream=s),
+        lambda: hsi.full_layer(x, x, x, x, x, x, i, 64, 128, x, 8, i, x, stream=s),
+        lambda: hsi.prefill_layer(x, x, x, x, x, x, i, 64, 128, x, 8, i, x, stream=s),
+        lambda: hsi.reindex_layer(x, x, x, x, x, x, i, i, i, i, 64, x, 8, i, x, stream=s),
+        lambda: hsi.calib_read(x, stream=s),
+        lambda: hsi.calib_mma(128, 1, stream=s),
+    ]
+    mine = {t.data_ptr() for t in (x, i, out, c.q, c.q_start)}
+    for n, call in enumerate(calls):
+        lib.args.clear()
+        call()
+        segments = torch.cuda.memory_snapshot()
+        made = [(a, g["stream"]) for a in lib.args[0] if a not in mine for g in segments
+                if g["address"] <= a < g["address"] + g["total_size"]]
+        assert len(made) == 1 and made[0][1] == s.cuda_stream, f"call {n}: {made}"
