@@ -577,11 +577,13 @@ hsi_status hsi_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride
  * and [page][head][place] are strides). K and V may lie in one allocation.
  *  k, v    (dev) 16-byte aligned; strides multiples of 8 elements, at least dim.
  *  table   (dev) int32 [B][ld_table]; only the pages of entries below kv_len are read.
+ *  table_width pages that a row of the table lists, where that is less than
+ *          the rows' distance ld_table (a slice of a wider table); 0: ld_table.
  *  kv_len  (dev) int32 [B]: entries, the call's new tokens among them (a
  *          sequence's new tokens are its last entries).
  *  dim     64 or 128; page_size a power of two, 8 .. 4096; dtype BF16 or FP16
  *          (UNSUPPORTED otherwise).
- * A length outside [0, the call's bound], a page id outside [0, n_pages) or a
+ * A length outside [0, the call's bound or what the table's row lists], a page id outside [0, n_pages) or a
  * q_start that descends is clamped or skipped and reported as
  * HSI_ERR_DEVICE_ARG by hsi_device_error. What the pages hold past a
  * sequence's length never reaches a result, NaN included.
@@ -599,6 +601,7 @@ typedef struct {
     const int32_t* kv_len;
     int32_t B, heads, dim, page_size;
     hsi_dtype dtype;
+    int64_t table_width;
 } hsi_paged_kv;
 
 /*

@@ -48,7 +48,7 @@ class _PagedKV(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int64),
                 ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int)]
+                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int), ("table_width", ctypes.c_int64)]
 
 
 class HsiError(RuntimeError):
@@ -454,14 +454,17 @@ def _lse(t: torch.Tensor, shape) -> int:
     return t.data_ptr()
 
 
-def _acc(t: torch.Tensor, name: str, B: int, H: int):
-    """Address and row stride of fp32 [B, H, entries] with evenly spaced rows."""
+def _acc(t: torch.Tensor, name: str, B: int, H: int, fn: str, bound: int):
+    """Address and row stride of fp32 [B, H, entries] with evenly spaced rows of at least `bound` entries. The library
+    sees the rows' distance only, which in a slice of a wider tensor is more than what they hold."""
     shape, st = t.shape, t.stride()
     if t.dtype is not torch.float32 or len(shape) != 3 or shape[0] != B or shape[1] != H or st[2] != 1 or not t.is_cuda:
         _bad(f"{name}: fp32 [{B}, {H}, entries] on the GPU")
     ld = st[1] if H > 1 else (st[0] if B > 1 else shape[2])
     if B > 1 and st[0] != H * ld:
         _bad(f"{name}: rows must be evenly spaced")
+    if shape[2] < bound:
+        raise HsiError(fn, -1)
     return t.data_ptr(), ld
 
 
@@ -514,7 +517,7 @@ class PagedKV:
         self.dtype = k.dtype
         self.c = _PagedKV(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[0], _ptr(table),
                           _table(table, "table", self.B), _i32(kv_len, "kv_len", self.B), self.B, self.heads, self.dim,
-                          self.page_size, _dtype(k))
+                          self.page_size, _dtype(k), table.shape[1])
         self.ref = ctypes.byref(self.c)
 
 
@@ -569,8 +572,9 @@ def attention_weights(kv: PagedKV, q, lse, q_start, max_q: int, max_kv: int, sca
     its KV head. acc_in None: zeros; it may be acc_out."""
     T, Hq = q.shape[:2]
     qp, qt, qh = _heads(q, "q", (T, Hq, kv.dim), kv.dtype)
-    ip, il = (None, 0) if acc_in is None else _acc(acc_in, "acc_in", kv.B, kv.heads)
-    op, ol = _acc(acc_out, "acc_out", kv.B, kv.heads)
+    bound = min(max_kv, kv.c.table_width * kv.page_size)
+    ip, il = (None, 0) if acc_in is None else _acc(acc_in, "acc_in", kv.B, kv.heads, "hsi_attention_weights", bound)
+    op, ol = _acc(acc_out, "acc_out", kv.B, kv.heads, "hsi_attention_weights", bound)
     st = (_lib or lib()).hsi_attention_weights(
         kv.ref, qp, qt, qh, Hq, _lse(lse, (T, Hq)), _i32(q_start, "q_start", kv.B + 1), T, max_q, max_kv, scale, causal,
         decay, ip, il, op, ol, _raw_stream(stream))
@@ -582,8 +586,8 @@ def evict_select(acc, kv_len, max_len: int, budget: int, keep, new_len, sink: in
                  stream=None):
     """The entries a budget keeps, per sequence and KV head: keep int32 [B, heads, >= budget], new_len int32 [B]."""
     B, H = acc.shape[:2]
-    ap, al = _acc(acc, "acc", B, H)
-    op, ol = (None, 0) if acc_out is None else _acc(acc_out, "acc_out", B, H)
+    ap, al = _acc(acc, "acc", B, H, "hsi_evict_select", max_len)
+    op, ol = (None, 0) if acc_out is None else _acc(acc_out, "acc_out", B, H, "hsi_evict_select", budget)
     st = (_lib or lib()).hsi_evict_select(
         ap, al, _i32(kv_len, "kv_len", B), B, H, max_len, budget, sink, recent, _keep(keep, B, H), keep.shape[2],
         _i32(new_len, "new_len", B), op, ol, _raw_stream(stream))
@@ -596,8 +600,10 @@ def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, strea
     budget: bound of new_len (keep's width by default)."""
     dst = kv.table if dst_table is None else dst_table
     kp, places = _keep(keep, kv.B, kv.heads), keep.shape[2]
+    budget, ld = places if budget is None else budget, _table(dst, "dst_table", kv.B)
+    if dst.shape[1] * kv.page_size < budget:  # its rows' distance may be more than their width
+        raise HsiError("hsi_paged_compact", -1)
     st = (_lib or lib()).hsi_paged_compact(
-        kv.ref, kp, places, _i32(new_len, "new_len", kv.B), places if budget is None else budget, dst.data_ptr(),
-        _table(dst, "dst_table", kv.B), _raw_stream(stream))
+        kv.ref, kp, places, _i32(new_len, "new_len", kv.B), budget, dst.data_ptr(), ld, _raw_stream(stream))
     if st:
         _check("hsi_paged_compact", st)

@@ -94,7 +94,8 @@ hsi_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
 
 hsi_status paged_view(const hsi_paged_kv* c, PagedView* v) {
     if (!c || !c->k || !c->v || !c->table || !c->kv_len || c->B <= 0 || c->heads <= 0 || c->n_pages <= 0 ||
-        c->n_pages >= INT32_MAX || c->ld_table <= 0 || c->page_size <= 0)
+        c->n_pages >= INT32_MAX || c->ld_table <= 0 || c->page_size <= 0 || c->table_width < 0 ||
+        c->table_width > c->ld_table)
         return HSI_ERR_INVALID_ARG;
     if (c->dtype == HSI_FP32) return HSI_ERR_UNSUPPORTED;
     if (c->dtype != HSI_BF16 && c->dtype != HSI_FP16) return HSI_ERR_INVALID_ARG;
@@ -115,6 +116,7 @@ hsi_status paged_view(const hsi_paged_kv* c, PagedView* v) {
     v->n_pages = c->n_pages;
     v->table = c->table;
     v->ld_table = c->ld_table;
+    v->capacity = (c->table_width ? c->table_width : c->ld_table) * c->page_size;
     v->kv_len = c->kv_len;
     v->B = c->B;
     v->H = c->heads;
@@ -270,8 +272,7 @@ hsi_status attend_params(const hsi_paged_kv* cache, const void* q, int64_t qt, i
     if (!q_start || T <= 0 || T > INT32_MAX || max_q <= 0 || max_kv <= 0 || max_kv > INT32_MAX || q_heads <= 0 ||
         q_heads % cache->heads || !rows_ok(q, qt, qh) || !(scale == scale))
         return HSI_ERR_INVALID_ARG;
-    const int64_t most = cache->ld_table * cache->page_size;
-    p->max_kv = (int)(max_kv < most ? max_kv : most);
+    p->max_kv = (int)(max_kv < p->kv.capacity ? max_kv : p->kv.capacity);
     p->q = q;
     p->qt = qt;
     p->qh = qh;
@@ -550,6 +551,7 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     p.dst = dst_table;
     p.ld_dst = ld_dst;
     p.in_place = dst_table == cache->table;
+    if (p.in_place && budget > p.kv.capacity) return HSI_ERR_INVALID_ARG;
     // blocks of a (sequence, KV head, K or V): until every SM has sixteen (four at a time), none
     // without a turn's entries
     const int64_t rows = (int64_t)cache->B * cache->heads * 2, sms = sm_count();

@@ -66,3 +66,28 @@ def test_scratch_that_a_call_makes_belongs_to_its_stream(monkeypatch):
         made = [(a, g["stream"]) for a in lib.args[0] if a not in mine for g in segments
                 if g["address"] <= a < g["address"] + g["total_size"]]
         assert len(made) == 1 and made[0][1] == s.cuda_stream, f"call {n}: {made}"
+
+
+# --------------------------------------------------------------------- views --
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [1, 40]])
+def test_lengths_past_a_sliced_table(q_lens):
+    """What stands behind a slice of a wider table is not its own: a length that reaches there is clamped and reported."""
+    c = Case(63, [100, 90], q_lens, 4, 2, 64, 16, BF)
+    width = 6  # 96 entries; the columns behind name no page
+    kv = hsi.PagedKV(c.k, c.v, c.table[:, :width], c.kv_len)
+    out = torch.empty_like(c.q)
+    hsi.paged_attention(kv, c.q, c.q_start, c.max_q, c.max_kv, 0.1, out)
+    assert hsi.device_error() == -6
+    want, _, tol, _ = c.attention(0.1, True)
+    within(out[1:], want[1:], tol[1:], "the other sequence")
+    short = Case(63, [100, 90], q_lens, 4, 2, 64, 16, BF)
+    short.kv_lens[0], short.K[0], short.V[0] = 96, short.K[0][:96], short.V[0][:96]
+    want, _, tol, _ = short.attention(0.1, True)
+    within(out[:1], want[:1], tol[:1], "clamped")
+    k_new = torch.randn(c.T, 2, 64, device=DEV).to(BF)
+    hsi.paged_append(kv, k_new, k_new, c.q_start)
+    assert hsi.device_error() == -6
+    for i in range(q_lens[1]):
+        e = 90 - q_lens[1] + i
+        assert torch.equal(c.k[int(c.table[1, e // 16]), e % 16], k_new[1 + i])

@@ -1,0 +1,120 @@
+"""The paged-cache calls of the binding without a GPU: views that are narrower than a call's bounds, handles whose
+tensors change, and the arguments that reach the library (a recorder stands in its place)."""
+import types
+
+import pytest
+import torch
+
+import long_context_decode_lightning_gb300 as hsi
+
+
+class OnGpu(torch.Tensor):
+    """A tensor that says it lies on the GPU; nothing here reads one."""
+    is_cuda = True
+
+
+class Recorder:
+    """In the library's place: takes every call and keeps its arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+def gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def ints(*shape):
+    return gpu(*shape, dtype=torch.int32)
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(hsi, "_lib", r)
+    return r
+
+
+STREAM = types.SimpleNamespace(cuda_stream=0)
+B, H, PAGE, PAGES = 2, 2, 16, 4
+
+
+def cache(table=None):
+    k = gpu(8, PAGE, H, 64, dtype=torch.bfloat16)
+    return hsi.PagedKV(k, k, ints(B, PAGES) if table is None else table, ints(B))
+
+
+def weights(kv, acc_in, acc_out, max_kv):
+    q = gpu(B, 4, 64, dtype=torch.bfloat16)
+    hsi.attention_weights(kv, q, gpu(B, 4), ints(B + 1), 1, max_kv, 0.1, acc_in, acc_out, stream=STREAM)
+
+
+def select(acc, max_len, budget, acc_out=None):
+    hsi.evict_select(acc, ints(B), max_len, budget, ints(B, H, budget), ints(B), acc_out=acc_out, stream=STREAM)
+
+
+def refused(lib, call, *args):
+    with pytest.raises(hsi.HsiError) as e:
+        call(*args)
+    assert e.value.status == -1 and not lib.calls
+
+
+@pytest.mark.parametrize("cut", [slice(0, 40), slice(24, 64)])  # rows of 64, 40 of them in the view
+def test_views_narrower_than_a_bound_are_refused(lib, cut):
+    """Their rows stand 64 apart, but the places past the view's 40 are not the call's to read or write."""
+    wide, view, kv = gpu(B, H, 64), gpu(B, H, 64)[:, :, cut], cache()
+    refused(lib, weights, kv, None, view, 41)
+    refused(lib, weights, kv, view, wide, 64)
+    refused(lib, select, view, 41, 8)
+    refused(lib, select, wide, 64, 41, view)
+    refused(lib, select, view, 64, 8, view)
+    weights(kv, view, view, 40)
+    select(view, 40, 40, view)
+    assert [c[0] for c in lib.calls] == ["hsi_attention_weights", "hsi_evict_select"]
+    assert lib.calls[0][1][-2] == 64 and lib.calls[1][1][1] == 64  # the rows' distances
+
+
+def test_weights_need_no_more_than_the_table_holds(lib):
+    """A bound past the table is the table's: 64 entries."""
+    weights(cache(), None, gpu(B, H, 64), 1 << 20)
+    lib.calls.clear()
+    refused(lib, weights, cache(), None, gpu(B, H, 63), 1 << 20)
+
+
+def test_table_views_keep_their_width(lib):
+    """Rows of a sliced table stand further apart than the pages that they list."""
+    table = ints(B, 2 * PAGES)
+    kv = cache(table[:, :PAGES])
+    assert (kv.c.ld_table, kv.c.table_width) == (2 * PAGES, PAGES)
+    assert (cache().c.ld_table, cache().c.table_width) == (PAGES, PAGES)
+    keep = ints(B, H, PAGES * PAGE)
+    hsi.paged_compact(kv, keep, ints(B), table[:, PAGES:], stream=STREAM)
+    assert lib.calls.pop()[1][-2] == 2 * PAGES
+    refused(lib, lambda: hsi.paged_compact(kv, keep, ints(B), table[:, PAGES + 1:], stream=STREAM))
+    refused(lib, lambda: hsi.paged_compact(kv, ints(B, H, PAGES * PAGE + 1), ints(B), stream=STREAM))
+    weights(kv, None, gpu(B, H, PAGES * PAGE), 1 << 20)
+    lib.calls.clear()
+    refused(lib, weights, kv, None, gpu(B, H, PAGES * PAGE - 1), 1 << 20)
+
+
+def test_the_library_refuses_a_wrong_table_width():
+    """(validation fails before a pointer is used)"""
+    import ctypes
+    import shutil
+    if shutil.which("nvcc") is None:
+        pytest.skip("nvcc not on PATH")
+    hsi.build()
+    f = 1 << 20
+
+    def compact(width, ld=4, budget=32):
+        kv = hsi._PagedKV(f, 2 * f, 16 * 128, 128, 64, 10, f, ld, f, 2, 2, 64, 16, 0, width)
+        return hsi.lib().hsi_paged_compact(ctypes.byref(kv), f, 64, f, budget, f, ld, None)
+
+    assert compact(-1) == -1 and compact(5) == -1
+    assert compact(1) == -1  # in place: 32 places in one page of 16
