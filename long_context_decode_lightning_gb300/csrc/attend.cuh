@@ -141,6 +141,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// The factor that takes sums by the maximum mine (base 2) to those by the
+// maximum m >= mine of all parts. A part whose maximum is -inf has seen nothing
+// (sums of 0) or nothing but NaN (which a maximum passes over): its sums stay as
+// they are, so that the NaN come through.
+__device__ __forceinline__ float part_factor(float mine, float m) { return mine == -INFINITY ? 1.f : ex2(mine - m); }
+
 // --------------------------------------------------------------- the kernel --
 
 template <int D, bool WEIGHTS>
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
             for (int j = 0; j < 2; ++j) {
                 const int r = r_lo + 8 * j;
                 float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-                f[j] = m2[j] == -INFINITY ? 0.f : ex2(m2[j] - m);
+                f[j] = part_factor(m2[j], m);
             }
             const bool whole = !csize && tile0 == 0 && n_tiles == w.nt;
             float* slot = csize ? reinterpret_cast<float*>(stage0)  // every tile has been read
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
             float rl = 0.f;
 #pragma unroll
             for (int i = 0; i < AT_WARPS; ++i)
-                rl += s_m[i][orow] == -INFINITY ? 0.f : s_l[i][orow] * ex2(s_m[i][orow] - rm);
+                rl += s_l[i][orow] * part_factor(s_m[i][orow], rm);
             const int r = rt * AT_ROWS + orow;
             const int64_t tok = w.at + (r < rows ? r / p.group : 0);
             const int h = head * p.group + (r < rows ? r % p.group : 0);
@@ -578,24 +584,28 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
         for (int i = rank * AT_THREADS + threadIdx.x; i < AT_ROWS * (D / 4); i += csize * AT_THREADS) {
             const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = rt * AT_ROWS + row;
             if (r >= w.m * p.group) break;
-            float mc[AT_CLUSTER], m = -INFINITY, l = 0.f;
+            float mc[AT_CLUSTER], lc[AT_CLUSTER], m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int c = 0; c < AT_CLUSTER; ++c) {
                 mc[c] = -INFINITY;
-                if (c < csize) mc[c] = cluster_load(slot + AT_ROWS * D + row, c, csize);
+                lc[c] = 0.f;
+                if (c < csize) {
+                    mc[c] = cluster_load(slot + AT_ROWS * D + row, c, csize);
+                    lc[c] = cluster_load(slot + AT_ROWS * (D + 1) + row, c, csize);
+                }
                 m = fmaxf(m, mc[c]);
             }
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < AT_CLUSTER; ++c) {
-                if (mc[c] == -INFINITY) continue;  // a part without tiles has no sums
-                const float f = ex2(mc[c] - m);
+                if (lc[c] == 0.f) continue;  // a part without tiles has no sums
+                const float f = part_factor(mc[c], m);
                 const float4 v = cluster_load4(slot + row * D + d, c, csize);
                 o.x += f * v.x;
                 o.y += f * v.y;
                 o.z += f * v.z;
                 o.w += f * v.w;
-                l += f * cluster_load(slot + AT_ROWS * (D + 1) + row, c, csize);
+                l += f * lc[c];
             }
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const int64_t tok = w.at + r / p.group;
@@ -681,7 +691,7 @@ __global__ void __launch_bounds__(AT_JOIN_THREADS) attend_join_kernel(const __gr
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
 #pragma unroll
         for (int k = 0; k < AT_MAX_RUNS / 32; ++k) {
-            mc[k] = mc[k] == -INFINITY ? 0.f : ex2(mc[k] - m);
+            mc[k] = part_factor(mc[k], m);
             l += mc[k] * lc[k];
         }
 #pragma unroll

@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
             const int i = i0 + k;
             const float* slot = i ? rest + (int64_t)2 * i * SLOT : first;
             mc[k] = -INFINITY;
+            lc[k] = 0.f;
             if (i >= runs) continue;
             mc[k] = slot[2 * CH_ROWS * D + row];
             lc[k] = slot[2 * CH_ROWS * (D + 1) + row];
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
         float m_new = m;
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) m_new = fmaxf(m_new, mc[k]);
-        const float keep = m == -INFINITY ? 0.f : ex2(m - m_new);
+        const float keep = part_factor(m, m_new);
         m = m_new;
         l *= keep;
 #pragma unroll
@@ -670,8 +671,8 @@ __global__ void __launch_bounds__(2 * CH_ROWS)
         }
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
-            if (mc[k] == -INFINITY) continue;  // past the runs, or a part that this row does not see
-            const float f = ex2(mc[k] - m);
+            if (lc[k] == 0.f) continue;  // past the runs, or a part that this row does not see
+            const float f = part_factor(mc[k], m);
             l += f * lc[k];
 #pragma unroll
             for (int j = 0; j < V; ++j) {

@@ -91,3 +91,50 @@ def test_lengths_past_a_sliced_table(q_lens):
     for i in range(q_lens[1]):
         e = 90 - q_lens[1] + i
         assert torch.equal(c.k[int(c.table[1, e // 16]), e % 16], k_new[1 + i])
+
+
+# -------------------------------------------------------------------------- NaN --
+
+# a cluster a unit; the line with units cut and whole; one unit over many runs; chunks cut, whole and both
+NAN_SHAPES = [([700, 90], [1, 1], 8, 2), ([4000] * 3, [2, 1, 1], 8, 2), ([40 + i % 7 for i in range(300)], [1] * 300, 4, 2),
+              ([20000], [1], 4, 1), ([300, 200, 128], [150, 120, 100], 8, 4), ([20000], [40], 4, 1), ([128] * 40, [60] * 40, 8, 4),
+              ([1300], [700], 8, 8)]
+
+
+def _attend(c):
+    out, lse = torch.full_like(c.q, 5.0), torch.full((c.T, c.Hq), 5.0, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.1, out, lse=lse)
+    acc = torch.zeros(c.B, c.Hkv, c.max_kv, device=DEV)
+    hsi.attention_weights(c.kv, c.q, lse, c.q_start, c.max_q, c.max_kv, 0.1, None, acc)
+    assert hsi.device_error() == 0
+    return out, lse, acc
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kv_lens,q_lens,Hq,Hkv", NAN_SHAPES)
+def test_nan_query_gives_nan(dtype, kv_lens, q_lens, Hq, Hkv):
+    """A row whose every score is NaN is no row that sees nothing: out and lse are NaN, and so are its weights."""
+    c = Case(67, kv_lens, q_lens, Hq, Hkv, 64, 16, dtype)
+    was, was_lse, was_acc = _attend(c)
+    row, head, b = c.T - 1, Hq - 1, c.B - 1
+    c.q[row, head, 3] = math.nan
+    out, lse, acc = _attend(c)
+    assert bool(out[row, head].isnan().all()) and bool(lse[row, head].isnan())
+    assert bool(acc[b, Hkv - 1, :kv_lens[b]].isnan().all())
+    out[row, head], lse[row, head], acc[b, Hkv - 1] = was[row, head], was_lse[row, head], was_acc[b, Hkv - 1]
+    assert torch.equal(out, was) and torch.equal(lse, was_lse) and torch.equal(acc, was_acc)
+
+
+@pytest.mark.parametrize("kv_lens,q_lens,Hq,Hkv", NAN_SHAPES)
+def test_nan_key_reaches_the_rows_that_see_it(kv_lens, q_lens, Hq, Hkv):
+    """A NaN in the last sequence's last key: its last row's alone (causal), or, a few entries earlier, some rows'."""
+    c = Case(71, kv_lens, q_lens, Hq, Hkv, 64, 16, BF)
+    was, was_lse, _ = _attend(c)
+    n, m, group = kv_lens[-1], q_lens[-1], Hq // Hkv
+    rows = min(m, 3)  # the last `rows` tokens see entry n - rows
+    e = n - rows
+    c.k[int(c.table[-1, e // 16]), e % 16, Hkv - 1, 5] = math.nan
+    out, lse, _ = _attend(c)
+    assert bool(out[c.T - rows:, Hq - group:].isnan().all()) and bool(lse[c.T - rows:, Hq - group:].isnan().all())
+    out[c.T - rows:, Hq - group:], lse[c.T - rows:, Hq - group:] = was[c.T - rows:, Hq - group:], was_lse[c.T - rows:, Hq - group:]
+    assert torch.equal(out, was) and torch.equal(lse, was_lse)
