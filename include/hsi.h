@@ -628,7 +628,8 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
  *   out = sum_e p_e v_e / sum_e p_e,  p_e = exp(scale q.k_e),
  *   lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0).
  * The products run on the tensor cores with fp32 sums; p is rounded to the
- * cache's type for the second one.
+ * cache's type for the second one (in fp16 by no more than 2^-32 of a row's
+ * largest p where it falls below that type's normal numbers).
  *  q, out  (dev) [T][q_heads][dim] of the cache's type, strides in elements
  *          (multiples of 8, 16-byte aligned); distinct. v_e of an entry below
  *          kv_len must be finite for every new token of its sequence, also

@@ -18,8 +18,8 @@
 //
 // mma.sync suffices here: a 64-entry tile needs 128 of them in the ~1400
 // cycles its 32 KB take at the SM's share of HBM. P is rounded to the cache's
-// type for the second product (weights in [0, 1], error 2^-8 relative per term
-// in bf16, averaged by the sum); maxima, sums and the output stay in fp32.
+// type for the second product (error 2^-9 relative per term in bf16, averaged by
+// the sum; fp16: see P_SHIFT); maxima, sums and the output stay in fp32.
 //
 // Measured (32 query and 8 KV heads of 128, bf16): one token over 16 sequences of
 // up to 65536 entries 475 to 497 us, 98 to 102% of the measured copy rate; over one
@@ -140,6 +140,14 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// fp16 ends at 2^-24, where p of many entries far below a row's largest still
+// add up (a million of 2^-25 hold 3% of a row). So p is taken as 2^(x - m + 15),
+// up to half the largest fp16 number, and reaches 2^-39 of the largest; as the sums
+// have the same factor, it is a maximum m - 15 to all that follows. bf16 has
+// fp32's exponents.
+template <typename T>
+constexpr float P_SHIFT = is_bf16<T> ? 0.f : 15.f;
 
 // The factor that takes sums by the maximum mine (base 2) to those by the
 // maximum m >= mine of all parts. A part whose maximum is -inf has seen nothing
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                 }
                 float base[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) base[j] = m2[j] == -INFINITY ? 0.f : m2[j];
+                for (int j = 0; j < 2; ++j) base[j] = m2[j] == -INFINITY ? 0.f : m2[j] - P_SHIFT<T>;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -504,6 +512,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
             for (int j = 0; j < 2; ++j) {
                 l[j] += __shfl_xor_sync(~0u, l[j], 1);
                 l[j] += __shfl_xor_sync(~0u, l[j], 2);
+                m2[j] -= P_SHIFT<T>;  // what the sums are by
             }
             if ((lane & 3) == 0) {
                 s_m[warp][r_lo] = m2[0];

@@ -12,8 +12,8 @@
 // starts while the second half is still being exponentiated.
 //
 // The running maximum is lazy: O is rescaled only where a row's maximum has
-// grown by more than 2^8 since the last time (p stays below 256, exact enough
-// in either type), which after the first tiles hardly happens; the row sum
+// grown by more than 2^8 since the last time (p stays below 256, or 2^15 where
+// fp16 is shifted), which after the first tiles hardly happens; the row sum
 // is taken from the fp32 p in the shadow of the exponentials (the exponentials of
 // half a tile by the old maximum, before the new one is known, were no faster).
 //
@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     // block was launched with (8 x 216 + 4 x 72 = 12 x 168).
     if (warp < 8) {  // softmax, a thread per row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        constexpr float SHIFT = P_SHIFT<T> ? P_SHIFT<T> - CH_LAZY : 0.f;  // p up to 2^CH_LAZY of its own
         int kvn = 0, seg = 0, it = 0;
         const int w = warp >> 2, row = threadIdx.x & 127;
         for (; ok && k.begin(p, tpt); k.advance(p, tpt)) {
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     }
                     m_used = m_new;
                 }
-                const float base = m_used == -INFINITY ? 0.f : m_used;
+                const float base = m_used == -INFINITY ? 0.f : m_used - SHIFT;
                 const uint64_t sl2 = f2_pack(p.sl2, p.sl2), nb = f2_pack(-base, -base);
                 if (w == 0 && k0 + CH_KEYS > k.q.len) {
                     // entries past the length hold whatever the page holds (or nothing was loaded):
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 l += (a + e) + (c2 + d2);
             }
             ok = ok && __all_sync(~0u, wait_bounded(&s.o_full[w], seg & 1, &s.abort));
+            m_used -= SHIFT;  // what the sums are by
             if (ok) {
                 tc_fence_after();
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;

@@ -138,3 +138,50 @@ def test_nan_key_reaches_the_rows_that_see_it(kv_lens, q_lens, Hq, Hkv):
     assert bool(out[c.T - rows:, Hq - group:].isnan().all()) and bool(lse[c.T - rows:, Hq - group:].isnan().all())
     out[c.T - rows:, Hq - group:], lse[c.T - rows:, Hq - group:] = was[c.T - rows:, Hq - group:], was_lse[c.T - rows:, Hq - group:]
     assert torch.equal(out, was) and torch.equal(lse, was_lse)
+
+
+# --------------------------------------------------------------- small weights --
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n,m", [(131072, 1), (5000, 1), (1000, 1), (131072, 30), (5000, 100)])
+def test_many_small_weights_are_not_lost(dtype, n, m):
+    """One entry of weight 1 and value 0, all others of weight 2^-25.1 and value 1: the output is what the small ones
+    hold together. p is rounded to the cache's type, relative to itself (u) and, in fp16, by no more than half the
+    smallest fp16 number, 2^-25, where the row's largest p stands at 2^7 at least; the result is rounded once more."""
+    D = 64
+    c = Case(73, [n], [m], 2, 1, D, 64, dtype)
+    c.q.zero_()
+    c.q[..., 0] = 4.0
+    live = c.table[0, :-(-n // 64)].long()
+    c.k[live] = 0.0
+    c.v[live] = 1.0
+    c.k[live[0], 0, 0, 0] = 25.1 * math.log(2.0) / 4.0
+    c.v[live[0], 0] = 0.0
+    top = 4.0 * float(c.k[live[0], 0, 0, 0])
+    out, lse = torch.empty_like(c.q), torch.empty(c.T, 2, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, m, n, 1.0, out, lse=lse)
+    assert hsi.device_error() == 0
+    seen = torch.arange(n - m + 1, n + 1, device=DEV, dtype=torch.float64)
+    small = (seen - 1) * math.exp(-top)
+    want = (small / (1 + small))[:, None, None].expand(m, 2, D)
+    # the exponent, 25 in base 2, and ex2: below 2^-16 of a p; fp16: 2^-25 * 2^-7 absolute each
+    tol = want * (2 * UNIT[dtype] + 2.0 ** -16) + (n * 2.0 ** -32 if dtype == HF else 0.0)
+    within(out, want, tol, "out")
+    within(lse, (top + torch.log1p(small))[:, None].expand(m, 2), torch.full_like(want[..., 0], 2.0 ** -16), "lse")
+
+
+@pytest.mark.parametrize("kv_lens,q_lens", [([900, 300], [1, 1]), ([30000], [2]), ([700, 400], [300, 90]), ([9000], [30])])
+def test_fp16_values_as_large_as_the_type(kv_lens, q_lens):
+    """Equal scores over values near the largest fp16 number: sums are fp32, the result is an average."""
+    c = Case(79, kv_lens, q_lens, 4, 2, 64, 16, HF)
+    c.q.zero_()
+    for v in c.V:
+        v.copy_(torch.where(v > 0, 60000.0, 65504.0).to(HF))
+    for b, n in enumerate(kv_lens):
+        for i in range(-(-n // 16)):
+            rows = c.V[b][i * 16:(i + 1) * 16]
+            c.v[int(c.table[b, i]), :rows.shape[0]] = rows
+    out = torch.empty_like(c.q)
+    hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.1, out)
+    want, _, tol, _ = c.attention(0.1, True)
+    within(out, want, tol, "out")
