@@ -247,8 +247,9 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 // columns [c_lo, rows) count; tiles where all do need no comparison
-                const int rows = min(rpt, (w.m - j * tpt) * p.group);
-                const int c_lo = (t_min - j * tpt) * p.group;
+                // (in tokens of the tile first: entries times heads may pass 31 bits)
+                const int rows = min(tpt, w.m - j * tpt) * p.group;
+                const int c_lo = min(max(t_min - j * tpt, 0), tpt) * p.group;
                 const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + kt * 128 + 127 - past);
                 uint64_t add[4] = {0, 0, 0, 0};
                 auto columns = [&](auto masked) {

@@ -185,3 +185,31 @@ def test_fp16_values_as_large_as_the_type(kv_lens, q_lens):
     hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, 0.1, out)
     want, _, tol, _ = c.attention(0.1, True)
     within(out, want, tol, "out")
+
+
+# ------------------------------------------------------------ far and many entries --
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_weights_past_31_bits_of_rows_times_entries(causal):
+    """64 query heads of one KV head over 33.6 million entries (one page, listed again and again): entries times heads
+    pass 2^31, and every entry's weight is that of its place in the page."""
+    D, page, n, Hq = 64, 4096, 33_600_003, 64
+    g = torch.Generator(device=DEV).manual_seed(83)
+    k = torch.randn(1, page, 1, D, generator=g, device=DEV).to(BF)
+    table = torch.zeros(1, -(-n // page), dtype=torch.int32, device=DEV)
+    kv = hsi.PagedKV(k, k, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+    q = torch.randn(1, Hq, D, generator=g, device=DEV).to(BF)
+    lse = torch.rand(1, Hq, generator=g, device=DEV) + 3.0
+    acc = torch.full((1, 1, n), -1.0, device=DEV)
+    hsi.attention_weights(kv, q, lse, torch.tensor([0, 1], dtype=torch.int32, device=DEV), 1, n, 0.125, None, acc, causal=causal)
+    assert hsi.device_error() == 0
+    Q, K = q[0].double(), k[0, :, 0].double()
+    p = torch.exp(Q @ K.T * 0.125 - lse[0].double()[:, None])
+    # p off by the score's error (D products in fp32) and the rounding of its exponent in base 2; the sum by 2^-22
+    E = Q.abs() @ K.abs().T * 0.125 * (D * 2.0 ** -23 + 2.0 ** -22) + lse[0].double()[:, None] * 2.0 ** -22 + 2.0 ** -20
+    want, tol = p.sum(0), (p * E).sum(0) + p.sum(0) * 2.0 ** -22
+    whole = n // page * page
+    rows = acc[0, 0, :whole].view(-1, page)
+    assert bool((rows == rows[0]).all())
+    within(rows[0], want, tol, "weights")
+    assert torch.equal(acc[0, 0, whole:], rows[0, :n - whole])
