@@ -638,7 +638,9 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
  *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
  *  lse     (dev) fp32 [T][q_heads], may be NULL.
  *  ws      (dev) hsi_paged_attention_ws(...) bytes.
- * Errors: INVALID_ARG, UNSUPPORTED (the cache's dims), WORKSPACE.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (the cache's dims; bounds at which
+ * the tiles of work pass 2^31: 256 entries by 128 / group tokens, times heads and
+ * B, for chunks, 64 entries by 16 rows for up to 16 rows of a KV head).
  */
 size_t hsi_paged_attention_ws(int32_t B, int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t max_q, int64_t max_kv);
 hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -283,10 +283,16 @@ hsi_status attend_params(const hsi_paged_kv* cache, const void* q, int64_t qt, i
     p->group = q_heads / cache->heads;
     p->sl2 = scale * LOG2E;
     p->causal = causal != 0;
-    // tiles are counted in 31 bits
-    const int64_t units = ((int64_t)p->max_q * p->group + AT_ROWS - 1) / AT_ROWS * cache->heads;
-    if (units > INT32_MAX || units * cache->B > INT32_MAX / ((p->max_kv + AT_KT - 1) / AT_KT)) return HSI_ERR_UNSUPPORTED;
+    // the kernels count entries, rounded up to whole tiles, and a KV head's rows in 31 bits
+    if (p->max_kv > INT32_MAX - 4096 || (int64_t)p->max_q * p->group > INT32_MAX - 4096) return HSI_ERR_UNSUPPORTED;
     return HSI_OK;
+}
+
+// Whether the tiles of a kernel's line, `keys` entries each of B x heads x row_tiles units, can be counted in 31 bits
+// (at the host's bounds, as the lengths are the device's). No factor is above 2^31 and heads, B are below 2^16.
+bool line_ok(int64_t row_tiles, int64_t heads, int64_t B, int64_t max_kv, int64_t keys) {
+    const int64_t units = row_tiles * heads;
+    return units <= INT32_MAX && units * B <= INT32_MAX / ((max_kv + keys - 1) / keys);
 }
 
 }  // namespace
@@ -430,6 +436,10 @@ hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t
     if (!rows_ok(out, o_token_stride, o_head_stride) || out == q || (T > 1 && o_token_stride < cache->dim) ||
         (q_heads > 1 && o_head_stride < cache->dim))
         return HSI_ERR_INVALID_ARG;
+    const bool chunk = chunk_rows(p);
+    const int64_t tile = chunk ? 2 * (CH_ROWS / p.group) : AT_ROWS, rows = chunk ? p.max_q : p.max_q * p.group;
+    if (!line_ok((rows + tile - 1) / tile, cache->heads, cache->B, p.max_kv, chunk ? CH_KEYS : AT_KT))
+        return HSI_ERR_UNSUPPORTED;
     const size_t need = hsi_paged_attention_ws(cache->B, cache->heads, q_heads, cache->dim, p.max_q, p.max_kv);
     if (!ws || ws_bytes < need || !aligned(ws, 256)) return HSI_ERR_WORKSPACE;
     p.out = out;
@@ -439,7 +449,7 @@ hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t
     p.base = static_cast<uint32_t*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attend_base_bytes(cache->B));
     CUtensorMap km, vm;
-    if (chunk_rows(p)) {
+    if (chunk) {
         const int tpt = CH_ROWS / p.group;
         CUtensorMap qm;
         if ((st = paged_map(*cache, p.kv, cache->k, CH_KEYS, &km)) != HSI_OK) return st;
@@ -474,6 +484,9 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
     if (st != HSI_OK) return st;
     if (!lse || !acc_out || ld_acc_out < p.max_kv || (acc_in && ld_acc_in < p.max_kv) || !(decay == decay))
         return HSI_ERR_INVALID_ARG;
+    const bool chunk = chunk_rows(p);
+    // a unit takes every row; the chunk kernel counts the units of all sequences in 64 bits
+    if (!line_ok(1, cache->heads, chunk ? 1 : cache->B, p.max_kv, chunk ? WC_KEYS : AT_KT)) return HSI_ERR_UNSUPPORTED;
     p.lse_in = lse;
     p.acc_in = acc_in;
     p.acc_out = acc_out;
@@ -481,7 +494,7 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
     p.ld_acc_out = ld_acc_out;
     p.decay = decay;
     CUtensorMap km;
-    if (chunk_rows(p)) {
+    if (chunk) {
         const int tpt = WC_ROWS / p.group;
         CUtensorMap qm;
         if ((st = paged_map(*cache, p.kv, cache->k, 128, &km)) != HSI_OK) return st;

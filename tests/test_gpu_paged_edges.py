@@ -213,3 +213,22 @@ def test_weights_past_31_bits_of_rows_times_entries(causal):
     assert bool((rows == rows[0]).all())
     within(rows[0], want, tol, "weights")
     assert torch.equal(acc[0, 0, whole:], rows[0, :n - whole])
+
+
+def test_wide_bounds_of_a_mixed_batch():
+    """A chunk of 2048 tokens, single tokens and none in one call, under a bound of a million entries a sequence."""
+    page, D, lens, new = 64, 64, [2300, 40, 700] + [100] * 29, [2048, 1, 0] + [1] * 29
+    c = Case(101, lens, new, 32, 8, D, page, BF, table_pad=(1 << 20) // page)
+    out, lse = torch.empty_like(c.q), torch.empty(c.T, 32, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, 2048, 1 << 20, 0.125, out, lse=lse)
+    acc = torch.zeros(c.B, 8, 1 << 20, device=DEV)
+    hsi.attention_weights(c.kv, c.q, lse, c.q_start, 2048, 1 << 20, 0.125, None, acc)
+    assert hsi.device_error() == 0
+    want, want_lse, tol, tol_lse = c.attention(0.125, True)
+    within(out, want, tol, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    w, wt = c.weights(0.125, True, lse, 1.0, None)
+    for b, n in enumerate(lens):
+        assert not bool(acc[b, :, n:].any())
+        for g in range(0, 8, 5):
+            within(acc[b, g, :n], w[b][g], wt[b][g], "weights")

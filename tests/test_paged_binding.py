@@ -118,3 +118,29 @@ def test_the_library_refuses_a_wrong_table_width():
 
     assert compact(-1) == -1 and compact(5) == -1
     assert compact(1) == -1  # in place: 32 places in one page of 16
+
+
+def test_wide_bounds_of_mixed_batches():
+    """Bounds of a batch in which one sequence brings a chunk and one may hold a million entries: what the kernels can
+    count is not refused (validation goes on to the scratch, or to the lse, that is missing here), what they cannot is."""
+    import ctypes
+    import shutil
+    if shutil.which("nvcc") is None:
+        pytest.skip("nvcc not on PATH")
+    hsi.build()
+    L, f = hsi.lib(), 1 << 20
+
+    def status(B, heads, q_heads, max_q, max_kv, T, token_stride=64 * 1024, fn="attention"):
+        kv = hsi._PagedKV(f, 2 * f, 64 * 64 * 8, 512, 64, 1 << 20, f, 1 << 26, f, B, heads, 64, 64, 0)
+        args = (ctypes.byref(kv), f, token_stride, 64, q_heads)
+        if fn == "attention":
+            return L.hsi_paged_attention(*args, f, T, max_q, max_kv, 0.1, 1, 4 * f, 64 * 1024, 64, None, None, 0, None)
+        return L.hsi_attention_weights(*args, None, f, T, max_q, max_kv, 0.1, 1, 1.0, None, 0, f, max_kv, None)
+
+    for fn, passed in (("attention", -5), ("weights", -1)):
+        assert status(32, 8, 32, 2048, 1 << 20, 4096, fn=fn) == passed
+        assert status(256, 8, 32, 2048, 1 << 17, 4096, fn=fn) == passed
+        assert status(256, 8, 32, 1, 1 << 20, 256, fn=fn) == passed
+        assert status(1, 8, 32, 1, (1 << 31) - 1, 1, fn=fn) == -2  # entries rounded up to tiles would pass 2^31
+        assert status(1, 1, 64, 1 << 26, 64, 1 << 26, token_stride=0, fn=fn) == -2  # 2^32 rows of a KV head
+    assert status(65535, 8, 32, 1 << 20, 1 << 20, 1 << 20) == -2
