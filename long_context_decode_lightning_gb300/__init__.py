@@ -504,7 +504,8 @@ def rope(x, positions, steps, out, rot_offset: int = 0, interleaved: bool = Fals
 class PagedKV:
     """A paged cache for the calls below: k, v [pages, page size, heads, dim] (any strides with contiguous
     dims, the same for both; a [pages, heads, page size, dim] cache is passed transposed), table int32
-    [B, pages a sequence], kv_len int32 [B] on the device. Keeps the tensors; their contents may change."""
+    [B, pages a sequence], kv_len int32 [B] on the device. Keeps the tensors; their contents may change, and
+    table and kv_len may be set to others of as many sequences."""
 
     def __init__(self, k, v, table, kv_len):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride() != k.stride() or \
@@ -512,13 +513,42 @@ class PagedKV:
             _bad("k, v: [pages, page size, heads, dim] on the GPU, the same strides, dims contiguous")
         if table.dim() != 2:
             _bad("table: int32 [sequences, pages]")
-        self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
+        self._k, self._v = k, v
         self.B, self.heads, self.dim, self.page_size = table.shape[0], k.shape[2], k.shape[3], k.shape[1]
         self.dtype = k.dtype
-        self.c = _PagedKV(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[0], _ptr(table),
-                          _table(table, "table", self.B), _i32(kv_len, "kv_len", self.B), self.B, self.heads, self.dim,
-                          self.page_size, _dtype(k), table.shape[1])
+        self.c = _PagedKV(k=_ptr(k), v=_ptr(v), page_stride=k.stride(0), token_stride=k.stride(1),
+                          head_stride=k.stride(2), n_pages=k.shape[0], B=self.B, heads=self.heads, dim=self.dim,
+                          page_size=self.page_size, dtype=_dtype(k))
+        self.table, self.kv_len = table, kv_len
         self.ref = ctypes.byref(self.c)
+
+    # The library has the addresses, so what is kept here and what it reads change together.
+
+    @property
+    def k(self):
+        return self._k
+
+    @property
+    def v(self):
+        return self._v
+
+    @property
+    def table(self):
+        return self._table
+
+    @table.setter
+    def table(self, t):
+        ld = _table(t, "table", self.B)
+        self._table, self.c.table, self.c.ld_table, self.c.table_width = t, t.data_ptr(), ld, t.shape[1]
+
+    @property
+    def kv_len(self):
+        return self._kv_len
+
+    @kv_len.setter
+    def kv_len(self, t):
+        self.c.kv_len = _i32(t, "kv_len", self.B)
+        self._kv_len = t
 
 
 def paged_append(kv: PagedKV, k_new, v_new, q_start, max_q=None, positions=None, steps=None, rot_offset: int = 0,

@@ -232,3 +232,33 @@ def test_wide_bounds_of_a_mixed_batch():
         assert not bool(acc[b, :, n:].any())
         for g in range(0, 8, 5):
             within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
+
+
+# -------------------------------------------------------------- moved caches --
+
+def test_attention_after_a_move_to_other_pages():
+    """The kept entries on their new pages, under their new table and lengths, and a second move, in place there."""
+    lens, budget, page, D = [500, 300], 200, 16, 64
+    need = -(-budget // page)
+    c = Case(103, lens, [1, 1], 4, 2, D, page, BF, spare=2 * need)
+    used = set(c.table[(c.table >= 0) & (c.table < c.k.shape[0])].tolist())
+    free = [p for p in range(c.k.shape[0]) if p not in used]
+    dst = torch.tensor(free[:2 * need], dtype=torch.int32, device=DEV).view(2, need)
+    for move, n in ((dst, budget), (None, 90)):
+        acc = torch.rand(2, 2, max(c.kv_lens), device=DEV)
+        keep = torch.empty(2, 2, n, dtype=torch.int32, device=DEV)
+        new_len = torch.empty(2, dtype=torch.int32, device=DEV)
+        hsi.evict_select(acc, c.kv.kv_len, max(c.kv_lens), n, keep, new_len, recent=1)
+        hsi.paged_compact(c.kv, keep, new_len, move)
+        if move is not None:
+            c.kv.table = move
+        c.kv.kv_len = new_len
+        c.kv_lens = [n, n]
+        for x in (c.K, c.V):
+            for b in range(2):
+                x[b] = torch.stack([x[b][keep[b, g].long(), g] for g in range(2)], 1)
+        out = torch.empty_like(c.q)
+        hsi.paged_attention(c.kv, c.q, c.q_start, 1, n, 0.125, out)
+        assert hsi.device_error() == 0
+        want, _, tol, _ = c.attention(0.125, True)
+        within(out, want, tol, "out")

@@ -144,3 +144,24 @@ def test_wide_bounds_of_mixed_batches():
         assert status(1, 8, 32, 1, (1 << 31) - 1, 1, fn=fn) == -2  # entries rounded up to tiles would pass 2^31
         assert status(1, 1, 64, 1 << 26, 64, 1 << 26, token_stride=0, fn=fn) == -2  # 2^32 rows of a KV head
     assert status(65535, 8, 32, 1 << 20, 1 << 20, 1 << 20) == -2
+
+
+def test_a_cache_follows_its_tensors(lib):
+    """After a move to other pages the caller sets table and kv_len: the library sees the new ones, and a move in place
+    is one of the library's own table."""
+    kv, dst, new_len = cache(), ints(B, PAGES + 1), ints(B)
+    kv.table, kv.kv_len = dst, new_len
+    assert (kv.c.table, kv.c.ld_table, kv.c.table_width) == (dst.data_ptr(), PAGES + 1, PAGES + 1)
+    assert kv.c.kv_len == new_len.data_ptr() and kv.table is dst and kv.kv_len is new_len
+    hsi.paged_compact(kv, ints(B, H, 8), ints(B), stream=STREAM)
+    assert lib.calls[0][1][-3] == kv.c.table
+    for wrong in (ints(B + 1, PAGES), ints(PAGES), gpu(B, PAGES), torch.zeros(B, PAGES, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            kv.table = wrong
+    for wrong in (ints(B + 1), ints(B, 1), torch.zeros(B, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            kv.kv_len = wrong
+    assert kv.table is dst and kv.kv_len is new_len and kv.c.table == dst.data_ptr()
+    for name in ("k", "v"):
+        with pytest.raises(AttributeError):
+            setattr(kv, name, gpu(8, PAGE, H, 64, dtype=torch.bfloat16))
