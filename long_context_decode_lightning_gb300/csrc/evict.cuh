@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(CP_THREADS, AHEAD ? 2 : 4)
     } else {
         for (int i0 = 0; i0 < n; i0 += step) {  // the same turns in every block of a cluster
             uint4 v[ROUNDS];
-            uint8_t* to[ROUNDS];
+            int to_page[ROUNDS];  // below 0: nothing to copy (a page takes one register where an address takes two)
             int src[ROUNDS];
 #pragma unroll
             for (int u = 0; u < ROUNDS; ++u) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(CP_THREADS, AHEAD ? 2 : 4)
 #pragma unroll
             for (int u = 0; u < ROUNDS; ++u) {
                 const int i = i0 + (part * ROUNDS + u) * rows + row;
-                to[u] = nullptr;
+                to_page[u] = -1;
                 if (src[u] == -2) continue;
                 if (src[u] < 0 || src[u] >= len) {
                     raise_error(DEVERR_ARG);
@@ -402,15 +402,18 @@ __global__ void __launch_bounds__(CP_THREADS, AHEAD ? 2 : 4)
                 }
                 const int64_t from = a * p.kv.page_stride + (src[u] & mask) * p.kv.token_stride;
                 v[u] = *reinterpret_cast<const uint4*>(base + 2 * from);
-                to[u] = base + 2 * (d * p.kv.page_stride + (i & mask) * p.kv.token_stride);
+                to_page[u] = d;
             }
             if (p.in_place) {  // a turn's reads precede its writes
                 if (csize > 1) cluster_sync();
                 else __syncthreads();
             }
 #pragma unroll
-            for (int u = 0; u < ROUNDS; ++u)
-                if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
+            for (int u = 0; u < ROUNDS; ++u) {
+                const int i = i0 + (part * ROUNDS + u) * rows + row;
+                if (to_page[u] >= 0)
+                    *reinterpret_cast<uint4*>(base + 2 * (to_page[u] * p.kv.page_stride + (i & mask) * p.kv.token_stride)) = v[u];
+            }
         }
     }
 }

@@ -49,20 +49,21 @@ struct PagedView {
     int64_t page_stride, token_stride, head_stride;  // elements
     int64_t n_pages;
     const int32_t* table;
-    int64_t ld_table, capacity;  // distance of the table's rows, entries that one lists
+    int64_t ld_table;  // distance of the table's rows
     const int32_t* kv_len;
     int B, H, D, page_shift;
+    int capacity;      // entries that a row of the table lists
 };
 
 constexpr int64_t PAGED_NO_ENTRY = -1, PAGED_NO_TOKEN = -2;
 
 // Entries of sequence b, clamped to what its table row can hold and to the host's bound.
-__device__ __forceinline__ int32_t paged_len(const PagedView& kv, int b, int64_t bound = INT32_MAX) {
+__device__ __forceinline__ int32_t paged_len(const PagedView& kv, int b, int32_t bound = INT32_MAX) {
     const int32_t n = __ldg(kv.kv_len + b);
-    const int64_t most = min(kv.capacity, bound);
+    const int32_t most = min(kv.capacity, bound);
     if (n < 0 || n > most) {
         raise_error(DEVERR_ARG);
-        return n < 0 ? 0 : (int32_t)most;
+        return n < 0 ? 0 : most;
     }
     return n;
 }

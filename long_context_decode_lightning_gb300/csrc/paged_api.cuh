@@ -116,7 +116,8 @@ hsi_status paged_view(const hsi_paged_kv* c, PagedView* v) {
     v->n_pages = c->n_pages;
     v->table = c->table;
     v->ld_table = c->ld_table;
-    v->capacity = (c->table_width ? c->table_width : c->ld_table) * c->page_size;
+    const int64_t width = c->table_width ? c->table_width : c->ld_table, most = INT32_MAX / c->page_size;
+    v->capacity = width > most ? INT32_MAX : (int)(width * c->page_size);  // lengths are 32-bit
     v->kv_len = c->kv_len;
     v->B = c->B;
     v->H = c->heads;
