@@ -654,7 +654,8 @@ hsi_status hsi_paged_attention(const hsi_paged_kv* cache, const void* q, int64_t
  *                      of exp(scale q.k_e - lse[row])        (e < kv_len[b])
  * with the lse that hsi_paged_attention wrote for the same arguments. Entries
  * at or past kv_len[b] are left untouched. fp32 sums in a fixed order.
- *  acc_in  (dev) fp32 [B][heads][ld_acc_in], may be NULL (zeros) or acc_out;
+ *  acc_in  (dev) fp32 [B][heads][ld_acc_in], may be NULL (zeros) or acc_out (the
+ *          same ld then: INVALID_ARG otherwise);
  *  acc_out (dev) fp32 [B][heads][ld_acc_out]; both ld at least the entries' bound.
  */
 hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -673,9 +674,10 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
  *  new_len (dev) out int32 [B]: min(kv_len[b], budget). Distinct from kv_len.
  *  acc_out (dev, may be NULL) fp32 [B][heads][ld_out]: the kept entries' acc in
  *          the order of keep, zeros up to `budget`. It may be acc itself (up to
- *          393216 entries, UNSUPPORTED beyond): then zeros up to max_len; it
- *          must not overlap acc otherwise.
- * Errors: INVALID_ARG (sink + recent > budget among them).
+ *          393216 entries, UNSUPPORTED beyond; ld_out = ld_acc): then zeros up to
+ *          max_len; it must not overlap acc otherwise.
+ * Errors: INVALID_ARG (sink + recent > budget, new_len = kv_len, acc_out = acc
+ * with another ld among them).
  */
 hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_len, int32_t B, int32_t heads,
                             int64_t max_len, int32_t budget, int32_t sink, int32_t recent, int32_t* keep,
@@ -684,8 +686,10 @@ hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_
 /*
  * Moves the kept entries to the front: entry keep[b][g][i] of KV head g becomes
  * entry i < new_len[b] of the table dst_table (dev, int32 [B][ld_dst]).
- * dst_table is cache->table itself (in place) or lists pages that no table row
- * of the cache lists. The cache's kv_len still holds the old lengths; the
+ * dst_table is cache->table itself (in place, ld_dst = ld_table: INVALID_ARG
+ * otherwise) or lists pages that no table row of the cache lists. No two places
+ * may be one: in place, sequences that share a page (a common prefix) overwrite
+ * each other's entries. The cache's kv_len still holds the old lengths; the
  * caller sets it to new_len (and table to dst_table) afterwards.
  * keep must ascend, as hsi_evict_select writes it.
  */

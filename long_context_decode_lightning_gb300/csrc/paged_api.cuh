@@ -485,6 +485,8 @@ hsi_status hsi_attention_weights(const hsi_paged_kv* cache, const void* q, int64
     if (st != HSI_OK) return st;
     if (!lse || !acc_out || ld_acc_out < p.max_kv || (acc_in && ld_acc_in < p.max_kv) || !(decay == decay))
         return HSI_ERR_INVALID_ARG;
+    // in place with other rows' distances, a row's results would lie on another row's inputs
+    if (acc_in == acc_out && ld_acc_in != ld_acc_out && (int64_t)cache->B * cache->heads > 1) return HSI_ERR_INVALID_ARG;
     const bool chunk = chunk_rows(p);
     // a unit takes every row; the chunk kernel counts the units of all sequences in 64 bits
     if (!line_ok(1, cache->heads, chunk ? 1 : cache->B, p.max_kv, chunk ? WC_KEYS : AT_KT)) return HSI_ERR_UNSUPPORTED;
@@ -528,6 +530,8 @@ hsi_status hsi_evict_select(const float* acc, int64_t ld_acc, const int32_t* kv_
     // past the clusters' shared memory, weights are read while others are written
     if (acc_out == acc && (max_len + csize - 1) / csize > EV_CAP) return HSI_ERR_UNSUPPORTED;
     if ((int64_t)B * heads * csize > INT32_MAX) return HSI_ERR_UNSUPPORTED;
+    // what a row's blocks write, other rows' blocks may not have read yet
+    if (new_len == kv_len || (acc_out == acc && ld_out != ld_acc && (int64_t)B * heads > 1)) return HSI_ERR_INVALID_ARG;
     EvictParams p{};
     p.acc = acc;
     p.ld_acc = ld_acc;
@@ -565,7 +569,7 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     p.dst = dst_table;
     p.ld_dst = ld_dst;
     p.in_place = dst_table == cache->table;
-    if (p.in_place && budget > p.kv.capacity) return HSI_ERR_INVALID_ARG;
+    if (p.in_place && (budget > p.kv.capacity || (ld_dst != cache->ld_table && cache->B > 1))) return HSI_ERR_INVALID_ARG;
     // blocks of a (sequence, KV head, K or V): until every SM has sixteen (four at a time), none
     // without a turn's entries
     const int64_t rows = (int64_t)cache->B * cache->heads * 2, sms = sm_count();

@@ -165,3 +165,27 @@ def test_a_cache_follows_its_tensors(lib):
     for name in ("k", "v"):
         with pytest.raises(AttributeError):
             setattr(kv, name, gpu(8, PAGE, H, 64, dtype=torch.bfloat16))
+
+
+def test_in_place_needs_the_same_rows():
+    """The same buffer read and written at other rows' distances, and lengths written over the lengths that are read:
+    the host sees both. (A single row has no distance.)"""
+    import ctypes
+    import shutil
+    if shutil.which("nvcc") is None:
+        pytest.skip("nvcc not on PATH")
+    hsi.build()
+    L, f = hsi.lib(), 1 << 20
+
+    def select(new_len=2 * f, acc_out=f, ld_out=100, B=2, heads=1):
+        return L.hsi_evict_select(f, 100, f, B, heads, 100, 50, 0, 0, f, 50, new_len, acc_out, ld_out, None)
+
+    assert select(new_len=f) == -1 and select(new_len=f, acc_out=None) == -1
+    assert select(ld_out=120) == -1 and select(ld_out=50) == -1 and select(ld_out=50, B=1, heads=2) == -1
+    kv = hsi._PagedKV(f, 2 * f, 16 * 128, 128, 64, 10, f, 4, f, 2, 2, 64, 16, 0)
+
+    def weights(la, lo):
+        return L.hsi_attention_weights(ctypes.byref(kv), f, 256, 64, 4, f, f, 3, 3, 60, 0.1, 1, 1.0, f, la, f, lo, None)
+
+    assert weights(60, 61) == -1 and weights(100, 60) == -1
+    assert L.hsi_paged_compact(ctypes.byref(kv), f, 32, f, 32, f, 5, None) == -1
