@@ -584,7 +584,7 @@ hsi_status hsi_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride
  *  dim     64 or 128; page_size a power of two, 8 .. 4096; dtype BF16 or FP16
  *          (UNSUPPORTED otherwise).
  * A length outside [0, the call's bound or what the table's row lists], a page id outside [0, n_pages) or a
- * q_start that descends is clamped or skipped and reported as
+ * q_start that descends or leaves [0, T] is clamped or skipped and reported as
  * HSI_ERR_DEVICE_ARG by hsi_device_error. What the pages hold past a
  * sequence's length never reaches a result, NaN included.
  *
@@ -612,7 +612,8 @@ typedef struct {
  * tokens' query heads, rotated into q_out (may be q).
  *  k_new, v_new (dev) [T][heads][dim], q, q_out [T][q_heads][dim] with strides
  *          in elements, 16-byte aligned, multiples of 8.
- * Tokens outside every sequence are left alone.
+ * Tokens outside every sequence are left alone, as are (reported) those around
+ * which q_start descends and those of a sequence that leaves [0, T].
  */
 hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_t k_token_stride, int64_t k_head_stride,
                             const void* v_new, int64_t v_token_stride, int64_t v_head_stride, const int32_t* q_start,

@@ -79,19 +79,34 @@ __device__ __forceinline__ int32_t paged_new(const int32_t* q_start, int b, int3
     return e - a;
 }
 
-// Element offset (head 0) of the place of new token t: entry kv_len - (new
-// tokens of its sequence) + its index among them. PAGED_NO_TOKEN where t lies
-// outside every sequence, PAGED_NO_ENTRY (reported) where it has no valid place.
-// Whole warp; the sequence is the number of those that end at or before t, so
-// that its lookup is one round of loads (for up to 32 sequences) and no chain.
-__device__ __forceinline__ int64_t paged_new_row_warp(const PagedView& kv, const int32_t* q_start, int64_t t) {
+// Element offset (head 0) of the place of new token t of `total`: entry kv_len -
+// (new tokens of its sequence) + its index among them. PAGED_NO_TOKEN where t
+// lies outside every sequence, PAGED_NO_ENTRY (reported) where it has no valid
+// place. Whole warp; the sequence is the number of those that end at or before
+// t, so that its lookup is one round of loads (for up to 32 sequences) and no
+// chain. Those are the first ones, or q_start descends around t: reported then,
+// as where the sequence leaves the tokens, and t belongs to none.
+__device__ __forceinline__ int64_t paged_new_row_warp(const PagedView& kv, const int32_t* q_start, int64_t t,
+                                                      int64_t total) {
     const int lane = threadIdx.x & 31;
-    int b = 0;
+    int b = 0, last = 0;
 #pragma unroll 4
-    for (int i = lane; i < kv.B; i += 32) b += __ldg(q_start + i + 1) <= t;
+    for (int i = lane; i < kv.B; i += 32) {
+        if (__ldg(q_start + i + 1) > t) continue;
+        ++b;
+        last = i + 1;
+    }
     b = __reduce_add_sync(~0u, b);
+    if (__reduce_max_sync(~0u, last) != b) {
+        raise_error(DEVERR_ARG);
+        return PAGED_NO_TOKEN;
+    }
     if (b >= kv.B || t < __ldg(q_start + b)) return PAGED_NO_TOKEN;
     const int32_t a = __ldg(q_start + b), e1 = __ldg(q_start + b + 1);
+    if (a < 0 || e1 > total) {
+        raise_error(DEVERR_ARG);
+        return PAGED_NO_TOKEN;
+    }
     const int32_t n = paged_len(kv, b);
     const int64_t e = (int64_t)n - (e1 - a) + (t - a);
     if (e < 0 || e >= n) {

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, APPEND_CTAS) paged_append_kernel
             }
             if (first) {
                 for (int j = threadIdx.x >> 5; j < nt; j += ROPE_THREADS / 32) {
-                    const int64_t row = paged_new_row_warp(p.kv, p.q_start, t0 + j);
+                    const int64_t row = paged_new_row_warp(p.kv, p.q_start, t0 + j, p.T);
                     if ((threadIdx.x & 31) == 0) s_row[j] = row;
                 }
                 for (int j = threadIdx.x; j < nt * half; j += ROPE_THREADS)

@@ -234,6 +234,40 @@ def test_wide_bounds_of_a_mixed_batch():
             within(acc[b, g, :n], w[b][g], wt[b][g], "weights")
 
 
+# --------------------------------------------------------------------- q_start --
+
+@pytest.mark.parametrize("start", [[0, 4, 2, 6], [-1, 2, 4, 6], [0, 2, 4, 7], [6, 4, 2, 0]])
+@pytest.mark.parametrize("more", [0, 37])  # up to 32 sequences a warp's lanes look at once
+def test_append_reports_a_wrong_q_start(start, more):
+    """A q_start that descends or leaves the call's tokens is reported; tokens of two sequences or of one that leaves the
+    call's are left alone, the others written where the call's other users look for them."""
+    lens, T = [20, 30, 10] + [5] * more, 6
+    c = Case(89, lens, [2, 2, 2] + [0] * more, 2, 1, 64, 8, BF)
+    k = torch.randn(T, 1, 64, device=DEV).to(BF)
+    want = c.k.clone(), c.v.clone()
+    start = start + [start[-1]] * more
+    steps, gain = hsi.rope_steps(64)
+    q, q_out = c.q[:T].clone(), torch.full((T, 2, 64), 7.0, dtype=BF, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    k_rot, q_rot, want_q = torch.empty_like(k), torch.empty_like(q), q_out.clone()
+    hsi.rope(k, pos, steps, k_rot, gain=gain)
+    hsi.rope(q, pos, steps, q_rot, gain=gain)
+    for t in range(T):
+        owners = [b for b in range(3) if 0 <= start[b] <= t < start[b + 1] <= T]
+        if len(owners) != 1:
+            continue
+        b = owners[0]
+        e = lens[b] - start[b + 1] + t
+        page, at = int(c.table[b, e // 8]), e % 8
+        want[0][page, at], want[1][page, at], want_q[t] = k_rot[t], k[t], q_rot[t]
+    hsi.paged_append(c.kv, k, k, torch.tensor(start, dtype=torch.int32, device=DEV), positions=pos, steps=steps, gain=gain,
+                     q=q, q_out=q_out)
+    assert hsi.device_error() == -6
+    for now, w in zip((c.k, c.v), want):
+        assert torch.equal(now.view(torch.int16), w.view(torch.int16))
+    assert torch.equal(q_out, want_q)
+
+
 # -------------------------------------------------------------- moved caches --
 
 def test_attention_after_a_move_to_other_pages():
