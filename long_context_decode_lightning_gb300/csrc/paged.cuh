@@ -107,9 +107,11 @@ __device__ __forceinline__ int64_t paged_new_row_warp(const PagedView& kv, const
         raise_error(DEVERR_ARG);
         return PAGED_NO_TOKEN;
     }
-    const int32_t n = paged_len(kv, b);
-    const int64_t e = (int64_t)n - (e1 - a) + (t - a);
-    if (e < 0 || e >= n) {
+    // (by the length as it is: by one clamped to the row, the tokens would land on the entries before them)
+    const int32_t n = __ldg(kv.kv_len + b);
+    const int64_t e = (int64_t)n - (e1 - t);
+    if (n > kv.capacity) raise_error(DEVERR_ARG);
+    if (e < 0 || e >= kv.capacity) {
         raise_error(DEVERR_ARG);
         return PAGED_NO_ENTRY;
     }

@@ -268,6 +268,24 @@ def test_append_reports_a_wrong_q_start(start, more):
     assert torch.equal(q_out, want_q)
 
 
+@pytest.mark.parametrize("n_extra", [0, 1])
+def test_append_past_a_sequence_s_pages(n_extra):
+    """A length past what the table's row lists: tokens that still have a place go there, the others nowhere (not onto
+    the entries that end the row), and it is reported."""
+    c = Case(91, [32, 20], [3, 1], 2, 1, 64, 8, BF, table_pad=0)  # rows of four pages, 32 entries
+    c.kv_len[0] = 32 + n_extra
+    k = torch.randn(4, 1, 64, device=DEV).to(BF)
+    want = c.k.clone()
+    for i in range(3):
+        e = 32 + n_extra - 3 + i
+        if e < 32:
+            want[int(c.table[0, e // 8]), e % 8] = k[i]
+    want[int(c.table[1, 2]), 3] = k[3]
+    hsi.paged_append(c.kv, k, k, c.q_start)
+    assert hsi.device_error() == (-6 if n_extra else 0)
+    assert torch.equal(c.k.view(torch.int16), want.view(torch.int16))
+
+
 # -------------------------------------------------------------- moved caches --
 
 def test_attention_after_a_move_to_other_pages():
