@@ -397,7 +397,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
             if (WEIGHTS && acc_in && lane < 16 && e0 + AT_KT + mine < w.len) next = acc_in[e0 + AT_KT + mine];
             float add[4] = {};  // weights of entries kq, kq + 1, 8 + kq, 9 + kq
             for (int rr = WEIGHTS ? 0 : rt; ok && rr < rt_end; ++rr) {
-                if (WEIGHTS && rt_end > 1) load_rows(rr);
+                if (WEIGHTS && rt_end > 1) {
+                    load_rows(rr);
+                    __syncwarp();
+                }
                 float s[2][4] = {};
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                 s_l[warp][r_lo] = l[0];
                 s_l[warp][r_lo + 8] = l[1];
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            bar_sync(1, 32 * AT_WARPS);
             float f[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                     *reinterpret_cast<float2*>(mine + r_lo * 32 + d * 8 + kq) = make_float2(v[0] * f[0], v[1] * f[0]);
                     *reinterpret_cast<float2*>(mine + (r_lo + 8) * 32 + d * 8 + kq) = make_float2(v[2] * f[1], v[3] * f[1]);
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                bar_sync(1, 32 * AT_WARPS);
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < AT_WARPS; ++i) {
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttendCfg<D, WEIGHTS>::CTAS)
                     uint2 v = make_uint2(pack2<T>(sum.x * inv, sum.y * inv), pack2<T>(sum.z * inv, sum.w * inv));
                     *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.ot + h * p.oh + c * 32 + od) = v;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                bar_sync(1, 32 * AT_WARPS);
             }
             if ((threadIdx.x & 7) == 0) {
                 if (!whole) {

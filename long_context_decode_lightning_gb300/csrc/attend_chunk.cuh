@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                                                   (e0 + idx / (D / 8)) * 128 + (idx & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
+                    __syncwarp();
                 }
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -411,11 +412,15 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 float* slot = p.part + (2 * (int64_t)blockIdx.x + (k.tile0 > 0 ? 0 : 1)) * chunk_slot_floats(D);
                 T* out = static_cast<T*>(p.out) + (int64_t)(k.q.at + tok) * p.ot + (int64_t)h * p.oh;
+                uint32_t all[D / 32][32];  // whole warps load, before some lanes store
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) tmem_ld32_issue(to + c * 32, all[c]);
+                tmem_ld_wait(all[0]);
+#pragma unroll
+                for (int c = 1; c < D / 32; ++c) tmem_ld_waited(all[c]);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32_issue(to + c * 32, o);
-                    tmem_ld_wait(o);
+                    const uint32_t(&o)[32] = all[c];
                     if (!k.whole) {  // four dims of 32 rows lie side by side; rows that hold nothing are not read
                         if (valid)
 #pragma unroll

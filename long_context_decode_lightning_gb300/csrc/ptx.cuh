@@ -103,9 +103,17 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// The .aligned barriers want a warp's lanes at them together, which code that
+// some lanes skipped (a store, a loop of another length) does not bring about.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Named barrier `id` (1 .. 15) of `threads` threads, whole warps.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // A 32-bit word of another CTA of the cluster, at the address it has in this one.
 __device__ __forceinline__ uint32_t dsmem_load(const uint32_t* mine, uint32_t rank) {

@@ -248,9 +248,13 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                 tc_fence_after();
                 // columns [c_lo, rows) count; tiles where all do need no comparison
                 // (in tokens of the tile first: entries times heads may pass 31 bits)
-                const int rows = min(tpt, w.m - j * tpt) * p.group;
-                const int c_lo = min(max(t_min - j * tpt, 0), tpt) * p.group;
-                const bool whole = rows == rpt && (!p.causal || j * tpt >= k0 + kt * 128 + 127 - past);
+                const int t0 = j * tpt;
+                const bool whole = w.m - t0 >= tpt && (!p.causal || t0 >= k0 + kt * 128 + 127 - past);
+                int rows = rpt, c_lo = 0;
+                if (!whole) {
+                    rows = min(tpt, w.m - t0) * p.group;
+                    c_lo = min(max(t_min - t0, 0), tpt) * p.group;
+                }
                 uint64_t add[4] = {0, 0, 0, 0};
                 auto columns = [&](auto masked) {
                     uint32_t r[2][32];
@@ -299,10 +303,10 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
             // the two warpgroups' sums, then the ranks'
             float* part = &s.part[kt][tid];
             if (par == 1) *part = total;
-            asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");
+            bar_sync(1 + kt, 256);
             if (par == 0) total += *part;
             if (csize > 1) {
-                asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");
+                bar_sync(1 + kt, 256);
                 if (par == 0) *part = total;
                 cluster_sync();
                 if (rank == 0 && par == 0) {
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
                         total += __uint_as_float(dsmem_load(reinterpret_cast<const uint32_t*>(part), r));
                 }
             } else {
-                asm volatile("bar.sync %0, 256;" ::"r"(1 + kt) : "memory");  // read, before the next unit's
+                bar_sync(1 + kt, 256);  // read, before the next unit's
             }
             if (rank == 0 && par == 0 && key < w.len && ok) {
                 const int64_t at = (int64_t)w.b * p.kv.H + head;
@@ -320,7 +324,6 @@ __global__ void __launch_bounds__(WC_THREADS, 1)
             }
         }
         if (csize > 1) {
-            __syncwarp();
             if (warp >= 16) cluster_sync();
             cluster_sync();  // the sums have been read
         }
