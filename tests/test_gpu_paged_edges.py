@@ -314,3 +314,55 @@ def test_attention_after_a_move_to_other_pages():
         assert hsi.device_error() == 0
         want, _, tol, _ = c.attention(0.125, True)
         within(out, want, tol, "out")
+
+
+# ------------------------------------------------- paths that nothing else takes --
+
+@pytest.mark.parametrize("page,D,layout", [(16, 64, "NHD"), (64, 128, "HND")])
+def test_compact_in_place_of_a_batch(page, D, layout):
+    """Eight sequences of eight heads: blocks for every SM, clusters of eight and more than one turn, in place."""
+    lens, budget, H = [6000, 5991, 5003, 4000, 3999, 17, 0, 5555], 4000, 8
+    c = Case(97, lens, [0] * 8, H, H, D, page, BF, layout)
+    acc = torch.rand(8, H, max(lens), device=DEV)
+    keep = torch.empty(8, H, budget, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(8, dtype=torch.int32, device=DEV)
+    hsi.evict_select(acc, c.kv_len, max(lens), budget, keep, new_len, sink=4, recent=100)
+    want = [c.k.clone(), c.v.clone()]
+    for pages, src in zip(want, (c.K, c.V)):
+        for b, n in enumerate(new_len.tolist()):
+            i = torch.arange(n, device=DEV)
+            for h in range(H):
+                pages[c.table[b, i // page].long(), i % page, h] = src[b][keep[b, h, :n].long(), h]
+    hsi.paged_compact(c.kv, keep, new_len)
+    assert hsi.device_error() == 0
+    for pages, w in zip((c.k, c.v), want):
+        assert torch.equal(pages.contiguous().view(torch.int16), w.contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scale", [1.0, 0.1, -0.4, 0.0])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [90, 300, 17]])
+def test_weights_of_large_scores_at_every_scale(dtype, scale, q_lens):
+    """Weights under scores of hundreds, negative and zero scales. p = exp(x) with x off by E: p off by p (e^E - 1)."""
+    c = Case(17, [1000, 800, 70], q_lens, 8, 2, 128, 32, dtype, q_scale=30.0)
+    out, lse = torch.empty_like(c.q), torch.empty(c.T, 8, device=DEV)
+    hsi.paged_attention(c.kv, c.q, c.q_start, c.max_q, c.max_kv, scale, out, lse=lse)
+    want_out, want_lse, tol_out, tol_lse = c.attention(scale, True)
+    within(out, want_out, tol_out, "out")
+    within(lse, want_lse, tol_lse, "lse")
+    old = torch.rand(3, 2, 1000, device=DEV)
+    acc = old.clone()
+    hsi.attention_weights(c.kv, c.q, lse, c.q_start, c.max_q, c.max_kv, scale, acc, acc, decay=0.5)
+    assert hsi.device_error() == 0
+    at = 0
+    for b, (n, m) in enumerate(zip(c.kv_lens, c.q_lens)):
+        for g in range(2):
+            want = 0.5 * old[b, g, :n].double()
+            tol = want * 2.0 ** -22
+            for h in range(4 * g, 4 * g + 4):
+                Q, K, L = c.q[at:at + m, h].double(), c.K[b][:, g].double(), lse[at:at + m, h].double()[:, None]
+                p = torch.where(c.rows(b, True), torch.exp(Q @ K.T * scale - L), 0.0)
+                E = Q.abs() @ K.abs().T * abs(scale) * (128 * 2.0 ** -23 + 2.0 ** -22) + L.abs() * 2.0 ** -22 + 2.0 ** -20
+                want, tol = want + p.sum(0), tol + (p * (torch.expm1(E) + 2.0 ** -22)).sum(0)
+            within(acc[b, g, :n], want, tol, f"weights {b} {g}")
+        at += m
