@@ -382,7 +382,7 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
         p.r = {reinterpret_cast<const unsigned long long*>(steps), positions, rot, rot_offset, interleaved != 0, gain, 1.f};
     }
     if (q) {
-        if (!steps || q_heads <= 0 || !rows_ok(q, q_token_stride, q_head_stride) ||
+        if (!steps || q_heads <= 0 || (int64_t)q_heads * cache->dim > INT32_MAX || !rows_ok(q, q_token_stride, q_head_stride) ||
             !rows_ok(q_out, o_token_stride, o_head_stride))
             return HSI_ERR_INVALID_ARG;
         if (q == q_out && (q_token_stride != o_token_stride || q_head_stride != o_head_stride)) return HSI_ERR_INVALID_ARG;
@@ -562,6 +562,8 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
     if (!keep || !new_len || !dst_table || budget <= 0 || ld_keep < budget || ld_dst <= 0 ||
         ld_dst * cache->page_size < budget)
         return HSI_ERR_INVALID_ARG;
+    // places are counted in 31 bits up to a turn of all blocks past the budget (256 of up to 16 blocks an SM)
+    if (budget > INT32_MAX - (1 << 20)) return HSI_ERR_UNSUPPORTED;
     p.keep = keep;
     p.ld_keep = ld_keep;
     p.new_len = new_len;

@@ -189,3 +189,19 @@ def test_in_place_needs_the_same_rows():
 
     assert weights(60, 61) == -1 and weights(100, 60) == -1
     assert L.hsi_paged_compact(ctypes.byref(kv), f, 32, f, 32, f, 5, None) == -1
+
+
+def test_sizes_that_32_bits_cannot_count():
+    """Places up to a turn past the budget, and a token's vectors, pass 2^31: refused before a pointer is used."""
+    import ctypes
+    import shutil
+    if shutil.which("nvcc") is None:
+        pytest.skip("nvcc not on PATH")
+    hsi.build()
+    L, f, most = hsi.lib(), 1 << 20, (1 << 31) - 1
+    kv = ctypes.byref(hsi._PagedKV(f, 2 * f, 4096 * 128, 128, 64, 10, f, 1 << 20, f, 2, 2, 64, 4096, 0))
+    for dst, ld in ((f, 1 << 20), (2 * f, 1 << 19)):
+        assert L.hsi_paged_compact(kv, f, most, f, most, dst, ld, None) == -2
+    heads = (1 << 25) + 1
+    assert L.hsi_paged_append(kv, f, 128, 64, f, 128, 64, f, 1, f, f, 64, 0, 0, 1.0, f, 64 * heads, 64, heads, 2 * f,
+                              64 * heads, 64, None) == -1
