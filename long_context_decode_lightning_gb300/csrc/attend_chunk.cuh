@@ -369,10 +369,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     ok = __all_sync(~0u, wait_bounded(&s.kv_full[st], (kvn + 2 * i + 1) / C::KV_STAGES & 1, &s.abort));
                     if (!ok) break;
                     const int e0 = k.q.len - k0;
-                    for (int idx = row; idx < (CH_KEYS - e0) * (D / 8); idx += 128)
+                    for (int i0 = 0; i0 < (CH_KEYS - e0) * (D / 8); i0 += 128) {
+                        const int idx = i0 + row;
+                        if (idx >= (CH_KEYS - e0) * (D / 8)) continue;
                         *reinterpret_cast<uint4*>(kv_ring + st * C::TILE_BYTES + (idx / 8 % (D / 64)) * C::HALF_BYTES +
                                                   (e0 + idx / (D / 8)) * 128 + (idx & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
