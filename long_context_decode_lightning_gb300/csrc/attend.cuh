@@ -22,8 +22,8 @@
 // the sum; fp16: see P_SHIFT); maxima, sums and the output stay in fp32.
 //
 // Measured (32 query and 8 KV heads of 128, bf16): one token over 16 sequences of
-// up to 65536 entries 475 to 497 us, 98 to 102% of the measured copy rate; over one
-// of 8000 entries 15 us (floor 5), the start, a tile's chain of 700 cycles and the
+// up to 65536 entries 475 to 500 us, 97 to 102% of the measured copy rate; over one
+// of 8000 entries 13 us (floor 5), the start, a tile's chain of 700 cycles and the
 // join; three short sequences of up to 777 entries (16 / 2 heads of 64) 7.1 us.
 #pragma once
 #include <cuda_bf16.h>

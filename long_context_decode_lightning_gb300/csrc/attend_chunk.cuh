@@ -22,8 +22,9 @@
 // a unit that spans runs is joined by a second kernel from fp32 partial sums.
 //
 // Measured (32 query and 8 KV heads of 128, bf16): 2048 tokens over 32768 entries
-// 735 us alone, 1450 TFLOP/s or 75% of the measured burst rate, and 780 us back to
-// back under the power limit, 80% of the sustained rate. A pair of tiles takes 3300
+// 735 us alone, 1450 TFLOP/s or 75% of the measured burst rate, and 780 to 800 us back
+// to back under the power limit, 80% of the sustained rate; heads of 64 600 us, half
+// the products for the same exponentials. A pair of tiles takes 3300
 // cycles, 2200 of products: the rest is the chain of a tile's S, softmax and P V
 // (1250 cycles from S to P) and the issuing warp's waits. Short units add 8000
 // cycles of start and end each: four chunks of up to 1001 tokens over 5003 entries

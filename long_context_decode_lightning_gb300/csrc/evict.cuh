@@ -24,8 +24,9 @@
 // Bound: HBM, one read and one write of the kept entries.
 //
 // Measured: 8 sequences of 16384 entries, 8 KV heads of 128, back to 8192: selection
-// 18 us (load 8000 cycles, passes 4000 each, counting and writing 4000 each), copy to
-// other pages 86 us (92% of the copy rate), in place 114 us.
+// 17 to 19 us (load 8000 cycles, passes 4000 each, counting and writing 4000 each), copy
+// to other pages 85 us (93% of the copy rate), in place 109 us. Selection in clusters, 8
+// heads of one sequence: 131072 entries 39 us, 500000 (past the shared memory) 87.
 #pragma once
 #include <cstdint>
 
@@ -304,11 +305,11 @@ constexpr int CP_THREADS = 256;
 // gridDim.x / (2 B H) (to other pages) share its places, ROUNDS times the
 // entries that 16-byte loads of CP_THREADS threads cover at a time: eight
 // rounds in flight a thread, or two where that leaves SMs without blocks (512
-// places of two sequences: 2.6 us against 4.2).
+// places of two sequences to other pages: 2.5 us against 4.2).
 // AHEAD: the next turn's indices and pages are looked up before the barrier,
 // which leaves one round trip between two barriers; for few blocks in place,
 // where the SMs have the registers (one sequence of 131072 entries 199 us to 154; with
-// every SM full 114 us to 131).
+// every SM full it lost, 131 us against 109).
 template <int ROUNDS, bool AHEAD>
 __global__ void __launch_bounds__(CP_THREADS, AHEAD ? 2 : 4)
     paged_compact_kernel(CompactParams p, int split, int csize) {

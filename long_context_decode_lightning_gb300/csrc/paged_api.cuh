@@ -65,6 +65,10 @@ hsi_status rows_map(hsi_dtype dt, const void* q, int64_t qt, int64_t qh, int64_t
 
 // Many rows per KV head go to the tensor-memory kernels, whose tiles hold
 // whole tokens of 128 rows (groups of at most 128 heads, no broadcast axis of q).
+// Measured, few-row kernel against theirs, 32 query and 8 KV heads of 128: 8
+// sequences of 8000 entries 65 and 66 us at 20 rows, 67 and 66 at 32, 133 and 67
+// at 40; 32 of 2000 94 and 68 at 20; two of 1000 9.7 and 11.9 at 20, 10.7 and 12.1
+// at 48: few units alone would have the few-row kernel, by 2 us.
 bool chunk_rows(const AttendParams& p) {
     return (int64_t)p.max_q * p.group > AT_ROWS && p.group <= 128 && (p.qt > 0 || p.T == 1) && (p.qh > 0 || p.Hq == 1);
 }
@@ -172,14 +176,16 @@ int64_t attend_grid(int32_t B, int32_t heads, int32_t group, int32_t max_q, int6
 size_t attend_base_bytes(int32_t B) { return align_up(((size_t)B + 1) * 4, 256); }
 
 // Blocks of a unit in the short form (0: the line): up to eight while all units'
-// blocks run at once, each with at most AT_SHORT_TILES tiles, as ragged lengths
-// leave the blocks uneven and the line does not. Units so few that twice the
-// blocks would still run at once leave SMs idle that the line would use: they
-// take it past AT_FEW_TILES. Measured, one token, 8 KV heads of 128, short
-// against line: 16 sequences of 1500 entries 21 and 27 us, four of 6000 22 and
-// 24; two of 1100 9.9 and 10.1, of 5100 17.3 and 15.4; one of 4600 15.1 and 11.8.
-// Clusters of sixteen: two of 1100 17.2 (they do not seem to run all at once),
-// one of 3000 11.7 against the line's 12.4.
+// blocks run at once, each with at most AT_SHORT_TILES tiles. Units so few that
+// twice the blocks would still run at once leave SMs idle that the line would
+// use: they take it past AT_FEW_TILES. Measured, one token, 8 KV heads of 128, us
+// short against line: 16 sequences of 1500 entries 20 and 26, four of 6000 20 and
+// 20; two of 1100 8.8 and 9.9, of 5100 13.9 and 12.4; one of 4600 11.8 and 11.2, of
+// 8000 16 and 13. Both bounds are below where the line wins: 32 of 1000 26 and 32
+// (lengths from half of that 21 and 23, of any 17 and 32), of 2500 54 and 63 (46
+// and 50, 36 and 50), 16 of 3000 35 and 44, four of 9000 29 and 33, one of 3000 9.8
+// and 12 take the line. Clusters of sixteen: two of 1100 17.2 (they do not seem to
+// run all at once).
 constexpr int AT_SHORT_TILES = 12, AT_FEW_TILES = 4;
 int attend_short(const AttendParams& p) {
     const int64_t rt = ((int64_t)p.max_q * p.group + AT_ROWS - 1) / AT_ROWS, units = rt * p.kv.H * p.kv.B;
