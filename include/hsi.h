@@ -627,7 +627,8 @@ hsi_status hsi_paged_append(const hsi_paged_kv* cache, const void* k_new, int64_
  * h / (q_heads / heads). Row (token i of sequence b's n, head h) sees entries
  * e < kv_len[b] - n + i + 1 (causal) or e < kv_len[b]:
  *   out = sum_e p_e v_e / sum_e p_e,  p_e = exp(scale q.k_e),
- *   lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0).
+ *   lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0;
+ *   NaN, as out, for a row that sees a NaN score).
  * The products run on the tensor cores with fp32 sums; p is rounded to the
  * cache's type for the second one (in fp16 by no more than 2^-32 of a row's
  * largest p where it falls below that type's normal numbers).
