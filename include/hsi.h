@@ -700,6 +700,117 @@ hsi_status hsi_paged_compact(const hsi_paged_kv* cache, const int32_t* keep, int
 
 /* ------------------------------------------------------------------------- */
 
+/*
+ * A latent cache: one vector of dim values a token that every query head shares.
+ * All of it is the key, its first 512 values are the value (latent attention in the
+ * absorbed form; of a main-KV entry, key and value are the same 512 values). What
+ * core attention reads after the indexer's top-k.
+ */
+typedef enum {
+    HSI_LATENT_BF16 = 0, /* dim values: 2 dim bytes */
+    HSI_LATENT_FP16 = 1,
+    HSI_LATENT_FP8 = 2,  /* E4M3 codes of the first dim - 64 values, the last 64 values in bf16, a byte 127 + e for
+                            each 64 codes (their values are code * 2^e), zeros up to a multiple of 16: dim + 80 bytes */
+    HSI_LATENT_FP4 = 3   /* the main-KV entry of hsi_quantize_mainkv: 288 bytes, dim 512 */
+} hsi_latent_format;
+
+/*
+ * Entry e of sequence b is place e mod page_size of page table[b][e / page_size],
+ * at page * page_stride + place * token_stride (bytes) of data; or, where table is
+ * NULL, entry offsets[b] + e of one run of n_pages entries token_stride apart (as
+ * kv_off of hsi_gather_mainkv).
+ *  data    (dev) 16-byte aligned; strides in bytes, multiples of 16, at least an entry.
+ *  table, kv_len, table_width as in hsi_paged_kv; offsets (dev) int64 [B].
+ *  dim     512, or 576 (not FP4); page_size a power of two, 1 .. 65536 (UNSUPPORTED
+ *          otherwise; neither page_size nor page_stride is read without a table).
+ * A length below 0 or past the call's bound or what the cache holds for the
+ * sequence, a page id outside [0, n_pages) or a q_start that descends or leaves
+ * [0, T] is clamped or skipped and reported as HSI_ERR_DEVICE_ARG by
+ * hsi_device_error. Tokens lie side by side and belong to sequences as in the paged
+ * cache: sequence b's are q_start[b] .. q_start[b+1] - 1, its last entries. What the
+ * cache holds outside the sequences' entries never reaches a result.
+ */
+typedef struct {
+    void* data;
+    int64_t page_stride, token_stride;
+    int64_t n_pages;
+    const int32_t* table;
+    int64_t ld_table;
+    const int64_t* offsets;
+    const int32_t* kv_len;
+    int32_t B, dim, page_size;
+    hsi_latent_format format;
+    int64_t table_width;
+} hsi_latent_cache;
+
+/* Bytes of an entry; 0 for a format or dim that there is not. */
+size_t hsi_latent_entry_bytes(hsi_latent_format format, int32_t dim);
+
+/*
+ * The new tokens' latents into the cache, in one launch with their rotation and
+ * quantisation: token i of sequence b's n becomes entry kv_len[b] - n + i. Tokens
+ * outside every sequence are left alone.
+ *  x       (dev) [T] rows of dim values, x_token_stride elements apart (a multiple of
+ *          8, 16-byte aligned): fp16 for an FP16 cache, bf16 otherwise.
+ *  steps   NULL: as they are; otherwise dims [rot_offset, rot_offset + rot) turned as
+ *          by hsi_rope (rot a multiple of 16, rot_offset of 8: UNSUPPORTED otherwise)
+ *          and rounded to x's type, then kept as the format keeps them.
+ * FP8: e is the smallest in [-118, 120] by which the largest of the 64 values is at
+ * most 448, the code E4M3_RN(x / 2^e). FP4: as hsi_quantize_mainkv. Values must be
+ * finite for both; others are reported as HSI_ERR_DEVICE_ARG.
+ */
+hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64_t x_token_stride,
+                             const int32_t* q_start, int64_t T, const int32_t* positions, const uint64_t* steps,
+                             int32_t rot, int32_t rot_offset, int32_t interleaved, float gain, cudaStream_t stream);
+
+/*
+ * Entries back as rows of dim 16-bit values (fp16 of an FP16 cache, bf16 otherwise;
+ * every value of FP8 and FP4 entries that hsi_latent_append writes is exact).
+ *  idx NULL: row r of row_start[b] .. row_start[b+1] - 1 (of T rows) is entry
+ *          (first ? first[b] : 0) + r - row_start[b] of sequence b.
+ *  idx     (dev) int32 [T][ld_idx]: the k entries of each of T tokens, sequence b's
+ *          being row_start[b] .. row_start[b+1] - 1; a negative one gives zeros. Row i of
+ *          token t is at t * out_stride + i * dim. first must be NULL.
+ *  out     (dev) 16-byte aligned, out_stride elements (a multiple of 8) between rows
+ *          (with idx: tokens). Rows outside every sequence are left as they were.
+ * An entry outside the sequence (other than a negative one of idx) is reported as
+ * HSI_ERR_DEVICE_ARG and gives zeros. An E4M3 NaN code reads as 480.
+ */
+hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_start, int64_t T, const int32_t* first,
+                           const int32_t* idx, int64_t ld_idx, int32_t k, void* out, int64_t out_stride,
+                           cudaStream_t stream);
+
+/*
+ * Attention of the new tokens over the cache, every query head over the same
+ * entries c_e:  out = sum_e p_e c_e[0:512] / sum_e p_e,  p_e = exp(scale q.c_e),
+ * lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0; NaN, as
+ * out, for a row that sees a NaN score). Token i of sequence b's n sees
+ *  idx NULL: entries e < kv_len[b] - n + i + 1 (causal) or e < kv_len[b];
+ *  idx     (dev) int32 [T][ld_idx]: the k entries of its list. A negative one is passed
+ *          over; one that the token does not see by the rule above is passed over and
+ *          reported as HSI_ERR_DEVICE_ARG; one that is listed twice counts twice.
+ * Products on the tensor cores with fp32 sums (FP8 and FP4 entries decoded to bf16,
+ * which is exact); p is rounded to 16 bits for the second one (in fp16 by no more
+ * than 2^-32 of a row's largest p where it falls below that type's normal numbers).
+ *  q       (dev) [T][q_heads][dim], out (dev) [T][q_heads][512]: fp16 for an FP16 cache,
+ *          bf16 otherwise; strides in elements (multiples of 8, 16-byte aligned); distinct.
+ *          An entry among a sequence's new tokens must be finite for every one of them,
+ *          also where it does not see it yet (0 times a NaN is a NaN).
+ *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
+ *  lse     (dev) fp32 [T][q_heads], may be NULL.
+ *  ws      (dev) hsi_latent_attention_ws(...) bytes (k 0 without lists).
+ * Rows of tokens outside every sequence are left as they were.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED.
+ */
+size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k);
+hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, int32_t q_heads, const int32_t* q_start, int64_t T,
+                                int32_t max_q, int64_t max_kv, const int32_t* idx, int64_t ld_idx, int32_t k,
+                                float scale, int32_t causal, void* out, int64_t o_token_stride, int64_t o_head_stride,
+                                float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+
 typedef enum {
     HSI_WS_QUANTIZE = 0,
     HSI_WS_SCORE = 1,

@@ -34,11 +34,15 @@ EXPORTS = ["hsi_quantize_nvfp4", "hsi_score_full", "hsi_topk", "hsi_candidate_po
            "hsi_topk_noalloc", "hsi_debug_set", "hsi_pool_gather", "hsi_quantize_mxfp4", "hsi_quantize_mainkv",
            "hsi_gather_mainkv", "hsi_append_token", "hsi_mask_scores", "hsi_prefill_layer",
            "hsi_gather_mainkv_layers", "hsi_rope_steps", "hsi_rope", "hsi_paged_append", "hsi_paged_attention_ws",
-           "hsi_paged_attention", "hsi_attention_weights", "hsi_evict_select", "hsi_paged_compact"]
+           "hsi_paged_attention", "hsi_attention_weights", "hsi_evict_select", "hsi_paged_compact",
+           "hsi_latent_entry_bytes", "hsi_latent_append", "hsi_latent_read", "hsi_latent_attention_ws",
+           "hsi_latent_attention"]
 
 
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+LATENT_BF16, LATENT_FP16, LATENT_FP8, LATENT_FP4 = 0, 1, 2, 3  # hsi_latent_format
+LATENT_VALUE = 512  # dims of a latent entry's value, the first of its key
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -49,6 +53,15 @@ class _PagedKV(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int), ("table_width", ctypes.c_int64)]
+
+
+class _LatentCache(ctypes.Structure):
+    """hsi_latent_cache of include/hsi.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("format", ctypes.c_int),
+                ("table_width", ctypes.c_int64)]
 
 
 class HsiError(RuntimeError):
@@ -127,6 +140,17 @@ def lib() -> ctypes.CDLL:
                                             i64, vp]
         L.hsi_evict_select.argtypes = [vp, i64, vp, i32, i32, i64, i32, i32, i32, vp, i64, vp, vp, i64, vp]
         L.hsi_paged_compact.argtypes = [kvp, vp, i64, vp, i32, vp, i64, vp]
+        lcp = ctypes.POINTER(_LatentCache)
+        L.hsi_latent_entry_bytes.argtypes = [ctypes.c_int, i32]
+        L.hsi_latent_entry_bytes.restype = sz
+        L.hsi_latent_append.argtypes = [lcp, vp, i64, vp, i64, vp, vp, i32, i32, i32, f32, vp]
+        L.hsi_latent_read.argtypes = [lcp, vp, i64, vp, vp, i64, i32, vp, i64, vp]
+        L.hsi_latent_attention_ws.argtypes = [i32, i32, i64, i32, i64, i32]
+        L.hsi_latent_attention_ws.restype = sz
+        L.hsi_latent_attention.argtypes = [lcp, vp, i64, i64, i32, vp, i64, i32, i64, vp, i64, i32, f32, i32, vp, i64,
+                                           i64, vp, vp, sz, vp]
+        for name in ("hsi_latent_append", "hsi_latent_read", "hsi_latent_attention"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("hsi_rope_steps", "hsi_rope", "hsi_paged_append", "hsi_paged_attention", "hsi_attention_weights",
                      "hsi_evict_select", "hsi_paged_compact"):
             getattr(L, name).restype = ctypes.c_int
@@ -637,3 +661,156 @@ def paged_compact(kv: PagedKV, keep, new_len, dst_table=None, budget=None, strea
         kv.ref, kp, places, _i32(new_len, "new_len", kv.B), budget, dst.data_ptr(), ld, _raw_stream(stream))
     if st:
         _check("hsi_paged_compact", st)
+
+
+class LatentCache:
+    """A latent cache for the calls below: one vector of 512 or 576 values a token that all query heads share.
+
+    Paged: data [pages, page size, X], table int32 [B, pages a sequence]; contiguous: data [entries, X], offsets
+    int64 [B], entry e of sequence b being row offsets[b] + e (the library's main KV is one: uint8 [entries, 288],
+    LATENT_FP4). X is dim values of bf16 or fp16 (fmt and dim follow from data then), or the bytes of an entry (uint8;
+    fmt and dim given). kv_len int32 [B] on the device. Keeps the tensors; their contents may change, and table,
+    offsets and kv_len may be set to others of as many sequences."""
+
+    def __init__(self, data, kv_len, table=None, offsets=None, fmt=None, dim=None):
+        if data.dtype is torch.uint8:
+            if fmt not in (LATENT_FP8, LATENT_FP4) or dim is None:
+                _bad("data in bytes: fmt LATENT_FP8 or LATENT_FP4, and dim")
+            self.x_dtype = torch.bfloat16
+        else:
+            own = {torch.bfloat16: LATENT_BF16, torch.float16: LATENT_FP16}.get(data.dtype)
+            if own is None or (fmt is not None and fmt != own):
+                _bad("data: bf16 or fp16 values, or bytes (LATENT_FP8, LATENT_FP4)")
+            fmt, self.x_dtype = own, data.dtype
+            if dim is not None and dim != data.shape[-1]:
+                _bad(f"data: rows of {dim} values")
+            dim = data.shape[-1]
+        if (table is None) == (offsets is None):
+            _bad("table (a paged cache) or offsets (a contiguous one)")
+        if data.dim() != (2 if table is None else 3) or data.stride(-1) != 1 or not data.is_cuda:
+            _bad("data: [pages, page size, X] with a table, [entries, X] with offsets, rows contiguous, on the GPU")
+        if table is not None and table.dim() != 2:
+            _bad("table: int32 [sequences, pages]")
+        es = data.element_size()
+        size = int(lib().hsi_latent_entry_bytes(fmt, dim))
+        if size and data.shape[-1] * es != size:
+            _bad(f"data: entries of {size} bytes expected, got {data.shape[-1] * es}")
+        self._data, self.dim, self.fmt = data, dim, fmt
+        self.B = (offsets if table is None else table).shape[0]
+        rows = data.shape[-2]
+        token = data.stride(-2) * es if rows > 1 else -(-data.shape[-1] * es // 16) * 16
+        self.c = _LatentCache(data=_ptr(data), page_stride=0 if table is None else data.stride(0) * es,
+                              token_stride=token, n_pages=data.shape[0], B=self.B, dim=dim,
+                              page_size=0 if table is None else data.shape[1], format=fmt)
+        if table is None:
+            self.offsets = offsets
+        else:
+            self.table = table
+        self.kv_len = kv_len
+        self.ref = ctypes.byref(self.c)
+
+    # The library has the addresses, so what is kept here and what it reads change together.
+
+    @property
+    def data(self):
+        return self._data
+
+    @property
+    def table(self):
+        return self._table if self.c.table else None
+
+    @table.setter
+    def table(self, t):
+        if self.c.offsets:
+            _bad("table: the cache is contiguous")
+        ld = _table(t, "table", self.B)
+        self._table, self.c.table, self.c.ld_table, self.c.table_width = t, t.data_ptr(), ld, t.shape[1]
+
+    @property
+    def offsets(self):
+        return self._offsets if self.c.offsets else None
+
+    @offsets.setter
+    def offsets(self, t):
+        if self.c.table:
+            _bad("offsets: the cache is paged")
+        if t.dtype is not torch.int64 or t.shape != (self.B,) or not t.is_contiguous() or not t.is_cuda:
+            _bad(f"offsets: int64 [{self.B}], contiguous, on the GPU")
+        self._offsets, self.c.offsets = t, t.data_ptr()
+
+    @property
+    def kv_len(self):
+        return self._kv_len
+
+    @kv_len.setter
+    def kv_len(self, t):
+        self.c.kv_len = _i32(t, "kv_len", self.B)
+        self._kv_len = t
+
+
+def _lists(idx, T: int):
+    """Address, row stride and width of int32 [T, k] lists with contiguous rows."""
+    if idx is None:
+        return None, 0, 0
+    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or idx.stride(1) != 1 or not idx.is_cuda:
+        _bad(f"idx: int32 [{T}, entries], rows contiguous, on the GPU")
+    return idx.data_ptr(), idx.stride(0) if T > 1 else idx.shape[1], idx.shape[1]
+
+
+def latent_append(cache: LatentCache, x, q_start, positions=None, steps=None, rot_offset=None, interleaved: bool = False,
+                  gain: float = 1.0, stream=None):
+    """x [T, dim] into the cache's last entries of each sequence, in its format; with steps, the dims from rot_offset
+    (by default the last ones) rotated at positions int32 [T] in the same launch."""
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != cache.dim or x.dtype is not cache.x_dtype or x.stride(1) != 1 or not x.is_cuda:
+        _bad(f"x: {cache.x_dtype} [tokens, {cache.dim}], rows contiguous, on the GPU")
+    T = shape[0]
+    pos = None if positions is None else _i32(positions, "positions", T)
+    sp, rot = (None, 0) if steps is None else (_steps(steps), 2 * steps.shape[0])
+    st = (_lib or lib()).hsi_latent_append(
+        cache.ref, x.data_ptr(), x.stride(0), _i32(q_start, "q_start", cache.B + 1), T, pos, sp, rot,
+        cache.dim - rot if rot_offset is None else rot_offset, interleaved, gain, _raw_stream(stream))
+    if st:
+        _check("hsi_latent_append", st)
+
+
+def latent_read(cache: LatentCache, out, start, first=None, idx=None, stream=None):
+    """Entries back as 16-bit rows. Without idx, rows start[b] .. start[b+1] - 1 of out [rows, dim] are sequence b's
+    entries from first[b] on (int32 [B]; None: from 0). With idx int32 [T, k], out [T, k, dim] gets each token's
+    entries, start being the tokens' q_start; a negative one gives zeros."""
+    shape, st = out.shape, out.stride()
+    rows = shape[0] if shape else 0
+    ip, il, k = _lists(idx, rows)
+    if shape != ((rows, cache.dim) if idx is None else (rows, k, cache.dim)) or out.dtype is not cache.x_dtype or \
+            st[-1] != 1 or not out.is_cuda or (idx is not None and k > 1 and st[1] != cache.dim):
+        _bad(f"out: {cache.x_dtype} [rows, {cache.dim}], or [tokens, entries, {cache.dim}] with idx, on the GPU")
+    st = (_lib or lib()).hsi_latent_read(
+        cache.ref, _i32(start, "start", cache.B + 1), rows, None if first is None else _i32(first, "first", cache.B), ip,
+        il, k, out.data_ptr(), st[0], _raw_stream(stream))
+    if st:
+        _check("hsi_latent_read", st)
+
+
+def latent_attention_workspace(cache: LatentCache, q, max_q: int, max_kv: int, k: int = 0, stream=None) -> torch.Tensor:
+    """A caller-owned scratch buffer for latent_attention on `stream`; k: the width of its lists (0: none)."""
+    n = int(lib().hsi_latent_attention_ws(cache.B, q.shape[1], q.shape[0], max_q, max_kv, k))
+    return _scratch(max(n, 1), q.device, stream)
+
+
+def latent_attention(cache: LatentCache, q, q_start, max_q: int, max_kv: int, scale: float, out, lse=None, idx=None,
+                     causal: bool = True, ws=None, stream=None):
+    """q [T, q heads, dim] over the cache's entries, or over those of idx int32 [T, k] (negative ones are passed over),
+    into out [T, q heads, 512] (and lse fp32 [T, q heads])."""
+    T, H = q.shape[:2]
+    qp, qt, qh = _heads(q, "q", (T, H, cache.dim), cache.x_dtype)
+    op, ot, oh = _heads(out, "out", (T, H, LATENT_VALUE), cache.x_dtype)
+    ip, il, k = _lists(idx, T)
+    if ws is None:
+        ws = latent_attention_workspace(cache, q, max_q, max_kv, k, stream)
+    elif not ws.is_cuda:
+        _bad("ws: on the GPU")
+    st = (_lib or lib()).hsi_latent_attention(
+        cache.ref, qp, qt, qh, H, _i32(q_start, "q_start", cache.B + 1), T, max_q, max_kv, ip, il, k, scale, causal, op,
+        ot, oh, None if lse is None else _lse(lse, (T, H)), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if st:
+        _check("hsi_latent_attention", st)

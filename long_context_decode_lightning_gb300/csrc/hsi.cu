@@ -1084,3 +1084,4 @@ hsi_status hsi_reindex_layer(const uint8_t* q_rec, const float* g_q, const float
 }  // extern "C"
 
 #include "paged_api.cuh"
+#include "latent_api.cuh"

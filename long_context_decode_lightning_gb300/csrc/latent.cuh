@@ -1,0 +1,360 @@
+// The latent cache: one vector of 512 or 576 values a token that all query heads
+// share (its first 512 are the value, all of it is the key), its formats, the
+// append of new tokens and reading entries back.
+//
+// Formats of an entry of `dim` values:
+//  16-bit  dim values.
+//  FP8     E4M3 codes of the first dim - 64 values, the last 64 (where rotary
+//          dims lie) in bf16, then a byte for each 64 codes, 127 + e: their values are
+//          code * 2^e, e the smallest by which the largest of the 64 is at most 448. As
+//          the scale is a power of two, decoded values are exact in bf16. Padded to 16
+//          bytes: dim + 80 in all.
+//  FP4     the main KV's entry (mainkv.cuh): 512 values in 288 bytes.
+//
+// Append and read are bound by HBM. Both give a warp whole rows with 8 values a
+// lane and step, so that every access is 4, 8 or 16 bytes a lane side by side.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "mainkv.cuh"
+#include "paged.cuh"
+#include "quantize.cuh"
+#include "rope.cuh"
+
+namespace hsi {
+
+enum LatentFormat { LF_BF16 = 0, LF_FP16 = 1, LF_FP8 = 2, LF_FP4 = 3 };
+
+constexpr int LT_VALUE = 512;      // dims of the value
+constexpr int LT_TAIL = 64;        // values of an FP8 entry that stay in bf16
+constexpr int LT_MIN_E = -118, LT_MAX_E = 120;  // scales' exponents: every code's value is a bf16 number
+
+__host__ __device__ constexpr int latent_entry_bytes(int fmt, int dim) {
+    return fmt == LF_FP8 ? dim + 80 : fmt == LF_FP4 ? KV_BYTES : 2 * dim;
+}
+
+struct LatentView {
+    uint8_t* data;
+    int64_t page_stride, token_stride;  // bytes
+    int64_t n_pages;                    // without a table: entries
+    const int32_t* table;               // [B][ld_table], or null: entry e of sequence b is entry off[b] + e
+    int64_t ld_table;
+    const int64_t* off;
+    const int32_t* kv_len;
+    int B, dim, page_shift;
+    int capacity;                       // entries that a row of the table lists (without a table: of the cache)
+};
+
+// Entries of sequence b, clamped to what the cache can hold for it and to the host's bound.
+__device__ __forceinline__ int32_t latent_len(const LatentView& c, int b, int32_t bound = INT32_MAX) {
+    const int32_t n = __ldg(c.kv_len + b);
+    int64_t most = min(c.capacity, bound);
+    if (!c.table) {
+        const int64_t at = __ldg(c.off + b);
+        most = at < 0 || at > c.n_pages ? 0 : min(most, c.n_pages - at);
+    }
+    if (n < 0 || n > most) {
+        raise_error(DEVERR_ARG);
+        return n < 0 ? 0 : (int32_t)most;
+    }
+    return n;
+}
+
+// The entry's address; null (reported) where the table names no page. e is below the sequence's length.
+__device__ __forceinline__ uint8_t* latent_entry(const LatentView& c, int b, int32_t e) {
+    if (!c.table) return c.data + (__ldg(c.off + b) + e) * c.token_stride;
+    const int32_t page = __ldg(c.table + b * c.ld_table + (e >> c.page_shift));
+    if (page < 0 || page >= c.n_pages) {
+        raise_error(DEVERR_ARG);
+        return nullptr;
+    }
+    return c.data + page * c.page_stride + (int64_t)(e & ((1 << c.page_shift) - 1)) * c.token_stride;
+}
+
+// Four E4M3 codes as two pairs of bf16 numbers, 2^-120 of their values: the code's seven bits
+// are moved to the bf16 fields, subnormal codes among them (0x7F is 480, not NaN).
+__device__ __forceinline__ void e4m3x4_fields(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    lo = (a & 0x80008000u) | ((a & 0x7F007F00u) >> 4);
+    hi = (b & 0x80008000u) | ((b & 0x7F007F00u) >> 4);
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+// Eight codes times 2^(scale byte - 127). Two products, as 2^(120 + e) may be past bf16; both are exact.
+__device__ __forceinline__ void decode8_fp8(uint2 codes, uint32_t scale, uint32_t (&o)[4]) {
+    const uint32_t s = scale << 7 | scale << 23;
+    e4m3x4_fields(codes.x, o[0], o[1]);
+    e4m3x4_fields(codes.y, o[2], o[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = bf16x2_mul(bf16x2_mul(o[i], 0x7B807B80u), s);  // 2^120
+}
+
+// ------------------------------------------------------------------- append --
+
+struct LatentAppendParams {
+    LatentView c;
+    RopeTurn r;        // steps null: no rotation
+    const void* x;     // [T] rows of dim values, xt apart
+    int64_t xt, T;
+    const int32_t* q_start;
+};
+
+// The sequence of token t of `total`, by a whole warp: -1 where it lies outside every one, or (reported) where q_start
+// descends around it or its sequence leaves the tokens. *first, *past: the sequence's tokens.
+__device__ __forceinline__ int token_seq_warp(const int32_t* q_start, int B, int64_t t, int64_t total, int32_t* first,
+                                              int32_t* past) {
+    int b = 0, last = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < B; i += 32) {
+        if (__ldg(q_start + i + 1) > t) continue;
+        ++b;
+        last = i + 1;
+    }
+    b = __reduce_add_sync(~0u, b);
+    if (__reduce_max_sync(~0u, last) != b) {
+        raise_error(DEVERR_ARG);
+        return -1;
+    }
+    if (b >= B) return -1;
+    *first = __ldg(q_start + b);
+    *past = __ldg(q_start + b + 1);
+    if (t < *first) return -1;
+    if (*first < 0 || *past > total) {
+        raise_error(DEVERR_ARG);
+        return -1;
+    }
+    return b;
+}
+
+constexpr int LT_WARPS = 8;
+
+// A warp per token. A rotated value is rounded to the tokens' type, then kept as
+// the format keeps it, so that the entry is the unrotated append of hsi_rope's result.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(32 * LT_WARPS) latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * LT_WARPS + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const int lane = threadIdx.x & 31, dim = p.c.dim;
+    const T* x = static_cast<const T*>(p.x) + t * p.xt;
+    uint4 raw[3] = {};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (lane + 32 * i < dim / 8) raw[i] = __ldg(reinterpret_cast<const uint4*>(x) + lane + 32 * i);
+    int32_t first, past;
+    const int b = token_seq_warp(p.q_start, p.c.B, t, p.T, &first, &past);
+    if (b < 0) return;
+    // by the length as it is: by one clamped to the row, the tokens would land on the entries before them
+    const int32_t n = __ldg(p.c.kv_len + b);
+    const int64_t e = (int64_t)n - (past - t);
+    int64_t most = p.c.capacity;
+    if (!p.c.table) {
+        const int64_t at = __ldg(p.c.off + b);
+        most = at < 0 || at > p.c.n_pages ? 0 : min(most, p.c.n_pages - at);
+    }
+    if (n > most && lane == 0) raise_error(DEVERR_ARG);
+    if (e < 0 || e >= most) {
+        if (lane == 0) raise_error(DEVERR_ARG);
+        return;
+    }
+    uint8_t* dst = latent_entry(p.c, b, (int32_t)e);
+    if (!dst) return;
+
+    if (p.r.steps) {
+        const int32_t pos = __ldg(p.r.pos + t);
+        const int half = p.r.rot / 2;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int m = 8 * (lane + 32 * i), d = m - p.r.off;  // rot is a multiple of 16, off of 8
+            if (m >= dim || d < 0 || d >= p.r.rot) continue;
+            uint32_t* w = &raw[i].x;
+            if (p.r.pairs) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 cs = rope_turn(p.r, d / 2 + j, pos), v = unpack2<T>(w[j]);
+                    w[j] = pack2<T>(v.x * cs.x - v.y * cs.y, v.x * cs.y + v.y * cs.x);
+                }
+            } else {
+                const bool low = d < half;
+                const uint4 other = __ldg(reinterpret_cast<const uint4*>(x + (low ? m + half : m - half)));
+                const uint32_t* o = &other.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int pair = (low ? d : d - half) + 2 * j;
+                    const float2 c0 = rope_turn(p.r, pair, pos), c1 = rope_turn(p.r, pair + 1, pos);
+                    const float2 v = unpack2<T>(w[j]), u = unpack2<T>(o[j]);
+                    // (u, v) -> (u cos - v sin, u sin + v cos): this lane holds u below half, v from there
+                    w[j] = low ? pack2<T>(v.x * c0.x - u.x * c0.y, v.y * c1.x - u.y * c1.y)
+                               : pack2<T>(u.x * c0.y + v.x * c0.x, u.y * c1.y + v.y * c1.x);
+                }
+            }
+        }
+    }
+    if constexpr (FMT == LF_BF16 || FMT == LF_FP16) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (lane + 32 * i < dim / 8) *(reinterpret_cast<uint4*>(dst) + lane + 32 * i) = raw[i];
+        return;
+    }
+    const int codes = FMT == LF_FP8 ? dim - LT_TAIL : dim;
+    uint32_t scales[2] = {0u, 0u};  // FP8: the scale bytes of groups 0-3, 4-7
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int m = 8 * (lane + 32 * i);
+        const uint32_t* w = &raw[i].x;
+        float v[8], amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<T>(w[j]);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+        // a NaN is passed over by the maximum, so values are looked at one by one
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            finite = finite && isfinite(v[j]);
+            amax = fmaxf(amax, fabsf(v[j]));
+        }
+        if constexpr (FMT == LF_FP8) {
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+            const uint32_t bits = __float_as_uint(amax);  // 448 = 1.75 * 2^8
+            int ex = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u);
+            ex = max(LT_MIN_E, min(LT_MAX_E, ex));
+            const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (m < codes) {
+                uint32_t c[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %1, %2; cvt.u32.u16 %0, t; }"
+                        : "=r"(c[j])
+                        : "f"(v[2 * j + 1] * inv), "f"(v[2 * j] * inv));
+                *reinterpret_cast<uint2*>(dst + m) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+            } else if (m < dim) {
+                *reinterpret_cast<uint4*>(dst + codes + 2 * (m - codes)) = raw[i];
+            }
+            if (i < 2) {
+                const uint32_t byte = m < codes ? (uint32_t)(ex + 127) << (lane & 24) : 0u;
+                scales[i] = __reduce_or_sync(~0u, (lane & 7) == 0 ? byte : 0u);
+            }
+        } else if (i < 2) {
+            amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+            const uint32_t sb = f32_to_e4m3_rn_sat(__fdiv_rn(amax, 6.0f));
+            const float sc = e4m3_to_f32(sb);
+            uint32_t c = 0u;
+            if (sc != 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], sc);
+                c = f32x4_to_e2m1x4(v[0], v[1], v[2], v[3]) | f32x4_to_e2m1x4(v[4], v[5], v[6], v[7]) << 16;
+            }
+            *reinterpret_cast<uint32_t*>(dst + m / 2) = c;
+            if ((lane & 1) == 0) dst[256 + m / 16] = (uint8_t)sb;
+        }
+    }
+    if (!finite) raise_error(DEVERR_ARG);
+    if (FMT == LF_FP8 && lane == 0)
+        *reinterpret_cast<uint4*>(dst + codes + 2 * LT_TAIL) = make_uint4(scales[0], scales[1], 0u, 0u);
+}
+
+// --------------------------------------------------------------------- read --
+
+struct LatentReadParams {
+    LatentView c;
+    const int32_t* start;  // [B + 1]: the rows (with lists: the tokens) of each sequence
+    const int32_t* first;  // [B] the entry of a sequence's first row, or null (0); not with lists
+    const int32_t* idx;    // [T][ld_idx], k entries a token, or null
+    int64_t ld_idx;
+    int32_t k;
+    int64_t T, rows;       // tokens (without lists: rows), rows
+    uint16_t* out;
+    int64_t ot;            // elements between rows (with lists: between tokens, whose rows lie side by side)
+};
+
+constexpr int LT_RPW = 4;  // rows a warp reads at once
+
+// A warp takes four rows side by side and has all their loads in flight.
+template <int FMT>
+__global__ void __launch_bounds__(32 * LT_WARPS) latent_read_kernel(const __grid_constant__ LatentReadParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t r0 = ((int64_t)blockIdx.x * LT_WARPS + (threadIdx.x >> 5)) * LT_RPW;
+    if (r0 >= p.rows) return;
+    const int lane = threadIdx.x & 31, dim = p.c.dim;
+    const uint8_t* src[LT_RPW];  // null: zeros
+    bool live[LT_RPW];           // rows of some sequence
+#pragma unroll
+    for (int j = 0; j < LT_RPW; ++j) {
+        const int64_t r = r0 + j, t = p.idx ? r / p.k : r;
+        src[j] = nullptr;
+        live[j] = false;
+        if (r >= p.rows) continue;
+        int32_t from, past;
+        const int b = token_seq_warp(p.start, p.c.B, t, p.T, &from, &past);
+        if (b < 0) continue;
+        live[j] = true;
+        const int64_t e = p.idx ? __ldg(p.idx + t * p.ld_idx + (r - t * p.k))
+                                : t - from + (p.first ? __ldg(p.first + b) : 0);
+        if (p.idx && e < 0) continue;
+        if (e < 0 || e >= latent_len(p.c, b)) {
+            raise_error(DEVERR_ARG);
+            continue;
+        }
+        src[j] = latent_entry(p.c, b, (int32_t)e);
+    }
+    constexpr int N = FMT == LF_FP8 || FMT == LF_FP4 ? 2 : 3;
+    uint4 v[LT_RPW][3] = {};
+    uint32_t sc[LT_RPW][2] = {};
+#pragma unroll
+    for (int j = 0; j < LT_RPW; ++j) {
+        if (!src[j]) continue;
+        if constexpr (FMT == LF_FP8) {
+            const int codes = dim - LT_TAIL;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int m = 8 * (lane + 32 * i);
+                if (m >= codes) continue;
+                const uint2 c = __ldcs(reinterpret_cast<const uint2*>(src[j] + m));
+                v[j][i].x = c.x;
+                v[j][i].y = c.y;
+                sc[j][i] = __ldcs(src[j] + codes + 2 * LT_TAIL + m / 64);
+            }
+            if (lane < 8) v[j][2] = __ldcs(reinterpret_cast<const uint4*>(src[j] + codes) + lane);
+        } else if constexpr (FMT == LF_FP4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[j][i].x = __ldcs(reinterpret_cast<const uint32_t*>(src[j]) + lane + 32 * i);
+                sc[j][i] = __ldcs(src[j] + 256 + (lane + 32 * i) / 2);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (lane + 32 * i < dim / 8) v[j][i] = __ldcs(reinterpret_cast<const uint4*>(src[j]) + lane + 32 * i);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < LT_RPW; ++j) {
+        if (!live[j]) continue;
+        const int64_t r = r0 + j;
+        uint16_t* row = p.idx ? p.out + r / p.k * p.ot + r % p.k * dim : p.out + r * p.ot;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int m = 8 * (lane + 32 * i);
+            uint32_t o[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
+            if constexpr (FMT == LF_FP8) decode8_fp8(make_uint2(v[j][i].x, v[j][i].y), sc[j][i], o);
+            if constexpr (FMT == LF_FP4) decode8_bf16(v[j][i].x, sc[j][i], o);
+            if (m < (FMT == LF_FP8 ? dim - LT_TAIL : dim))
+                __stcs(reinterpret_cast<uint4*>(row + m), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        if (FMT == LF_FP8 && lane < 8) __stcs(reinterpret_cast<uint4*>(row + dim - LT_TAIL) + lane, v[j][2]);
+    }
+}
+
+}  // namespace hsi

@@ -1,0 +1,160 @@
+// C-ABI entry points of the latent cache: host-side validation and launch
+// shapes. Included by hsi.cu after paged_api.cuh.
+#pragma once
+#include <cmath>
+
+#include "latent.cuh"
+#include "latent_attend.cuh"
+
+namespace {
+
+hsi_status latent_view(const hsi_latent_cache* c, LatentView* v) {
+    if (!c || !c->data || !c->kv_len || c->B <= 0 || c->n_pages <= 0) return HSI_ERR_INVALID_ARG;
+    if (c->format < HSI_LATENT_BF16 || c->format > HSI_LATENT_FP4) return HSI_ERR_INVALID_ARG;
+    if (!(c->dim == 512 || (c->dim == 576 && c->format != HSI_LATENT_FP4)) || c->B > 65535) return HSI_ERR_UNSUPPORTED;
+    const int64_t bytes = latent_entry_bytes(c->format, c->dim), far = int64_t(1) << 40;
+    if (!aligned(c->data, 16) || c->token_stride < bytes || c->token_stride % 16 || c->token_stride >= far)
+        return HSI_ERR_INVALID_ARG;
+    v->data = static_cast<uint8_t*>(c->data);
+    v->token_stride = c->token_stride;
+    v->n_pages = c->n_pages;
+    v->kv_len = c->kv_len;
+    v->B = c->B;
+    v->dim = c->dim;
+    if (!c->table) {
+        if (!c->offsets || !aligned(c->offsets, 8)) return HSI_ERR_INVALID_ARG;
+        v->off = c->offsets;
+        v->capacity = (int)(c->n_pages < INT32_MAX ? c->n_pages : INT32_MAX);
+        return HSI_OK;
+    }
+    if (c->ld_table <= 0 || c->table_width < 0 || c->table_width > c->ld_table || c->page_size <= 0 ||
+        c->n_pages >= INT32_MAX)
+        return HSI_ERR_INVALID_ARG;
+    if (c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return HSI_ERR_UNSUPPORTED;
+    v->page_stride = c->n_pages == 1 ? c->token_stride : c->page_stride;  // never used where there is one page
+    if (v->page_stride < bytes || v->page_stride % 16 || v->page_stride >= far) return HSI_ERR_INVALID_ARG;
+    v->table = c->table;
+    v->ld_table = c->ld_table;
+    const int64_t width = c->table_width ? c->table_width : c->ld_table, most = INT32_MAX / c->page_size;
+    v->capacity = width > most ? INT32_MAX : (int)(width * c->page_size);  // lengths are 32-bit
+    while ((1 << v->page_shift) < c->page_size) ++v->page_shift;
+    return HSI_OK;
+}
+
+bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) { return k > 0 && ld_idx >= k && aligned(idx, 4); }
+
+}  // namespace
+
+extern "C" {
+
+size_t hsi_latent_entry_bytes(hsi_latent_format format, int32_t dim) {
+    if (format < HSI_LATENT_BF16 || format > HSI_LATENT_FP4) return 0;
+    if (!(dim == 512 || (dim == 576 && format != HSI_LATENT_FP4))) return 0;
+    return (size_t)latent_entry_bytes(format, dim);
+}
+
+hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64_t x_token_stride,
+                             const int32_t* q_start, int64_t T, const int32_t* positions, const uint64_t* steps,
+                             int32_t rot, int32_t rot_offset, int32_t interleaved, float gain, cudaStream_t stream) {
+    LatentAppendParams p{};
+    const hsi_status st = latent_view(cache, &p.c);
+    if (st != HSI_OK) return st;
+    if (!q_start || T <= 0 || T > INT32_MAX || !rows_ok(x, x_token_stride, 0)) return HSI_ERR_INVALID_ARG;
+    if (steps) {
+        if (!positions || !aligned(positions, 4) || !aligned(steps, 8) || !turn_ok(cache->dim, rot, rot_offset) ||
+            !(gain == gain))
+            return HSI_ERR_INVALID_ARG;
+        if (rot % 16 || rot_offset % 8) return HSI_ERR_UNSUPPORTED;
+        p.r = {reinterpret_cast<const unsigned long long*>(steps), positions, rot, rot_offset, interleaved != 0, gain, 1.f};
+    }
+    p.x = x;
+    p.xt = x_token_stride;
+    p.T = T;
+    p.q_start = q_start;
+    const dim3 grid((unsigned)((T + LT_WARPS - 1) / LT_WARPS)), block(32 * LT_WARPS);
+    switch (cache->format) {
+        case HSI_LATENT_BF16: return launch(latent_append_kernel<__nv_bfloat16, LF_BF16>, grid, block, 0, stream, p);
+        case HSI_LATENT_FP16: return launch(latent_append_kernel<__half, LF_FP16>, grid, block, 0, stream, p);
+        case HSI_LATENT_FP8: return launch(latent_append_kernel<__nv_bfloat16, LF_FP8>, grid, block, 0, stream, p);
+        default: return launch(latent_append_kernel<__nv_bfloat16, LF_FP4>, grid, block, 0, stream, p);
+    }
+}
+
+hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_start, int64_t T, const int32_t* first,
+                           const int32_t* idx, int64_t ld_idx, int32_t k, void* out, int64_t out_stride,
+                           cudaStream_t stream) {
+    LatentReadParams p{};
+    const hsi_status st = latent_view(cache, &p.c);
+    if (st != HSI_OK) return st;
+    if (!row_start || T <= 0 || T > INT32_MAX || !rows_ok(out, out_stride, 0)) return HSI_ERR_INVALID_ARG;
+    if (idx && (!lists_ok(idx, ld_idx, k) || first)) return HSI_ERR_INVALID_ARG;
+    if (T > 1 && out_stride < (int64_t)cache->dim * (idx ? k : 1)) return HSI_ERR_INVALID_ARG;  // two results in one place
+    p.start = row_start;
+    p.first = first;
+    p.idx = idx;
+    p.ld_idx = ld_idx;
+    p.k = k;
+    p.T = T;
+    p.rows = idx ? T * k : T;
+    p.out = static_cast<uint16_t*>(out);
+    p.ot = out_stride;
+    const int64_t blocks = (p.rows + LT_WARPS * LT_RPW - 1) / (LT_WARPS * LT_RPW);
+    if (blocks > INT32_MAX) return HSI_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks), block(32 * LT_WARPS);
+    switch (cache->format) {
+        case HSI_LATENT_FP8: return launch(latent_read_kernel<LF_FP8>, grid, block, 0, stream, p);
+        case HSI_LATENT_FP4: return launch(latent_read_kernel<LF_FP4>, grid, block, 0, stream, p);
+        default: return launch(latent_read_kernel<LF_BF16>, grid, block, 0, stream, p);
+    }
+}
+
+size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k) {
+    if (B <= 0 || q_heads <= 0 || T <= 0 || max_q <= 0 || max_kv <= 0 || k < 0) return 0;
+    return 256;
+}
+
+hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, int32_t q_heads, const int32_t* q_start, int64_t T,
+                                int32_t max_q, int64_t max_kv, const int32_t* idx, int64_t ld_idx, int32_t k,
+                                float scale, int32_t causal, void* out, int64_t o_token_stride, int64_t o_head_stride,
+                                float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    LatentAttendParams p{};
+    const hsi_status st = latent_view(cache, &p.c);
+    if (st != HSI_OK) return st;
+    if (!q_start || T <= 0 || T > INT32_MAX || max_q <= 0 || max_kv <= 0 || max_kv > INT32_MAX || q_heads <= 0 ||
+        !rows_ok(q, q_token_stride, q_head_stride) || !(scale == scale) || (idx && !lists_ok(idx, ld_idx, k)))
+        return HSI_ERR_INVALID_ARG;
+    if (!rows_ok(out, o_token_stride, o_head_stride) || out == q || (T > 1 && o_token_stride < LT_VALUE) ||
+        (q_heads > 1 && o_head_stride < LT_VALUE))
+        return HSI_ERR_INVALID_ARG;
+    if (q_heads > 65535) return HSI_ERR_UNSUPPORTED;
+    p.max_kv = (int)(max_kv < p.c.capacity ? max_kv : p.c.capacity);
+    p.max_q = (int)(max_q < T ? max_q : T);
+    if (p.max_kv > INT32_MAX - 4096) return HSI_ERR_UNSUPPORTED;
+    const size_t need = hsi_latent_attention_ws(cache->B, q_heads, T, p.max_q, p.max_kv, idx ? k : 0);
+    if (!ws || ws_bytes < need || !aligned(ws, 256)) return HSI_ERR_WORKSPACE;
+    p.q = q;
+    p.qt = q_token_stride;
+    p.qh = q_head_stride;
+    p.q_start = q_start;
+    p.T = T;
+    p.H = q_heads;
+    p.idx = idx;
+    p.ld_idx = ld_idx;
+    p.k = idx ? k : 0;
+    p.sl2 = scale * LOG2E;
+    p.causal = causal != 0;
+    p.out = out;
+    p.ot = o_token_stride;
+    p.oh = o_head_stride;
+    p.lse = lse;
+    const dim3 grid((unsigned)T, (unsigned)((q_heads + LS_HEADS - 1) / LS_HEADS)), block(LS_THREADS);
+    switch (cache->format) {
+        case HSI_LATENT_BF16: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_BF16>, grid, block, 0, stream, p);
+        case HSI_LATENT_FP16: return launch(latent_attend_simple_kernel<__half, LF_FP16>, grid, block, 0, stream, p);
+        case HSI_LATENT_FP8: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_FP8>, grid, block, 0, stream, p);
+        default: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_FP4>, grid, block, 0, stream, p);
+    }
+}
+
+}  // extern "C"
