@@ -1,6 +1,7 @@
 // C-ABI entry points of the latent cache: host-side validation and launch
 // shapes. Included by hsi.cu after paged_api.cuh.
 #pragma once
+#include <algorithm>
 #include <cmath>
 
 #include "latent.cuh"
@@ -42,6 +43,43 @@ hsi_status latent_view(const hsi_latent_cache* c, LatentView* v) {
 }
 
 bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) { return k > 0 && ld_idx >= k && aligned(idx, 4); }
+
+// How heads and tokens make units of at most 64 rows.
+struct LatentTiles {
+    int nht, hp, tpt;  // head tiles of a token, heads of one, tokens of a unit
+    LatentTiles(int32_t H, bool lists) {
+        nht = (H + LA_ROWS - 1) / LA_ROWS;
+        hp = (H + nht - 1) / nht;
+        tpt = lists || nht > 1 ? 1 : LA_ROWS / H;
+    }
+};
+
+// Tiles of the line, at the host's bounds; more than 2^31 where they pass it.
+int64_t latent_tiles(const LatentTiles& t, int32_t B, int64_t T, int64_t max_q, int64_t max_kv, int32_t k) {
+    const int64_t keys = k > 0 ? k : max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS;
+    // sequences without tokens have no units, so there are no more units than tokens
+    const int64_t units = k > 0 ? T : std::min(T, B * ((max_q + t.tpt - 1) / t.tpt));
+    return units > INT32_MAX || nt > INT32_MAX ? int64_t(1) << 62 : units * nt;
+}
+
+// Runs: a CTA per SM and head tile, no more than there can be tiles.
+int64_t latent_runs(const LatentTiles& t, int64_t tiles) {
+    const int64_t sms = sm_count(), room = sms > t.nht ? sms / t.nht : 1;
+    return tiles < room ? tiles : room;
+}
+
+size_t latent_desc_bytes(const LatentTiles& t, int64_t runs) { return align_up((size_t)runs * t.nht * sizeof(int4), 256); }
+
+template <typename T, int DIM, int FMT>
+hsi_status launch_latent_attend(const LatentAttendParams& p, cudaStream_t s) {
+    using C = LatentCfg<DIM>;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (smem_attr_once(latent_attend_kernel<T, DIM, FMT>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
+    const unsigned grid = (unsigned)(p.runs * p.nht);
+    const hsi_status st = launch(latent_attend_kernel<T, DIM, FMT>, dim3(grid), dim3(LA_THREADS), C::SMEM_BYTES, s, p);
+    if (st != HSI_OK || p.runs == 1) return st;
+    return launch(latent_join_kernel<T>, dim3(p.tpt * p.hp, grid), dim3(LT_VALUE / 4), 0, s, p);
+}
 
 }  // namespace
 
@@ -110,7 +148,9 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
 
 size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k) {
     if (B <= 0 || q_heads <= 0 || T <= 0 || max_q <= 0 || max_kv <= 0 || k < 0) return 0;
-    return 256;
+    const LatentTiles t(q_heads, k > 0);
+    const int64_t runs = latent_runs(t, latent_tiles(t, B, T, max_q, max_kv, k));
+    return latent_desc_bytes(t, runs) + align_up((size_t)runs * 2 * t.nht * LA_SLOT * 4, 256);
 }
 
 hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,
@@ -131,6 +171,9 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     p.max_kv = (int)(max_kv < p.c.capacity ? max_kv : p.c.capacity);
     p.max_q = (int)(max_q < T ? max_q : T);
     if (p.max_kv > INT32_MAX - 4096) return HSI_ERR_UNSUPPORTED;
+    const LatentTiles tiles(q_heads, idx != nullptr);
+    const int64_t most = latent_tiles(tiles, cache->B, T, p.max_q, p.max_kv, idx ? k : 0);
+    if (most > INT32_MAX) return HSI_ERR_UNSUPPORTED;  // the kernels count them in 31 bits
     const size_t need = hsi_latent_attention_ws(cache->B, q_heads, T, p.max_q, p.max_kv, idx ? k : 0);
     if (!ws || ws_bytes < need || !aligned(ws, 256)) return HSI_ERR_WORKSPACE;
     p.q = q;
@@ -139,21 +182,35 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     p.q_start = q_start;
     p.T = T;
     p.H = q_heads;
+    p.nht = tiles.nht;
+    p.hp = tiles.hp;
+    p.tpt = tiles.tpt;
     p.idx = idx;
     p.ld_idx = ld_idx;
     p.k = idx ? k : 0;
-    p.sl2 = scale * LOG2E;
+    p.negate = scale < 0.f;
+    p.sl2 = std::fmax(std::fabs(scale * LOG2E), 1e-30f);  // above 0, so that -inf stays -inf: at scale 0 every p is 1
     p.causal = causal != 0;
     p.out = out;
     p.ot = o_token_stride;
     p.oh = o_head_stride;
     p.lse = lse;
-    const dim3 grid((unsigned)T, (unsigned)((q_heads + LS_HEADS - 1) / LS_HEADS)), block(LS_THREADS);
+    p.runs = (int)latent_runs(tiles, most);
+    if (p.runs <= 0) return HSI_ERR_CUDA;
+    p.desc = static_cast<int4*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + latent_desc_bytes(tiles, p.runs));
+    const bool wide = cache->dim > LT_VALUE;
     switch (cache->format) {
-        case HSI_LATENT_BF16: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_BF16>, grid, block, 0, stream, p);
-        case HSI_LATENT_FP16: return launch(latent_attend_simple_kernel<__half, LF_FP16>, grid, block, 0, stream, p);
-        case HSI_LATENT_FP8: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_FP8>, grid, block, 0, stream, p);
-        default: return launch(latent_attend_simple_kernel<__nv_bfloat16, LF_FP4>, grid, block, 0, stream, p);
+        case HSI_LATENT_BF16:
+            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_BF16>(p, stream)
+                        : launch_latent_attend<__nv_bfloat16, 512, LF_BF16>(p, stream);
+        case HSI_LATENT_FP16:
+            return wide ? launch_latent_attend<__half, 576, LF_FP16>(p, stream)
+                        : launch_latent_attend<__half, 512, LF_FP16>(p, stream);
+        case HSI_LATENT_FP8:
+            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_FP8>(p, stream)
+                        : launch_latent_attend<__nv_bfloat16, 512, LF_FP8>(p, stream);
+        default: return launch_latent_attend<__nv_bfloat16, 512, LF_FP4>(p, stream);
     }
 }
 

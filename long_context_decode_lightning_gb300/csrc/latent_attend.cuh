@@ -2,14 +2,37 @@
 // whole entry and its value the entry's first 512 dims.
 //   s_e = scale q.c_e,  out = sum p_e c_e[:512] / sum p_e,  p_e = exp(s_e - max)
 // over the entries that a token sees, or those of a list it brings.
+//
+// A unit is up to 64 rows (row = token * heads + head) over the same entries: a
+// token's heads (or 64 of them), several tokens of few heads where there are no
+// lists. Its entries come in tiles of 64, kept in shared memory once, 64 dims of
+// the tile to a chunk, and used twice by the tensor cores:
+//   S = Q K^T       64 rows x 64 entries, K-major chunks
+//   O^T += V^T P^T  512 dims x 64 rows, the same chunks MN-major
+// O is kept transposed, as 64 rows x 512 dims in place take all of tensor
+// memory and leave nothing for S: transposed they are four accumulators of 128
+// dims by 64 columns. A row's rescaling (lazy, as in attend_chunk.cuh) is one of columns then.
+//
+// Warps: four turn S into P and write results, one issues products, one looks
+// entries up (lists, pages) a few tiles ahead, one brings the queries, and
+// eight bring the entries chunk by chunk, decoding FP8 and FP4 on the way.
+// The units' tiles form one line that is cut into equal runs, one per CTA; a
+// unit that spans runs is joined by a second kernel from fp32 partial sums.
 #pragma once
 #include <cstdint>
 
 #include "attend.cuh"
+#include "attend_chunk.cuh"
 #include "common.cuh"
 #include "latent.cuh"
 
 namespace hsi {
+
+constexpr int LA_ROWS = 64;   // rows of a unit
+constexpr int LA_KEYS = 64;   // entries of a tile
+constexpr int LA_LOADERS = 8, LA_WARPS = 7 + LA_LOADERS, LA_THREADS = 32 * LA_WARPS;
+constexpr int LA_CHUNK = LA_KEYS * 128;  // bytes of 64 dims of a tile, of a unit's queries, and of P
+constexpr int LA_ADDR = 3;    // tiles whose entries are looked up ahead
 
 struct LatentAttendParams {
     LatentView c;
@@ -18,126 +41,815 @@ struct LatentAttendParams {
     const int32_t* q_start;
     int64_t T;
     int max_q, max_kv, H;  // host bounds of new tokens and entries; query heads
+    int nht, hp, tpt;      // head tiles of a token, heads of one, tokens of a unit
     const int32_t* idx;    // [T][ld_idx], k entries a token, or null
     int64_t ld_idx;
     int k;
-    float sl2;             // scale * log2(e)
-    int causal;
+    float sl2;             // |scale| * log2(e), above 0
+    int causal, negate;    // negate: scale is negative
     void* out;
     int64_t ot, oh;
     float* lse;            // [T][H] or null
+    int runs;              // runs that the line is cut into, at most
+    int4* desc;            // [runs][nht]: the unit that begins in this run and ends in another: runs, first token, tokens
+    float* part;           // partial sums, latent_slot below
 };
 
-constexpr int LS_HEADS = 8, LS_KEYS = 16, LS_THREADS = 128;
-
-// Eight values of an entry in the cache's format as 16-bit numbers of type T; m is a multiple of 8.
-template <int FMT>
-__device__ __forceinline__ uint4 latent_load8(const uint8_t* e, int m, int dim) {
-    uint32_t o[4];
-    if constexpr (FMT == LF_FP8) {
-        const int codes = dim - LT_TAIL;
-        if (m >= codes) return __ldg(reinterpret_cast<const uint4*>(e + codes + 2 * (m - codes)));
-        decode8_fp8(__ldg(reinterpret_cast<const uint2*>(e + m)), __ldg(e + codes + 2 * LT_TAIL + m / 64), o);
-    } else if constexpr (FMT == LF_FP4) {
-        decode8_bf16(__ldg(reinterpret_cast<const uint32_t*>(e + m / 2)), __ldg(e + 256 + m / 16), o);
-    } else {
-        return __ldg(reinterpret_cast<const uint4*>(e + 2 * m));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+constexpr int LA_SLOT = LA_ROWS * (LT_VALUE + 2);  // floats: [row][512], maxima (base 2), sums
+// A run's partial sums: of a unit that began before it (0) and of one that goes on after it (1).
+__device__ __forceinline__ float* latent_slot(const LatentAttendParams& p, int run, int ht, int last) {
+    return p.part + (((int64_t)run * 2 + last) * p.nht + ht) * LA_SLOT;
 }
 
-// A block takes a token's eight heads and goes through its entries, 16 at a time: a thread
-// per (entry, head) for the scores, four value dims of all heads a thread for the sums.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(LS_THREADS) latent_attend_simple_kernel(const __grid_constant__ LatentAttendParams p) {
-    __shared__ uint4 s_e[LS_KEYS][576 / 8], s_q[LS_HEADS][576 / 8];
-    __shared__ float s_p[LS_HEADS][LS_KEYS];
+// Lengths of sequence b and what follows from them.
+struct LatentSeq {
+    int len, m, at, past, n_rt;
+    __device__ __forceinline__ void load(const LatentAttendParams& p, int b) {
+        len = latent_len(p.c, b, p.max_kv);
+        m = paged_new(p.q_start, b, p.max_q, p.T, &at);
+        past = len - m;
+        n_rt = (m + p.tpt - 1) / p.tpt;
+    }
+    // entries that some row of unit rt sees, and tiles of them: one where there are none, so that somebody writes its rows
+    __device__ __forceinline__ int seen(const LatentAttendParams& p, int rt) const {
+        return p.causal ? max(0, min(len, past + min(m, (rt + 1) * p.tpt))) : len;
+    }
+    __device__ __forceinline__ int tiles(const LatentAttendParams& p, int rt) const {
+        return max(1, (seen(p, rt) + LA_KEYS - 1) / LA_KEYS);
+    }
+    // tiles of the units before rt (rt <= n_rt)
+    __device__ __forceinline__ uint32_t before(const LatentAttendParams& p, int rt) const {
+        if (rt == 0) return 0u;
+        if (!p.causal) return (uint32_t)rt * tiles(p, 0);
+        // unit j - 1 sees past + j tpt entries, the last unit of all len
+        uint32_t sum = rt == n_rt ? tiles(p, rt - 1) : 0u;
+        const int n = rt == n_rt ? rt - 1 : rt;
+        const int none = past >= 0 ? 0 : min(n, -past / p.tpt);  // see nothing: a tile each
+        sum += none;
+        // sum over j of ceil((past + j tpt) / 64) for j = none + 1 .. n: the sum of (a j + b) less that of its
+        // residues, which go round the multiples of a's power of two
+        const int a = p.tpt, g = a & -a, per = LA_KEYS / g;
+        const uint64_t cnt = n - none, b = (uint64_t)(past + (int64_t)(none + 1) * a + LA_KEYS - 1);
+        uint64_t all = b * cnt + (cnt ? cnt * (cnt - 1) / 2 : 0) * a;
+        all -= cnt / per * ((uint64_t)per * (b & (g - 1)) + LA_KEYS / 2 * (per - 1));
+        for (uint64_t i = cnt / per * per; i < cnt; ++i) all -= (b + i * a) & (LA_KEYS - 1);
+        return sum + (uint32_t)(all / LA_KEYS);
+    }
+};
+
+// A walk along a block's run of the line: segment by segment, each a unit or the part of one that the run holds.
+// Whole warps.
+struct LatentWalk {
+    int left, b, rt, tile0;  // with lists rt is the token
+    LatentSeq q;
+    int n, nt, tok0, ntok;   // tiles of the segment and of the unit; its first token and its tokens
+    int seen;                // entries that some row of the unit sees
+
+    __device__ __forceinline__ bool begin(const LatentAttendParams& p) {
+        if (p.idx) {
+            for (;; left -= n, tile0 = 0, ++rt) {
+                if (left <= 0) return false;
+                nt = (p.k + LA_KEYS - 1) / LA_KEYS;
+                n = min(left, nt - tile0);
+                int32_t first, past;
+                b = token_seq_warp(p.q_start, p.c.B, rt, p.T, &first, &past);
+                if (b < 0) continue;  // a token of no sequence: its tiles are passed over
+                q.len = latent_len(p.c, b, p.max_kv);
+                q.past = q.len - (past - rt);
+                seen = p.causal ? max(0, min(q.len, q.past + 1)) : q.len;
+                tok0 = rt;
+                ntok = 1;
+                return true;
+            }
+        }
+        if (left <= 0) return false;
+        nt = q.tiles(p, rt);
+        n = min(left, nt - tile0);
+        seen = q.seen(p, rt);
+        tok0 = q.at + rt * p.tpt;
+        ntok = min(p.tpt, q.m - rt * p.tpt);
+        return true;
+    }
+    __device__ __forceinline__ void advance(const LatentAttendParams& p) {
+        left -= n;
+        tile0 = 0;
+        if (left <= 0) return;
+        ++rt;
+        if (p.idx || rt < q.n_rt) return;
+        rt = 0;
+        do q.load(p, ++b);  // there are tiles left, so a sequence that has some follows
+        while (q.n_rt == 0 && b + 1 < p.c.B);
+    }
+    __device__ __forceinline__ bool whole() const { return tile0 == 0 && n == nt; }
+    // entries that the unit's token i sees
+    __device__ __forceinline__ int sees(const LatentAttendParams& p, int i) const {
+        return p.idx ? seen : p.causal ? max(0, min(q.len, q.past + rt * p.tpt + i + 1)) : q.len;
+    }
+};
+
+template <int DIM>
+struct LatentCfg {
+    static constexpr int CHUNKS = DIM / 64, PAIRS = LT_VALUE / 128;
+    static constexpr int STAGE_BYTES = CHUNKS * LA_CHUNK;
+    static constexpr int P_OFF = CHUNKS * LA_CHUNK, KV_OFF = P_OFF + LA_CHUNK;
+    static constexpr int RING_BYTES = KV_OFF + 2 * STAGE_BYTES;
+    struct Tail {
+        uint64_t q_full, q_empty, s_full[2], p_full, p_empty, o_full, o_empty, meet, done;
+        uint64_t full[2][CHUNKS];      // a chunk is there
+        uint64_t empty[2][PAIRS + 1];  // 128 dims of a tile have been used; the dims past the value
+        uint64_t addr_full[LA_ADDR], addr_empty[LA_ADDR];
+        const uint8_t* entry[LA_ADDR][LA_KEYS];  // null: no such entry
+        uint32_t live[LA_ADDR][2];     // entries that there are
+        int end[LA_ADDR];              // no tile follows
+        int64_t row_out[LA_ROWS];      // where a row's result goes (elements), -1: nowhere
+        float factor[LA_ROWS];
+        uint32_t grew[2][4];
+        uint32_t tmem, total;
+        int abort;
+        int left, b, rt, tile;         // this block's run: tiles, and where it starts
+        LatentSeq q;
+    };
+    static constexpr int SMEM_BYTES = RING_BYTES + (int)sizeof(Tail);
+    static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
+};
+
+// Accumulators' columns of tensor memory: O^T in four of 64, S in two of 64.
+constexpr uint32_t LA_S_COL = 256;
+
+// 64 columns of 16 lanes, as matrix fragments: register 4 g + 2 h + x is column 8 g + 2 (lane & 3) + x of row
+// (lane >> 2) + 8 h.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    tmem_ld_wait(r);
+}
+
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// 16 bytes into shared memory without waiting, zeros where src is null.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, const void* any) {
+    const int bytes = src ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src : any), "r"(bytes) : "memory");
+}
+// An arrival on `bar` once all copies of this thread so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The line: its length, then where this block's run starts. One warp.
+template <typename Tail>
+__device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run, Tail& s) {
+    const int lane = threadIdx.x & 31;
+    if (p.idx) {
+        const uint32_t nt = (p.k + LA_KEYS - 1) / LA_KEYS;
+        const Line line((uint32_t)p.T * nt, p.runs);
+        if (lane == 0) {
+            s.total = line.total;
+            const uint32_t x = line.cut(run);
+            s.left = run < (int)line.G ? (int)(line.cut(run + 1) - x) : 0;
+            s.rt = x / nt;
+            s.tile = x % nt;
+        }
+        return;
+    }
+    LatentSeq mine;
+    const auto load = [&](int b0) {  // tiles of sequence b0 + lane
+        mine.n_rt = 0;
+        if (b0 + lane < p.c.B) mine.load(p, b0 + lane);
+        return mine.n_rt ? mine.before(p, mine.n_rt) : 0u;
+    };
+    const auto upto = [&](uint32_t n) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(~0u, n, o);
+            if (lane >= o) n += up;
+        }
+        return n;
+    };
+    uint32_t total = 0, n = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        n = load(b0);
+        total += __reduce_add_sync(~0u, n);
+    }
+    const Line line(total, p.runs);
+    const uint32_t x = line.cut(run);
+    if (lane == 0) {
+        s.total = total;
+        s.left = run < (int)line.G ? (int)(line.cut(run + 1) - x) : 0;
+    }
+    if (run >= (int)line.G) return;
+    uint32_t first = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        if (p.c.B > 32) n = load(b0);
+        const uint32_t sum = upto(n), f = first + sum - n;
+        const uint32_t has = __ballot_sync(~0u, x >= f && x < f + n);
+        first += __shfl_sync(~0u, sum, 31);
+        if (!has) continue;
+        const int at = __ffs(has) - 1;
+        LatentSeq q;
+        q.len = __shfl_sync(~0u, mine.len, at);
+        q.m = __shfl_sync(~0u, mine.m, at);
+        q.at = __shfl_sync(~0u, mine.at, at);
+        q.past = __shfl_sync(~0u, mine.past, at);
+        q.n_rt = __shfl_sync(~0u, mine.n_rt, at);
+        const uint32_t off = x - __shfl_sync(~0u, f, at);
+        // the last unit that starts at or before the tile, by 32 guesses at a time
+        int lo = 0, hi = q.n_rt;  // before(lo) <= off < before(hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, guess = lo + step * lane;
+            const uint32_t ok = __ballot_sync(~0u, guess < hi && (lane == 0 || q.before(p, guess) <= off));
+            lo += step * (31 - __clz(ok));
+            hi = min(hi, lo + step);
+        }
+        const uint32_t start = q.before(p, lo);
+        if (lane == 0) {
+            s.b = b0 + at;
+            s.rt = lo;
+            s.tile = (int)(off - start);
+            s.q = q;
+        }
+        return;
+    }
+}
+
+template <typename T, int DIM, int FMT>
+__global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
+    using C = LatentCfg<DIM>;
+    extern __shared__ __align__(1024) uint8_t ring[];
+    typename C::Tail& s = *reinterpret_cast<typename C::Tail*>(ring + C::RING_BYTES);
+    uint8_t* const q_smem = ring;
+    uint8_t* const p_smem = ring + C::P_OFF;
+    uint8_t* const kv_smem = ring + C::KV_OFF;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
+    constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
+
+    if (threadIdx.x == 0) {
+        mbar_init(&s.q_full, 32), mbar_init(&s.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.s_full[i], 1);
+            for (int c = 0; c < C::CHUNKS; ++c) mbar_init(&s.full[i][c], PLAIN ? 32 : LA_LOADERS);
+            for (int c = 0; c <= C::PAIRS; ++c) mbar_init(&s.empty[i][c], 1);
+        }
+        mbar_init(&s.p_full, 4), mbar_init(&s.p_empty, 1);
+        mbar_init(&s.o_full, 1), mbar_init(&s.o_empty, 4);
+        for (int i = 0; i < LA_ADDR; ++i) mbar_init(&s.addr_full[i], 1), mbar_init(&s.addr_empty[i], 4 + LA_LOADERS);
+        mbar_init(&s.meet, 4), mbar_init(&s.done, 1);
+        fence_mbar_init();
+        s.abort = 0;
+    }
+    if (warp == 4) tmem_alloc(&s.tmem, 512);
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t t = blockIdx.x;
-    const int dim = p.c.dim, vecs = dim / 8, h0 = blockIdx.y * LS_HEADS;
-    int32_t first, past;
-    const int b = token_seq_warp(p.q_start, p.c.B, t, p.T, &first, &past);
-    if (b < 0) return;
-    const int len = latent_len(p.c, b, p.max_kv);
-    const int seen = p.causal ? min(len, len - (past - (int)t) + 1) : len;
-    const int n = p.idx ? p.k : max(seen, 0);
-    for (int i = threadIdx.x; i < LS_HEADS * vecs; i += LS_THREADS) {
-        const int h = h0 + i / vecs;
-        s_q[i / vecs][i % vecs] = h < p.H ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + t * p.qt +
-                                                                                 h * p.qh) + i % vecs)
-                                          : make_uint4(0u, 0u, 0u, 0u);
-    }
-    const int me = threadIdx.x % LS_KEYS, mh = threadIdx.x / LS_KEYS;  // the score of this thread
-    float m = -INFINITY, l = 0.f, acc[LS_HEADS][4] = {};
-    for (int k0 = 0; k0 < n; k0 += LS_KEYS) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < LS_KEYS * vecs; i += LS_THREADS) {
-            const int j = k0 + i / vecs;
-            int e = -1;
-            if (j < n) e = p.idx ? __ldg(p.idx + t * p.ld_idx + j) : j;
-            if (e >= seen) {
-                raise_error(DEVERR_ARG);
-                e = -1;
-            }
-            const uint8_t* at = e >= 0 ? latent_entry(p.c, b, e) : nullptr;
-            s_e[i / vecs][i % vecs] = at ? latent_load8<FMT>(at, i % vecs * 8, dim) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        __syncthreads();
-        float s = 0.f;
-        for (int v = 0; v < vecs; ++v) {
-            const uint32_t *a = &s_e[me][v].x, *q = &s_q[mh][v].x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 x = unpack2<T>(a[j]), y = unpack2<T>(q[j]);
-                s += x.x * y.x + x.y * y.y;
-            }
-        }
-        s *= p.sl2;
-        const int j = k0 + me;
-        if (j >= n || (p.idx && (uint32_t)__ldg(p.idx + t * p.ld_idx + j) >= (uint32_t)max(seen, 0))) s = -INFINITY;
-        float top = s;
-#pragma unroll
-        for (int o = 1; o < LS_KEYS; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        top = fmaxf(top, m);
-        const float f = m == -INFINITY ? 1.f : ex2(m - top), pe = s == -INFINITY ? 0.f : ex2(s - top);
-        float sum = pe;
-#pragma unroll
-        for (int o = 1; o < LS_KEYS; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        l = l * f + sum;
-        m = top;
-        s_p[mh][me] = pe;
-        __shared__ float s_f[LS_HEADS];
-        if (me == 0) s_f[mh] = f;
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < LS_HEADS; ++h)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) acc[h][d] *= s_f[h];
-        for (int e = 0; e < LS_KEYS; ++e) {
-            const uint2 w = *(reinterpret_cast<const uint2*>(s_e[e]) + threadIdx.x);
-            const float2 a = unpack2<T>(w.x), c = unpack2<T>(w.y);
-#pragma unroll
-            for (int h = 0; h < LS_HEADS; ++h) {
-                const float pe2 = s_p[h][e];
-                acc[h][0] += pe2 * a.x;
-                acc[h][1] += pe2 * a.y;
-                acc[h][2] += pe2 * c.x;
-                acc[h][3] += pe2 * c.y;
-            }
-        }
-    }
-    __shared__ float s_l[LS_HEADS];
-    if (me == 0) {
-        s_l[mh] = l;
-        if (p.lse && h0 + mh < p.H) p.lse[t * p.H + h0 + mh] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-    }
+    if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == 0) latent_line(p, run, s);
+    tc_fence_before();
     __syncthreads();
-    for (int h = 0; h < LS_HEADS && h0 + h < p.H; ++h) {
-        const float li = s_l[h], inv = li > 0.f || li != li ? 1.f / li : 0.f;
-        *(reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.ot + (h0 + h) * p.oh) + threadIdx.x) =
-            make_uint2(pack2<T>(acc[h][0] * inv, acc[h][1] * inv), pack2<T>(acc[h][2] * inv, acc[h][3] * inv));
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    LatentWalk k;
+    k.left = s.left;
+    k.b = s.b;
+    k.rt = s.rt;
+    k.tile0 = s.tile;
+    k.q = s.q;
+    bool ok = true;  // false once a wait has run out: the role ends, after what it has in flight
+
+    if (warp < 4) {  // softmax: rows ra and ra + 8, a quarter of their columns each lane
+        constexpr float SHIFT = P_SHIFT<T> ? P_SHIFT<T> - CH_LAZY : 0.f;  // p up to 2^CH_LAZY of its own
+        const int ra = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
+        const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+        uint32_t it = 0, seg = 0, met = 0;  // tiles, segments and meetings so far
+        // the four warps come together, by a wait that may run out
+        const auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.meet);
+            __syncwarp();
+            ok = __all_sync(~0u, wait_bounded(&s.meet, met & 1, &s.abort));
+            ++met;
+            return ok;
+        };
+        for (; ok && k.begin(p); k.advance(p), ++seg) {
+            if (threadIdx.x < LA_ROWS) {
+                const int i = threadIdx.x / p.hp, h = ht * p.hp + threadIdx.x % p.hp;
+                s.row_out[threadIdx.x] = i < k.ntok && h < p.H ? (int64_t)(k.tok0 + i) * p.ot + (int64_t)h * p.oh : -1;
+            }
+            int lim[2];
+            float m_used[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = (ra + 8 * h) / p.hp;
+                lim[h] = p.idx ? INT32_MAX : k.sees(p, min(i, k.ntok - 1));
+            }
+            const int lim_all = p.idx ? INT32_MAX : k.sees(p, 0);  // entries that every row sees
+            for (int i = 0; i < k.n && ok; ++i, ++it) {
+                const int k0 = (k.tile0 + i) * LA_KEYS, a = it % LA_ADDR;
+                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort) &&
+                                         wait_bounded(&s.s_full[it & 1], it / 2 & 1, &s.abort));
+                if (!ok) break;
+                const uint32_t live[2] = {s.live[a][0], s.live[a][1]};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.addr_empty[a]);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t r[32];
+                tmem_ld_16x64(tmem + quarter + LA_S_COL + (it & 1) * LA_KEYS, r);
+                if ((live[0] & live[1]) != ~0u || k0 + LA_KEYS > lim_all) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int col = 8 * (j >> 2) + c0 + (j & 1);
+                        const bool sees = (live[j >> 4] >> (col & 31) & 1) && (p.idx || k0 + col < lim[j >> 1 & 1]);
+                        r[j] = sees ? r[j] : 0xFF800000u;
+                    }
+                }
+                float mt[2];
+                bool grew = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = fmaxf(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
+#pragma unroll
+                    for (int g = 1; g < 8; ++g)
+                        top = max3(top, __uint_as_float(r[4 * g + 2 * h]), __uint_as_float(r[4 * g + 2 * h + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    mt[h] = top * p.sl2;  // p.sl2 > 0
+                    grew = grew || mt[h] > m_used[h] + CH_LAZY;
+                }
+                // a row whose maximum has grown: all warps rescale O's columns, as each holds all rows of its dims
+                const uint32_t any = __ballot_sync(~0u, grew);
+                if (lane == 0) s.grew[it & 1][warp] = any;
+                if (!meet()) break;
+                const uint32_t some = s.grew[it & 1][0] | s.grew[it & 1][1] | s.grew[it & 1][2] | s.grew[it & 1][3];
+                if (some) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float m_new = mt[h] > m_used[h] + CH_LAZY ? mt[h] : m_used[h];
+                        const float f = m_new == -INFINITY ? 1.f : ex2(m_used[h] - m_new);
+                        l[h] *= f;
+                        m_used[h] = m_new;
+                        if ((lane & 3) == 0) s.factor[ra + 8 * h] = f;
+                    }
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float base = m_used[h] == -INFINITY ? 0.f : m_used[h] - SHIFT;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const float x = ex2(fmaf(__uint_as_float(r[4 * g + 2 * h]), p.sl2, -base));
+                        const float y = ex2(fmaf(__uint_as_float(r[4 * g + 2 * h + 1]), p.sl2, -base));
+                        sum += x + y;
+                        pk[2 * g + h] = pack2<T>(x, y);
+                    }
+                    l[h] += sum;
+                }
+                // P's place is free, and O at rest, once the last tile's product is done
+                ok = __all_sync(~0u, wait_bounded(&s.p_empty, (it & 1) ^ 1, &s.abort));
+                if (!ok) break;
+                if (some) {
+                    if (!meet()) break;
+                    if (i > 0) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32_issue(tmem + quarter + c * 32, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * s.factor[(c & 1) * 32 + j]);
+                            tmem_st32(tmem + quarter + c * 32, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    if (!meet()) break;  // the factors have been read
+                }
+                const int row = 16 * warp + (lane & 15), g1 = lane >> 4;
+                const uint32_t dst = smem_u32(p_smem) + row * 128;
+#pragma unroll
+                for (int g = 0; g < 8; g += 2)
+                    stmatrix_x4(dst + (((g + g1) ^ (row & 7)) << 4), pk[2 * g], pk[2 * g + 1], pk[2 * g + 2], pk[2 * g + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full);
+                __syncwarp();
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(~0u, l[h], 1);
+                l[h] += __shfl_xor_sync(~0u, l[h], 2);
+                m_used[h] -= SHIFT;  // what the sums are by
+                if ((lane & 3) == 0) s.factor[ra + 8 * h] = l[h] > 0.f || l[h] != l[h] ? 1.f / l[h] : 0.f;
+            }
+            const bool whole = k.whole();
+            float* slot = latent_slot(p, run, ht, k.tile0 == 0);
+            if ((lane & 3) == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = ra + 8 * h;
+                    if (!whole) {
+                        slot[LA_ROWS * LT_VALUE + row] = m_used[h];
+                        slot[LA_ROWS * (LT_VALUE + 1) + row] = l[h];
+                    } else if (p.lse && s.row_out[row] >= 0) {
+                        p.lse[(int64_t)(k.tok0 + row / p.hp) * p.H + ht * p.hp + row % p.hp] =
+                            l[h] == 0.f ? -INFINITY : (m_used[h] + log2f(l[h])) * LN2;
+                    }
+                }
+            }
+            if (!whole && k.tile0 == 0 && threadIdx.x == 0) {  // the unit goes on in later runs
+                const Line line(s.total, p.runs);
+                const int last = (int)line.run(line.cut(run + 1) + (k.nt - k.n) - 1);
+                p.desc[blockIdx.x] = make_int4(last - run + 1, k.tok0, k.ntok, 0);
+            }
+            if (!meet()) break;  // factors and rows are there
+            ok = __all_sync(~0u, wait_bounded(&s.o_full, seg & 1, &s.abort));
+            if (!ok) break;
+            tc_fence_after();
+            const int rows = k.ntok * p.hp;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                const int col0 = (c & 1) * 32, d = (c >> 1) * 128 + warp * 32 + lane;
+                if (col0 >= rows) continue;
+                __syncwarp();
+                uint32_t o[32];
+                tmem_ld32_issue(tmem + quarter + c * 32, o);
+                tmem_ld_wait(o);
+                if (!whole) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col0 + j < rows) slot[(col0 + j) * LT_VALUE + d] = __uint_as_float(o[j]);
+                } else {
+                    // two rows at a time: an even lane stores two dims of the first, an odd one of the second
+                    T* const out = static_cast<T*>(p.out) + (d & ~1);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float x = __uint_as_float(o[j]) * s.factor[col0 + j];
+                        const float y = __uint_as_float(o[j + 1]) * s.factor[col0 + j + 1];
+                        const float z = __shfl_xor_sync(~0u, lane & 1 ? x : y, 1);
+                        const uint32_t v = lane & 1 ? pack2<T>(z, y) : pack2<T>(x, z);
+                        const int64_t to = s.row_out[col0 + j + (lane & 1)];
+                        if (to >= 0) *reinterpret_cast<uint32_t*>(out + to) = v;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!meet()) break;  // rows and factors have been read
+            if (lane == 0) mbar_arrive(&s.o_empty);
+        }
+    } else if (warp == 4) {  // products: the warp waits, one lane issues
+        constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, LA_ROWS, false) | 1u << 15;  // A = V^T, MN-major
+        const uint32_t id_s = idesc_f16(is_bf16<T>, LA_ROWS, LA_KEYS, false) | (p.negate ? 1u << 13 : 0u);  // of -Q
+        constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
+        const uint32_t tm = uniform(tmem);
+        const uint32_t q_desc = smem_desc_sw128(smem_u32(q_smem)), k_desc = smem_desc_sw128(smem_u32(kv_smem)),
+                       v_desc = smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK), p_desc = smem_desc_sw128(smem_u32(p_smem));
+        uint32_t it = 0, seg = 0;
+        const auto product_s = [&](uint32_t i) {
+            const uint32_t st = uniform(i & 1), d = tm + LA_S_COL + st * LA_KEYS, kd = k_desc + st * STAGE16;
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c) {
+                ok = ok && wait_bounded(&s.full[st][c], i / 2 & 1, &s.abort);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    return;
+                }
+                fence_proxy_async_smem();  // copies of other warps, then the tensor cores
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t off = c * CHUNK16 + ks * 2;
+                        if (c == 0 && ks == 0) mma_f16_ss(d, q_desc, kd, id_s);
+                        else mma_f16_ss_add(d, q_desc + off, kd + off, id_s);
+                    }
+                }
+                __syncwarp();
+            }
+            if (elect_one()) {
+                tc_commit(&s.s_full[st]);
+                if (C::CHUNKS > 2 * C::PAIRS) tc_commit(&s.empty[st][C::PAIRS]);
+            }
+            __syncwarp();
+        };
+        for (; ok && k.begin(p); k.advance(p), ++seg) {
+            ok = __all_sync(~0u, wait_bounded(&s.q_full, seg & 1, &s.abort));
+            if (!ok) break;
+            product_s(it);
+            for (int i = 0; i < k.n && ok; ++i, ++it) {
+                if (i + 1 < k.n) product_s(it + 1);
+                else if (elect_one()) tc_commit(&s.q_empty);
+                __syncwarp();
+                if (!ok) break;
+                ok = wait_bounded(&s.p_full, it & 1, &s.abort);
+                if (i == 0) ok = ok && wait_bounded(&s.o_empty, (seg & 1) ^ 1, &s.abort);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t st = uniform(it & 1), vd = v_desc + st * STAGE16, more = uniform((uint32_t)i);
+                if (elect_one()) {
+#pragma unroll
+                    for (int m = 0; m < C::PAIRS; ++m) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint32_t a = vd + 2 * m * CHUNK16 + ks * 128, b = p_desc + ks * 2;
+                            if (ks == 0 && more == 0) mma_f16_ss(tm + m * 64, a, b, id_o);
+                            else mma_f16_ss_add(tm + m * 64, a, b, id_o);
+                        }
+                        tc_commit(&s.empty[st][m]);
+                    }
+                    tc_commit(&s.p_empty);
+                    if (i + 1 == k.n) tc_commit(&s.o_full);
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) {
+            tc_commit(&s.done);
+            wait_drain(&s.done, 0);
+        }
+    } else if (warp == 5) {  // entries: where the tiles' rows are
+        uint32_t it = 0;
+        for (; ok && k.begin(p); k.advance(p)) {
+            for (int i = 0; i < k.n && ok; ++i, ++it) {
+                const int k0 = (k.tile0 + i) * LA_KEYS, a = it % LA_ADDR;
+                const uint8_t* at[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = k0 + 32 * h + lane;
+                    int e = j < k.seen ? j : -1;
+                    if (p.idx) {
+                        e = j < p.k ? __ldg(p.idx + (int64_t)k.tok0 * p.ld_idx + j) : -1;
+                        if (e >= k.seen) {
+                            raise_error(DEVERR_ARG);
+                            e = -1;
+                        }
+                    }
+                    at[h] = e >= 0 ? latent_entry(p.c, k.b, e) : nullptr;
+                }
+                ok = __all_sync(~0u, wait_bounded(&s.addr_empty[a], (it / LA_ADDR & 1) ^ 1, &s.abort));
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    s.entry[a][32 * h + lane] = at[h];
+                    const uint32_t live = __ballot_sync(~0u, at[h] != nullptr);
+                    if (lane == 0) s.live[a][h] = live;
+                }
+                if (lane == 0) s.end[a] = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.addr_full[a]);
+            }
+        }
+        if (ok) {
+            const int a = it % LA_ADDR;
+            ok = __all_sync(~0u, wait_bounded(&s.addr_empty[a], (it / LA_ADDR & 1) ^ 1, &s.abort));
+            if (ok && lane == 0) {
+                s.end[a] = 1;
+                mbar_arrive(&s.addr_full[a]);
+            }
+        }
+    } else if (warp == 6) {  // queries, a unit at a time
+        const T* const q = static_cast<const T*>(p.q);
+        uint32_t seg = 0;
+        for (; ok && k.begin(p); k.advance(p), ++seg) {
+            ok = __all_sync(~0u, wait_bounded(&s.q_empty, (seg & 1) ^ 1, &s.abort));
+            if (!ok) break;
+            const int j = lane & 7;
+#pragma unroll 1
+            for (int r = lane >> 3; r < LA_ROWS; r += 4) {
+                const int i = r / p.hp, h = ht * p.hp + r % p.hp;
+                const T* src = i < k.ntok && h < p.H ? q + (int64_t)(k.tok0 + i) * p.qt + (int64_t)h * p.qh + 8 * j : nullptr;
+                const uint32_t dst = smem_u32(q_smem) + r * 128 + ((j ^ (r & 7)) << 4);
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) cp_async16(dst + c * LA_CHUNK, src ? src + c * 64 : nullptr, q);
+            }
+            if (!(seg == 0 && *(volatile int*)&g_hsi_skip_first_copy)) cp_async_arrive(&s.q_full);
+        }
+        cp_async_wait_all();
+    } else {  // entries' values
+        const int w = warp - 7;
+        uint32_t it = 0;
+        if constexpr (PLAIN) {
+            uint32_t n = 0;  // chunks so far: each warp takes every eighth
+            for (;; ++it) {
+                const int a = it % LA_ADDR, st = it & 1;
+                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
+                if (!ok || s.end[a]) break;
+#pragma unroll 1
+                for (int c = 0; c < C::CHUNKS; ++c, ++n) {
+                    if ((int)(n % LA_LOADERS) != w) continue;
+                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][c >> 1], (it / 2 & 1) ^ 1, &s.abort));
+                    if (!ok) break;
+                    const int j = lane & 7;
+                    const uint32_t dst = smem_u32(kv_smem) + st * C::STAGE_BYTES + c * LA_CHUNK;
+#pragma unroll
+                    for (int r0 = 0; r0 < LA_KEYS; r0 += 4) {
+                        const int r = r0 + (lane >> 3);
+                        const uint8_t* e = s.entry[a][r];
+                        cp_async16(dst + r * 128 + ((j ^ (r & 7)) << 4), e ? e + c * 128 + j * 16 : nullptr, p.c.data);
+                    }
+                    cp_async_arrive(&s.full[st][c]);
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.addr_empty[a]);
+            }
+            cp_async_wait_all();
+        } else {
+            const int tid = threadIdx.x - 7 * 32;
+            constexpr int CODES = FMT == LF_FP8 ? DIM - LT_TAIL : DIM;
+            // FP8: 16 codes of rows tid / 8 and + 32 a step of 128 values, FP4: 32 codes of row tid / 4; a step
+            // of the next tile is loaded when the registers of this one's are free
+            constexpr int R = FMT == LF_FP8 ? 2 : 1;
+            const int row = FMT == LF_FP8 ? tid >> 3 : tid >> 2, j = FMT == LF_FP8 ? tid & 7 : tid & 3;
+            uint4 v[4][R], tail[R];
+            uint2 scale[R];
+            uint32_t scale4[4];
+            const uint8_t* e[R];
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            const auto load = [&](int step) {
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    if constexpr (FMT == LF_FP8) {
+                        const int m = 128 * step + 16 * j;
+                        v[step][x] = e[x] && m < CODES ? __ldg(reinterpret_cast<const uint4*>(e[x] + m)) : zero;
+                    } else {
+                        v[step][x] = e[x] ? __ldg(reinterpret_cast<const uint4*>(e[x] + 64 * step + 16 * j)) : zero;
+                        scale4[step] = e[x] ? __ldg(reinterpret_cast<const uint16_t*>(e[x] + 256 + 8 * step + 2 * j)) : 0u;
+                    }
+                }
+            };
+            const auto load_tail = [&]() {
+                if constexpr (FMT == LF_FP8) {
+#pragma unroll
+                    for (int x = 0; x < R; ++x) {
+                        tail[x] = e[x] ? __ldg(reinterpret_cast<const uint4*>(e[x] + CODES + 16 * j)) : zero;
+                        scale[x] = e[x] ? __ldg(reinterpret_cast<const uint2*>(e[x] + CODES + 2 * LT_TAIL)) : make_uint2(0u, 0u);
+                    }
+                }
+            };
+            // the next tile's rows; false at the end
+            const auto rows = [&](uint32_t i) {
+                const int a = i % LA_ADDR;
+                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], i / LA_ADDR & 1, &s.abort));
+                if (!ok || s.end[a]) return false;
+#pragma unroll
+                for (int x = 0; x < R; ++x) e[x] = s.entry[a][row + 32 * x];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.addr_empty[a]);
+                return true;
+            };
+            bool more = rows(0);
+            if (more) {
+                load_tail();
+#pragma unroll
+                for (int step = 0; step < 4; ++step) load(step);
+            }
+            while (more) {
+                const int st = it & 1;
+                const uint32_t base = smem_u32(kv_smem) + st * C::STAGE_BYTES;
+                const auto put = [&](int r, int m, const uint32_t (&o)[4]) {  // eight values from dim m on
+                    const uint32_t dst = base + (m >> 6) * LA_CHUNK + r * 128 + (((m >> 3 & 7) ^ (r & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                                 "r"(o[3])
+                                 : "memory");
+                };
+                const auto there = [&](int c) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.full[st][c]);
+                };
+                uint2 sc[R];
+                uint4 tl[R];
+#pragma unroll
+                for (int x = 0; x < R; ++x) sc[x] = scale[x], tl[x] = tail[x];
+                more = rows(it + 1);
+                if (!ok) break;
+                if (more) load_tail();
+#pragma unroll
+                for (int step = 0; step < 4; ++step) {
+                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][step], (it / 2 & 1) ^ 1, &s.abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int x = 0; x < R; ++x) {
+                        uint32_t o[4];
+                        if constexpr (FMT == LF_FP8) {
+                            const int m = 128 * step + 16 * j;
+                            if (m < CODES) {
+                                const uint32_t both = step < 2 ? sc[x].x : sc[x].y;
+                                const uint32_t byte = both >> (16 * (step & 1) + 8 * (j >> 2)) & 0xFFu;
+                                decode8_fp8(make_uint2(v[step][x].x, v[step][x].y), byte, o);
+                                put(row + 32 * x, m, o);
+                                decode8_fp8(make_uint2(v[step][x].z, v[step][x].w), byte, o);
+                                put(row + 32 * x, m + 8, o);
+                            }
+                            if (DIM == LT_VALUE && step == 3) {  // the tail is the value's last chunk
+                                const uint32_t t[4] = {tl[x].x, tl[x].y, tl[x].z, tl[x].w};
+                                put(row + 32 * x, CODES + 8 * j, t);
+                            }
+                        } else {
+                            const int m = 128 * step + 32 * j;
+                            const uint32_t lo = scale4[step] & 0xFFu, hi = scale4[step] >> 8;
+                            decode8_bf16(v[step][x].x, lo, o);
+                            put(row, m, o);
+                            decode8_bf16(v[step][x].y, lo, o);
+                            put(row, m + 8, o);
+                            decode8_bf16(v[step][x].z, hi, o);
+                            put(row, m + 16, o);
+                            decode8_bf16(v[step][x].w, hi, o);
+                            put(row, m + 24, o);
+                        }
+                    }
+                    there(2 * step);
+                    if (lane == 0) mbar_arrive(&s.full[st][2 * step + 1]);
+                    if (more) load(step);
+                }
+                if (!ok) break;
+                if constexpr (FMT == LF_FP8 && DIM > LT_VALUE) {
+                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][C::PAIRS], (it / 2 & 1) ^ 1, &s.abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int x = 0; x < R; ++x) {
+                        const uint32_t t[4] = {tl[x].x, tl[x].y, tl[x].z, tl[x].w};
+                        put(row + 32 * x, CODES + 8 * j, t);
+                    }
+                    there(C::CHUNKS - 1);
+                }
+                ++it;
+            }
+        }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tmem, 512);
+}
+
+// Joins the units that several runs hold: a block per run, head tile and row, four dims a thread.
+template <typename T>
+__global__ void __launch_bounds__(LT_VALUE / 4) latent_join_kernel(const __grid_constant__ LatentAttendParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int row = blockIdx.x, run = blockIdx.y / p.nht, ht = blockIdx.y % p.nht;
+    const int4 unit = p.desc[blockIdx.y];
+    const int i = row / p.hp, h = ht * p.hp + row % p.hp;
+    if (unit.x == 0 || i >= unit.z || h >= p.H) return;
+    constexpr int AT_ONCE = 8;  // runs whose loads are in flight
+    float m = -INFINITY, l = 0.f;
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < unit.x; c0 += AT_ONCE) {
+        float mc[AT_ONCE], lc[AT_ONCE];
+        float4 oc[AT_ONCE];
+#pragma unroll
+        for (int c = 0; c < AT_ONCE; ++c) {
+            mc[c] = -INFINITY;
+            lc[c] = 0.f;
+            if (c0 + c >= unit.x) continue;
+            const float* slot = latent_slot(p, run + c0 + c, ht, c0 + c == 0);
+            mc[c] = slot[LA_ROWS * LT_VALUE + row];
+            lc[c] = slot[LA_ROWS * (LT_VALUE + 1) + row];
+            oc[c] = reinterpret_cast<const float4*>(slot + row * LT_VALUE)[threadIdx.x];
+        }
+        float top = m;
+#pragma unroll
+        for (int c = 0; c < AT_ONCE; ++c) top = fmaxf(top, mc[c]);
+        const float keep = part_factor(m, top);
+        m = top;
+        l *= keep;
+        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+        for (int c = 0; c < AT_ONCE; ++c) {
+            if (lc[c] == 0.f) continue;  // past the runs, or a part that this row does not see
+            const float f = part_factor(mc[c], m);
+            l += f * lc[c];
+            o.x += f * oc[c].x;
+            o.y += f * oc[c].y;
+            o.z += f * oc[c].z;
+            o.w += f * oc[c].w;
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int64_t t = unit.y + i;
+    *(reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.ot + (int64_t)h * p.oh) + threadIdx.x) =
+        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (threadIdx.x == 0 && p.lse) p.lse[t * p.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 }  // namespace hsi
