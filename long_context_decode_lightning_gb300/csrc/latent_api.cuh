@@ -76,7 +76,7 @@ hsi_status launch_latent_attend(const LatentAttendParams& p, cudaStream_t s) {
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(latent_attend_kernel<T, DIM, FMT>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
     const unsigned grid = (unsigned)(p.runs * p.nht);
-    const hsi_status st = launch(latent_attend_kernel<T, DIM, FMT>, dim3(grid), dim3(LA_THREADS), C::SMEM_BYTES, s, p);
+    const hsi_status st = launch(latent_attend_kernel<T, DIM, FMT>, dim3(grid), dim3(latent_threads(FMT)), C::SMEM_BYTES, s, p);
     if (st != HSI_OK || p.runs == 1) return st;
     return launch(latent_join_kernel<T>, dim3(p.tpt * p.hp, grid), dim3(LT_VALUE / 4), 0, s, p);
 }

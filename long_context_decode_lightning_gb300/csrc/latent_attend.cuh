@@ -13,7 +13,7 @@
 // memory and leave nothing for S: transposed they are four accumulators of 128
 // dims by 64 columns. A row's rescaling (lazy, as in attend_chunk.cuh) is one of columns then.
 //
-// Warps: four turn S into P and write results, one issues products, one looks
+// Warps: four turn S into P and write results, two issue products, one looks
 // entries up (lists, pages) a few tiles ahead, one brings the queries, and
 // eight bring the entries chunk by chunk, decoding FP8 and FP4 on the way.
 // The units' tiles form one line that is cut into equal runs, one per CTA; a
@@ -30,7 +30,17 @@ namespace hsi {
 
 constexpr int LA_ROWS = 64;   // rows of a unit
 constexpr int LA_KEYS = 64;   // entries of a tile
-constexpr int LA_LOADERS = 8, LA_WARPS = 7 + LA_LOADERS, LA_THREADS = 32 * LA_WARPS;
+#ifndef LA_S_GROUPS
+#define LA_S_GROUPS 2
+#endif
+#ifndef LA_PLAIN_LOADERS
+#define LA_PLAIN_LOADERS 4
+#endif
+#ifndef LA_PACE_CLK
+#define LA_PACE_CLK 0
+#endif
+__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? LA_PLAIN_LOADERS : 8; }
+__host__ __device__ constexpr int latent_threads(int fmt) { return 32 * (8 + latent_loaders(fmt)); }
 constexpr int LA_CHUNK = LA_KEYS * 128;  // bytes of 64 dims of a tile, of a unit's queries, and of P
 constexpr int LA_ADDR = 3;    // tiles whose entries are looked up ahead
 
@@ -150,20 +160,23 @@ struct LatentWalk {
 template <int DIM>
 struct LatentCfg {
     static constexpr int CHUNKS = DIM / 64, PAIRS = LT_VALUE / 128;
-    static constexpr int STAGE_BYTES = CHUNKS * LA_CHUNK;
-    static constexpr int P_OFF = CHUNKS * LA_CHUNK, KV_OFF = P_OFF + LA_CHUNK;
-    static constexpr int RING_BYTES = KV_OFF + 2 * STAGE_BYTES;
+    // a stage holds a tile: eight chunks of the value, then one of the dims past it, in whose place P comes once S is done
+    static constexpr int STAGE_BYTES = (2 * PAIRS + 1) * LA_CHUNK, P_OFF = 2 * PAIRS * LA_CHUNK;
+    static constexpr int KV_OFF = CHUNKS * LA_CHUNK, RING_BYTES = KV_OFF + 2 * STAGE_BYTES;
+    // S is issued by groups of chunks
+    static constexpr int GROUPS = LA_S_GROUPS, GROUP = (CHUNKS + GROUPS - 1) / GROUPS;
+    __host__ __device__ static constexpr int in_group(int g) { return g + 1 < GROUPS ? GROUP : CHUNKS - g * GROUP; }
     struct Tail {
-        uint64_t q_full, q_empty, s_full[2], p_full, p_empty, o_full, o_empty, meet, done;
-        uint64_t full[2][CHUNKS];      // a chunk is there
-        uint64_t empty[2][PAIRS + 1];  // 128 dims of a tile have been used; the dims past the value
+        uint64_t q_full, q_empty, s_full[2], p_full[2], o_empty, done[2];
+        uint64_t full[2][GROUPS];      // the entries' dims of a group are there
+        uint64_t empty[2][PAIRS];      // 128 dims of a tile have been used (with the last: all of it, and O is at rest)
         uint64_t addr_full[LA_ADDR], addr_empty[LA_ADDR];
         const uint8_t* entry[LA_ADDR][LA_KEYS];  // null: no such entry
         uint32_t live[LA_ADDR][2];     // entries that there are
         int end[LA_ADDR];              // no tile follows
         int64_t row_out[LA_ROWS];      // where a row's result goes (elements), -1: nowhere
         float factor[LA_ROWS];
-        uint32_t grew[2][4];
+        uint32_t vote[2][4];
         uint32_t tmem, total;
         int abort;
         int left, b, rt, tile;         // this block's run: tiles, and where it starts
@@ -287,28 +300,27 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
 }
 
 template <typename T, int DIM, int FMT>
-__global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
+__global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
     using C = LatentCfg<DIM>;
     extern __shared__ __align__(1024) uint8_t ring[];
     typename C::Tail& s = *reinterpret_cast<typename C::Tail*>(ring + C::RING_BYTES);
     uint8_t* const q_smem = ring;
-    uint8_t* const p_smem = ring + C::P_OFF;
     uint8_t* const kv_smem = ring + C::KV_OFF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
+    constexpr int LOADERS = latent_loaders(FMT);
     constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
 
     if (threadIdx.x == 0) {
         mbar_init(&s.q_full, 32), mbar_init(&s.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.s_full[i], 1);
-            for (int c = 0; c < C::CHUNKS; ++c) mbar_init(&s.full[i][c], PLAIN ? 32 : LA_LOADERS);
-            for (int c = 0; c <= C::PAIRS; ++c) mbar_init(&s.empty[i][c], 1);
+            mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 4);
+            for (int g = 0; g < C::GROUPS; ++g) mbar_init(&s.full[i][g], (PLAIN ? 32 : LOADERS) * C::in_group(g));
+            for (int c = 0; c < C::PAIRS; ++c) mbar_init(&s.empty[i][c], 1);
         }
-        mbar_init(&s.p_full, 4), mbar_init(&s.p_empty, 1);
-        mbar_init(&s.o_full, 1), mbar_init(&s.o_empty, 4);
-        for (int i = 0; i < LA_ADDR; ++i) mbar_init(&s.addr_full[i], 1), mbar_init(&s.addr_empty[i], 4 + LA_LOADERS);
-        mbar_init(&s.meet, 4), mbar_init(&s.done, 1);
+        mbar_init(&s.o_empty, 4);
+        for (int i = 0; i < LA_ADDR; ++i) mbar_init(&s.addr_full[i], 1), mbar_init(&s.addr_empty[i], 4 + LOADERS);
+        mbar_init(&s.done[0], 1), mbar_init(&s.done[1], 1);
         fence_mbar_init();
         s.abort = 0;
     }
@@ -333,16 +345,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
         constexpr float SHIFT = P_SHIFT<T> ? P_SHIFT<T> - CH_LAZY : 0.f;  // p up to 2^CH_LAZY of its own
         const int ra = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
         const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-        uint32_t it = 0, seg = 0, met = 0;  // tiles, segments and meetings so far
-        // the four warps come together, by a wait that may run out
-        const auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.meet);
-            __syncwarp();
-            ok = __all_sync(~0u, wait_bounded(&s.meet, met & 1, &s.abort));
-            ++met;
+        uint32_t it = 0, seg = 0, votes = 0;  // tiles, segments and votes so far
+        // The four warps come together, each with a wait that it has won or lost and a question: whether all have won
+        // (they go on or leave together, so that none stays behind at the barrier), and in *any whether one says yes.
+        const auto vote = [&](bool yes, bool* any) {
+            const uint32_t mine = (__any_sync(~0u, yes) ? 1u : 0u) | (ok ? 0u : 2u);
+            uint32_t* const all = s.vote[votes++ & 1];
+            if (lane == 0) all[warp] = mine;
+            bar_sync(1, 128);
+            const uint32_t sum = all[0] | all[1] | all[2] | all[3];
+            *any = sum & 1u;
+            ok = !(sum & 2u);
             return ok;
         };
+        bool any;
         for (; ok && k.begin(p); k.advance(p), ++seg) {
             if (threadIdx.x < LA_ROWS) {
                 const int i = threadIdx.x / p.hp, h = ht * p.hp + threadIdx.x % p.hp;
@@ -356,11 +372,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                 lim[h] = p.idx ? INT32_MAX : k.sees(p, min(i, k.ntok - 1));
             }
             const int lim_all = p.idx ? INT32_MAX : k.sees(p, 0);  // entries that every row sees
-            for (int i = 0; i < k.n && ok; ++i, ++it) {
+            for (int i = 0; i < k.n; ++i, ++it) {
                 const int k0 = (k.tile0 + i) * LA_KEYS, a = it % LA_ADDR;
-                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort) &&
+                ok = ok && __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort) &&
                                          wait_bounded(&s.s_full[it & 1], it / 2 & 1, &s.abort));
-                if (!ok) break;
                 const uint32_t live[2] = {s.live[a][0], s.live[a][1]};
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.addr_empty[a]);
@@ -390,10 +405,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                     grew = grew || mt[h] > m_used[h] + CH_LAZY;
                 }
                 // a row whose maximum has grown: all warps rescale O's columns, as each holds all rows of its dims
-                const uint32_t any = __ballot_sync(~0u, grew);
-                if (lane == 0) s.grew[it & 1][warp] = any;
-                if (!meet()) break;
-                const uint32_t some = s.grew[it & 1][0] | s.grew[it & 1][1] | s.grew[it & 1][2] | s.grew[it & 1][3];
+                bool some;
+                if (!vote(grew, &some)) break;
                 if (some) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -418,11 +431,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                     }
                     l[h] += sum;
                 }
-                // P's place is free, and O at rest, once the last tile's product is done
-                ok = __all_sync(~0u, wait_bounded(&s.p_empty, (it & 1) ^ 1, &s.abort));
-                if (!ok) break;
                 if (some) {
-                    if (!meet()) break;
+                    // O is at rest once the last tile's product is done
+                    if (i > 0) ok = __all_sync(~0u, wait_bounded(&s.empty[(it & 1) ^ 1][C::PAIRS - 1], (it - 1) / 2 & 1, &s.abort));
+                    if (!vote(false, &any)) break;
                     if (i > 0) {
                         tc_fence_after();
 #pragma unroll 1
@@ -437,20 +449,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                         }
                         tmem_st_wait();
                     }
-                    if (!meet()) break;  // the factors have been read
+                    if (!vote(false, &any)) break;  // the factors have been read
                 }
                 const int row = 16 * warp + (lane & 15), g1 = lane >> 4;
-                const uint32_t dst = smem_u32(p_smem) + row * 128;
+                const uint32_t dst = smem_u32(kv_smem) + (it & 1) * C::STAGE_BYTES + C::P_OFF + row * 128;
 #pragma unroll
                 for (int g = 0; g < 8; g += 2)
                     stmatrix_x4(dst + (((g + g1) ^ (row & 7)) << 4), pk[2 * g], pk[2 * g + 1], pk[2 * g + 2], pk[2 * g + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full);
+                if (lane == 0) mbar_arrive(&s.p_full[it & 1]);
                 __syncwarp();
             }
-            if (!ok) break;
+            if (!vote(false, &any)) break;  // (a warp may have lost its last wait)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 l[h] += __shfl_xor_sync(~0u, l[h], 1);
@@ -478,9 +490,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                 const int last = (int)line.run(line.cut(run + 1) + (k.nt - k.n) - 1);
                 p.desc[blockIdx.x] = make_int4(last - run + 1, k.tok0, k.ntok, 0);
             }
-            if (!meet()) break;  // factors and rows are there
-            ok = __all_sync(~0u, wait_bounded(&s.o_full, seg & 1, &s.abort));
-            if (!ok) break;
+            ok = __all_sync(~0u, wait_bounded(&s.empty[(it - 1) & 1][C::PAIRS - 1], (it - 1) / 2 & 1, &s.abort));
+            if (!vote(false, &any)) break;  // factors and rows are there
             tc_fence_after();
             const int rows = k.ntok * p.hp;
 #pragma unroll 1
@@ -510,79 +521,81 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                 }
             }
             tc_fence_before();
-            if (!meet()) break;  // rows and factors have been read
+            if (!vote(false, &any)) break;  // rows and factors have been read
             if (lane == 0) mbar_arrive(&s.o_empty);
         }
-    } else if (warp == 4) {  // products: the warp waits, one lane issues
-        constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, LA_ROWS, false) | 1u << 15;  // A = V^T, MN-major
+    } else if (warp == 4) {  // S: the warp waits, one lane issues
         const uint32_t id_s = idesc_f16(is_bf16<T>, LA_ROWS, LA_KEYS, false) | (p.negate ? 1u << 13 : 0u);  // of -Q
         constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
-        const uint32_t tm = uniform(tmem);
-        const uint32_t q_desc = smem_desc_sw128(smem_u32(q_smem)), k_desc = smem_desc_sw128(smem_u32(kv_smem)),
-                       v_desc = smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK), p_desc = smem_desc_sw128(smem_u32(p_smem));
-        uint32_t it = 0, seg = 0;
-        const auto product_s = [&](uint32_t i) {
-            const uint32_t st = uniform(i & 1), d = tm + LA_S_COL + st * LA_KEYS, kd = k_desc + st * STAGE16;
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c) {
-                ok = ok && wait_bounded(&s.full[st][c], i / 2 & 1, &s.abort);
-                if (!__all_sync(~0u, ok)) {
-                    ok = false;
-                    return;
-                }
-                fence_proxy_async_smem();  // copies of other warps, then the tensor cores
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint32_t off = c * CHUNK16 + ks * 2;
-                        if (c == 0 && ks == 0) mma_f16_ss(d, q_desc, kd, id_s);
-                        else mma_f16_ss_add(d, q_desc + off, kd + off, id_s);
-                    }
-                }
-                __syncwarp();
-            }
-            if (elect_one()) {
-                tc_commit(&s.s_full[st]);
-                if (C::CHUNKS > 2 * C::PAIRS) tc_commit(&s.empty[st][C::PAIRS]);
-            }
-            __syncwarp();
-        };
+        const uint32_t q_desc = uniform(smem_desc_sw128(smem_u32(q_smem))), k_desc = smem_desc_sw128(smem_u32(kv_smem));
+        uint32_t it = 0, seg = 0;  // tiles and segments so far
         for (; ok && k.begin(p); k.advance(p), ++seg) {
             ok = __all_sync(~0u, wait_bounded(&s.q_full, seg & 1, &s.abort));
-            if (!ok) break;
-            product_s(it);
-            for (int i = 0; i < k.n && ok; ++i, ++it) {
-                if (i + 1 < k.n) product_s(it + 1);
-                else if (elect_one()) tc_commit(&s.q_empty);
-                __syncwarp();
+            for (int i = 0; ok && i < k.n; ++i, ++it) {
+                // a stage is filled again when its last tile's P V is done, so its S has been read, too
+                const uint32_t st = uniform(it & 1), d = uniform(tmem + LA_S_COL + st * LA_KEYS);
+                const uint32_t kd = uniform(k_desc + st * STAGE16);
+                const bool end = i + 1 == k.n;
+#pragma unroll
+                for (int g = 0; g < C::GROUPS; ++g) {
+                    ok = ok && wait_bounded(&s.full[st][g], it / 2 & 1, &s.abort);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    fence_proxy_async_smem();  // copies of other warps, then the tensor cores
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < C::in_group(g) * 4; ++x) {
+                            const uint32_t off = (g * C::GROUP + (x >> 2)) * CHUNK16 + (x & 3) * 2;
+                            if (g == 0 && x == 0) mma_f16_ss(d, q_desc, kd, id_s);
+                            else mma_f16_ss_add(d, q_desc + off, kd + off, id_s);
+                        }
+                        if (g + 1 == C::GROUPS) {
+                            tc_commit(&s.s_full[st]);
+                            if (end) tc_commit(&s.q_empty);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (elect_one()) {
+            tc_commit(&s.done[0]);
+            wait_drain(&s.done[0], 0);
+        }
+    } else if (warp == 6) {  // P V, from a warp of its own: each issues while the other waits
+        constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, LA_ROWS, false) | 1u << 15;  // A = V^T, MN-major
+        constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
+        const uint32_t tm = uniform(tmem), v_desc = smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK),
+                       p_desc = smem_desc_sw128(smem_u32(kv_smem) + C::P_OFF);
+        uint32_t it = 0, seg = 0;
+        for (; ok && k.begin(p); k.advance(p), ++seg) {
+            ok = __all_sync(~0u, wait_bounded(&s.o_empty, (seg & 1) ^ 1, &s.abort));
+            for (int i = 0; ok && i < k.n; ++i, ++it) {
+                const uint32_t st = uniform(it & 1), vd = uniform(v_desc + st * STAGE16);
+                const uint32_t pd = uniform(p_desc + st * STAGE16), more = uniform((uint32_t)i);
+                ok = __all_sync(~0u, wait_bounded(&s.p_full[st], it / 2 & 1, &s.abort));
                 if (!ok) break;
-                ok = wait_bounded(&s.p_full, it & 1, &s.abort);
-                if (i == 0) ok = ok && wait_bounded(&s.o_empty, (seg & 1) ^ 1, &s.abort);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
+                fence_proxy_async_smem();  // the entries' copies as well, which the softmax of their S came after
                 tc_fence_after();
-                const uint32_t st = uniform(it & 1), vd = v_desc + st * STAGE16, more = uniform((uint32_t)i);
                 if (elect_one()) {
 #pragma unroll
                     for (int m = 0; m < C::PAIRS; ++m) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
-                            const uint32_t a = vd + 2 * m * CHUNK16 + ks * 128, b = p_desc + ks * 2;
-                            if (ks == 0 && more == 0) mma_f16_ss(tm + m * 64, a, b, id_o);
+                            const uint32_t a = vd + 2 * m * CHUNK16 + ks * 128, b = pd + ks * 2;
+                            if (ks == 0) mma_f16_ss_acc(tm + m * 64, a, b, id_o, more);
                             else mma_f16_ss_add(tm + m * 64, a, b, id_o);
                         }
                         tc_commit(&s.empty[st][m]);
                     }
-                    tc_commit(&s.p_empty);
-                    if (i + 1 == k.n) tc_commit(&s.o_full);
                 }
                 __syncwarp();
             }
         }
         if (elect_one()) {
-            tc_commit(&s.done);
-            wait_drain(&s.done, 0);
+            tc_commit(&s.done[1]);
+            wait_drain(&s.done[1], 0);
         }
     } else if (warp == 5) {  // entries: where the tiles' rows are
         uint32_t it = 0;
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                 mbar_arrive(&s.addr_full[a]);
             }
         }
-    } else if (warp == 6) {  // queries, a unit at a time
+    } else if (warp == 7) {  // queries, a unit at a time
         const T* const q = static_cast<const T*>(p.q);
         uint32_t seg = 0;
         for (; ok && k.begin(p); k.advance(p), ++seg) {
@@ -643,36 +656,45 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
         }
         cp_async_wait_all();
     } else {  // entries' values
-        const int w = warp - 7;
+        const int w = warp - 8;
         uint32_t it = 0;
         if constexpr (PLAIN) {
-            uint32_t n = 0;  // chunks so far: each warp takes every eighth
+            clock_t last = clock();
+            uint32_t n = 0;  // chunks so far: the warps take them in turn
             for (;; ++it) {
                 const int a = it % LA_ADDR, st = it & 1;
                 ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
                 if (!ok || s.end[a]) break;
-#pragma unroll 1
-                for (int c = 0; c < C::CHUNKS; ++c, ++n) {
-                    if ((int)(n % LA_LOADERS) != w) continue;
-                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][c >> 1], (it / 2 & 1) ^ 1, &s.abort));
-                    if (!ok) break;
-                    const int j = lane & 7;
-                    const uint32_t dst = smem_u32(kv_smem) + st * C::STAGE_BYTES + c * LA_CHUNK;
+                const uint8_t* e[LA_KEYS / 4];  // of rows 4 x + lane / 8, this lane's 16 bytes of a chunk
 #pragma unroll
-                    for (int r0 = 0; r0 < LA_KEYS; r0 += 4) {
-                        const int r = r0 + (lane >> 3);
-                        const uint8_t* e = s.entry[a][r];
-                        cp_async16(dst + r * 128 + ((j ^ (r & 7)) << 4), e ? e + c * 128 + j * 16 : nullptr, p.c.data);
-                    }
-                    cp_async_arrive(&s.full[st][c]);
+                for (int x = 0; x < LA_KEYS / 4; ++x) {
+                    e[x] = s.entry[a][4 * x + (lane >> 3)];
+                    if (e[x]) e[x] += (lane & 7) * 16;
                 }
-                if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.addr_empty[a]);
+#pragma unroll 1
+                for (int c = 0; c < C::CHUNKS; ++c, ++n) {
+                    if ((int)(n % LOADERS) != w) continue;
+                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][min(c >> 1, C::PAIRS - 1)], (it / 2 & 1) ^ 1, &s.abort));
+                    if (!ok) break;
+                    const uint32_t dst = smem_u32(kv_smem) + st * C::STAGE_BYTES + c * LA_CHUNK + (lane >> 3) * 128;
+#pragma unroll
+                    for (int x = 0; x < LA_KEYS / 4; ++x) {
+                        if (LA_PACE_CLK) {
+                            while (clock() - last < LA_PACE_CLK) {}
+                            last = clock();
+                        }
+                        cp_async16(dst + x * 512 + (((lane & 7) ^ (lane >> 3) ^ (x & 1) * 4) << 4),
+                                   e[x] ? e[x] + c * 128 : nullptr, p.c.data);
+                    }
+                    cp_async_arrive(&s.full[st][c / C::GROUP]);
+                }
+                if (!ok) break;
             }
             cp_async_wait_all();
         } else {
-            const int tid = threadIdx.x - 7 * 32;
+            const int tid = threadIdx.x - 8 * 32;
             constexpr int CODES = FMT == LF_FP8 ? DIM - LT_TAIL : DIM;
             // FP8: 16 codes of rows tid / 8 and + 32 a step of 128 values, FP4: 32 codes of row tid / 4; a step
             // of the next tile is loaded when the registers of this one's are free
@@ -733,7 +755,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                 const auto there = [&](int c) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.full[st][c]);
+                    if (lane == 0) mbar_arrive(&s.full[st][c / C::GROUP]);
                 };
                 uint2 sc[R];
                 uint4 tl[R];
@@ -777,13 +799,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1) latent_attend_kernel(const __gr
                         }
                     }
                     there(2 * step);
-                    if (lane == 0) mbar_arrive(&s.full[st][2 * step + 1]);
+                    if (lane == 0) mbar_arrive(&s.full[st][(2 * step + 1) / C::GROUP]);
                     if (more) load(step);
                 }
                 if (!ok) break;
                 if constexpr (FMT == LF_FP8 && DIM > LT_VALUE) {
-                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][C::PAIRS], (it / 2 & 1) ^ 1, &s.abort));
-                    if (!ok) break;
 #pragma unroll
                     for (int x = 0; x < R; ++x) {
                         const uint32_t t[4] = {tl[x].x, tl[x].y, tl[x].z, tl[x].w};

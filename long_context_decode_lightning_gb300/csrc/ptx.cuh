@@ -398,6 +398,18 @@ __device__ __forceinline__ void mma_f16_ss_add(uint32_t d_tmem, uint32_t adesc, 
         : "memory");
 }
 
+// The same, D added to where `accumulate` is not 0.
+__device__ __forceinline__ void mma_f16_ss_acc(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "n"(SMEM_DESC_SW128_HI), "r"(accumulate)
+        : "memory");
+}
+
 // The same with A in tensor memory (two 16-bit values of K to a column), D
 // added to where `accumulate` is not 0.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
