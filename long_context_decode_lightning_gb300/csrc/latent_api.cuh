@@ -54,11 +54,14 @@ struct LatentTiles {
     }
 };
 
+// Units of a head tile, at the host's bounds. Sequences without tokens have none, so there are no more than tokens.
+int64_t latent_units(const LatentTiles& t, int32_t B, int64_t T, int64_t max_q, int32_t k) {
+    return k > 0 ? T : std::min(T, B * ((max_q + t.tpt - 1) / t.tpt));
+}
+
 // Tiles of the line, at the host's bounds; more than 2^31 where they pass it.
 int64_t latent_tiles(const LatentTiles& t, int32_t B, int64_t T, int64_t max_q, int64_t max_kv, int32_t k) {
-    const int64_t keys = k > 0 ? k : max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS;
-    // sequences without tokens have no units, so there are no more units than tokens
-    const int64_t units = k > 0 ? T : std::min(T, B * ((max_q + t.tpt - 1) / t.tpt));
+    const int64_t keys = k > 0 ? k : max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS, units = latent_units(t, B, T, max_q, k);
     return units > INT32_MAX || nt > INT32_MAX ? int64_t(1) << 62 : units * nt;
 }
 
@@ -71,14 +74,16 @@ int64_t latent_runs(const LatentTiles& t, int64_t tiles) {
 size_t latent_desc_bytes(const LatentTiles& t, int64_t runs) { return align_up((size_t)runs * t.nht * sizeof(int4), 256); }
 
 template <typename T, int DIM, int FMT>
-hsi_status launch_latent_attend(const LatentAttendParams& p, cudaStream_t s) {
+hsi_status launch_latent_attend(const LatentAttendParams& p, int64_t units, cudaStream_t s) {
     using C = LatentCfg<DIM>;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(latent_attend_kernel<T, DIM, FMT>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
     const unsigned grid = (unsigned)(p.runs * p.nht);
     const hsi_status st = launch(latent_attend_kernel<T, DIM, FMT>, dim3(grid), dim3(latent_threads(FMT)), C::SMEM_BYTES, s, p);
     if (st != HSI_OK || p.runs == 1) return st;
-    return launch(latent_join_kernel<T>, dim3(p.tpt * p.hp, grid), dim3(LT_VALUE / 4), 0, s, p);
+    const unsigned rows = (p.tpt * p.hp + 3) / 4;  // (the last four may pass the unit's rows, not the slot's)
+    if (units >= p.runs / 8) return launch(latent_join_kernel<T, 1>, dim3(rows, grid), dim3(LJ_THREADS), 0, s, p);
+    return launch(latent_join_kernel<T, 8>, dim3(rows * 8, (unsigned)units * p.nht), dim3(LJ_THREADS), 0, s, p);
 }
 
 }  // namespace
@@ -199,18 +204,20 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     if (p.runs <= 0) return HSI_ERR_CUDA;
     p.desc = static_cast<int4*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + latent_desc_bytes(tiles, p.runs));
+    p.inv_hp = 65536 / p.hp + 1;
+    const int64_t units = latent_units(tiles, cache->B, T, p.max_q, p.k);
     const bool wide = cache->dim > LT_VALUE;
     switch (cache->format) {
         case HSI_LATENT_BF16:
-            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_BF16>(p, stream)
-                        : launch_latent_attend<__nv_bfloat16, 512, LF_BF16>(p, stream);
+            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_BF16>(p, units, stream)
+                        : launch_latent_attend<__nv_bfloat16, 512, LF_BF16>(p, units, stream);
         case HSI_LATENT_FP16:
-            return wide ? launch_latent_attend<__half, 576, LF_FP16>(p, stream)
-                        : launch_latent_attend<__half, 512, LF_FP16>(p, stream);
+            return wide ? launch_latent_attend<__half, 576, LF_FP16>(p, units, stream)
+                        : launch_latent_attend<__half, 512, LF_FP16>(p, units, stream);
         case HSI_LATENT_FP8:
-            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_FP8>(p, stream)
-                        : launch_latent_attend<__nv_bfloat16, 512, LF_FP8>(p, stream);
-        default: return launch_latent_attend<__nv_bfloat16, 512, LF_FP4>(p, stream);
+            return wide ? launch_latent_attend<__nv_bfloat16, 576, LF_FP8>(p, units, stream)
+                        : launch_latent_attend<__nv_bfloat16, 512, LF_FP8>(p, units, stream);
+        default: return launch_latent_attend<__nv_bfloat16, 512, LF_FP4>(p, units, stream);
     }
 }
 

@@ -34,12 +34,12 @@ constexpr int LA_KEYS = 64;   // entries of a tile
 #define LA_S_GROUPS 2
 #endif
 #ifndef LA_PLAIN_LOADERS
-#define LA_PLAIN_LOADERS 4
+#define LA_PLAIN_LOADERS 8
 #endif
 #ifndef LA_PACE_CLK
 #define LA_PACE_CLK 0
 #endif
-__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? LA_PLAIN_LOADERS : 8; }
+__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? LA_PLAIN_LOADERS : 16; }
 __host__ __device__ constexpr int latent_threads(int fmt) { return 32 * (8 + latent_loaders(fmt)); }
 constexpr int LA_CHUNK = LA_KEYS * 128;  // bytes of 64 dims of a tile, of a unit's queries, and of P
 constexpr int LA_ADDR = 3;    // tiles whose entries are looked up ahead
@@ -52,6 +52,7 @@ struct LatentAttendParams {
     int64_t T;
     int max_q, max_kv, H;  // host bounds of new tokens and entries; query heads
     int nht, hp, tpt;      // head tiles of a token, heads of one, tokens of a unit
+    int inv_hp;            // 2^16 / hp + 1: row / hp is row * inv_hp >> 16 for the rows of a unit
     const int32_t* idx;    // [T][ld_idx], k entries a token, or null
     int64_t ld_idx;
     int k;
@@ -65,7 +66,8 @@ struct LatentAttendParams {
     float* part;           // partial sums, latent_slot below
 };
 
-constexpr int LA_SLOT = LA_ROWS * (LT_VALUE + 2);  // floats: [row][512], maxima (base 2), sums
+// floats: four rows of a dim side by side, [row / 4][512][4], then maxima (base 2) and sums
+constexpr int LA_SLOT = LA_ROWS * (LT_VALUE + 2);
 // A run's partial sums: of a unit that began before it (0) and of one that goes on after it (1).
 __device__ __forceinline__ float* latent_slot(const LatentAttendParams& p, int run, int ht, int last) {
     return p.part + (((int64_t)run * 2 + last) * p.nht + ht) * LA_SLOT;
@@ -98,11 +100,11 @@ struct LatentSeq {
         sum += none;
         // sum over j of ceil((past + j tpt) / 64) for j = none + 1 .. n: the sum of (a j + b) less that of its
         // residues, which go round the multiples of a's power of two
-        const int a = p.tpt, g = a & -a, per = LA_KEYS / g;
+        const int a = p.tpt, g = a & -a, sh = 6 - (__ffs(g) - 1), per = 1 << sh;  // per = 64 / g
         const uint64_t cnt = n - none, b = (uint64_t)(past + (int64_t)(none + 1) * a + LA_KEYS - 1);
         uint64_t all = b * cnt + (cnt ? cnt * (cnt - 1) / 2 : 0) * a;
-        all -= cnt / per * ((uint64_t)per * (b & (g - 1)) + LA_KEYS / 2 * (per - 1));
-        for (uint64_t i = cnt / per * per; i < cnt; ++i) all -= (b + i * a) & (LA_KEYS - 1);
+        all -= (cnt >> sh) * (uint64_t)(per * (int)(b & (g - 1)) + LA_KEYS / 2 * (per - 1));
+        for (uint32_t i = (uint32_t)cnt & ~(per - 1u); i < (uint32_t)cnt; ++i) all -= ((uint32_t)b + i * a) & (LA_KEYS - 1);
         return sum + (uint32_t)(all / LA_KEYS);
     }
 };
@@ -212,6 +214,25 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t 
                  : "memory");
 }
 
+// Loads that stay where they are written, far ahead of their use (the compiler would move them down to it).
+__device__ __forceinline__ uint4 load_ahead16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 load_ahead8(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_ahead2(const void* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
 // 16 bytes into shared memory without waiting, zeros where src is null.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, const void* any) {
     const int bytes = src ? 16 : 0;
@@ -315,11 +336,11 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         mbar_init(&s.q_full, 32), mbar_init(&s.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 4);
-            for (int g = 0; g < C::GROUPS; ++g) mbar_init(&s.full[i][g], (PLAIN ? 32 : LOADERS) * C::in_group(g));
+            for (int g = 0; g < C::GROUPS; ++g) mbar_init(&s.full[i][g], (PLAIN ? 32 : LOADERS / 2) * C::in_group(g));
             for (int c = 0; c < C::PAIRS; ++c) mbar_init(&s.empty[i][c], 1);
         }
         mbar_init(&s.o_empty, 4);
-        for (int i = 0; i < LA_ADDR; ++i) mbar_init(&s.addr_full[i], 1), mbar_init(&s.addr_empty[i], 4 + LOADERS);
+        for (int i = 0; i < LA_ADDR; ++i) mbar_init(&s.addr_full[i], 1), mbar_init(&s.addr_empty[i], 4 + (PLAIN ? LOADERS : LOADERS / 2));
         mbar_init(&s.done[0], 1), mbar_init(&s.done[1], 1);
         fence_mbar_init();
         s.abort = 0;
@@ -361,14 +382,14 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         bool any;
         for (; ok && k.begin(p); k.advance(p), ++seg) {
             if (threadIdx.x < LA_ROWS) {
-                const int i = threadIdx.x / p.hp, h = ht * p.hp + threadIdx.x % p.hp;
+                const int i = (int)threadIdx.x * p.inv_hp >> 16, h = ht * p.hp + threadIdx.x - i * p.hp;
                 s.row_out[threadIdx.x] = i < k.ntok && h < p.H ? (int64_t)(k.tok0 + i) * p.ot + (int64_t)h * p.oh : -1;
             }
             int lim[2];
             float m_used[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = (ra + 8 * h) / p.hp;
+                const int i = (ra + 8 * h) * p.inv_hp >> 16;
                 lim[h] = p.idx ? INT32_MAX : k.sees(p, min(i, k.ntok - 1));
             }
             const int lim_all = p.idx ? INT32_MAX : k.sees(p, 0);  // entries that every row sees
@@ -480,7 +501,8 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                         slot[LA_ROWS * LT_VALUE + row] = m_used[h];
                         slot[LA_ROWS * (LT_VALUE + 1) + row] = l[h];
                     } else if (p.lse && s.row_out[row] >= 0) {
-                        p.lse[(int64_t)(k.tok0 + row / p.hp) * p.H + ht * p.hp + row % p.hp] =
+                        const int i = row * p.inv_hp >> 16;
+                        p.lse[(int64_t)(k.tok0 + i) * p.H + ht * p.hp + row - i * p.hp] =
                             l[h] == 0.f ? -INFINITY : (m_used[h] + log2f(l[h])) * LN2;
                     }
                 }
@@ -504,8 +526,10 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 tmem_ld_wait(o);
                 if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col0 + j < rows) slot[(col0 + j) * LT_VALUE + d] = __uint_as_float(o[j]);
+                    for (int j = 0; j < 32; j += 4)
+                        if (col0 + j < rows)
+                            reinterpret_cast<uint4*>(slot)[(col0 + j) / 4 * LT_VALUE + d] =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 } else {
                     // two rows at a time: an even lane stores two dims of the first, an odd one of the second
                     T* const out = static_cast<T*>(p.out) + (d & ~1);
@@ -629,13 +653,14 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 if (lane == 0) mbar_arrive(&s.addr_full[a]);
             }
         }
-        if (ok) {
+        for (int i = 0; ok && i < 2; ++i, ++it) {  // two ends: the loaders of even and odd tiles look for one each
             const int a = it % LA_ADDR;
             ok = __all_sync(~0u, wait_bounded(&s.addr_empty[a], (it / LA_ADDR & 1) ^ 1, &s.abort));
             if (ok && lane == 0) {
                 s.end[a] = 1;
                 mbar_arrive(&s.addr_full[a]);
             }
+            __syncwarp();
         }
     } else if (warp == 7) {  // queries, a unit at a time
         const T* const q = static_cast<const T*>(p.q);
@@ -643,10 +668,10 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         for (; ok && k.begin(p); k.advance(p), ++seg) {
             ok = __all_sync(~0u, wait_bounded(&s.q_empty, (seg & 1) ^ 1, &s.abort));
             if (!ok) break;
-            const int j = lane & 7;
-#pragma unroll 1
-            for (int r = lane >> 3; r < LA_ROWS; r += 4) {
-                const int i = r / p.hp, h = ht * p.hp + r % p.hp;
+            const int r0 = lane >> 3, j = lane & 7;
+#pragma unroll 4
+            for (int x = 0; x < LA_ROWS / 4; ++x) {
+                const int r = 4 * x + r0, i = r * p.inv_hp >> 16, h = ht * p.hp + r - i * p.hp;
                 const T* src = i < k.ntok && h < p.H ? q + (int64_t)(k.tok0 + i) * p.qt + (int64_t)h * p.qh + 8 * j : nullptr;
                 const uint32_t dst = smem_u32(q_smem) + r * 128 + ((j ^ (r & 7)) << 4);
 #pragma unroll
@@ -694,76 +719,51 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
             }
             cp_async_wait_all();
         } else {
-            const int tid = threadIdx.x - 8 * 32;
+            // Eight warps take the even tiles and eight the odd ones: a tile's loads are all issued, then waited for,
+            // while the other half decodes. (Loads for the next tile among the steps of this one, by eight warps,
+            // were waited for at every step: a warp has few counters of loads in flight, and waits for all on one.)
+            const int half = w >> 3, tid = (w & 7) * 32 + lane, st = half;
             constexpr int CODES = FMT == LF_FP8 ? DIM - LT_TAIL : DIM;
-            // FP8: 16 codes of rows tid / 8 and + 32 a step of 128 values, FP4: 32 codes of row tid / 4; a step
-            // of the next tile is loaded when the registers of this one's are free
+            // FP8: 16 codes of rows tid / 8 and + 32 a step of 128 values, FP4: 32 codes of row tid / 4
             constexpr int R = FMT == LF_FP8 ? 2 : 1;
             const int row = FMT == LF_FP8 ? tid >> 3 : tid >> 2, j = FMT == LF_FP8 ? tid & 7 : tid & 3;
-            uint4 v[4][R], tail[R];
-            uint2 scale[R];
-            uint32_t scale4[4];
-            const uint8_t* e[R];
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            const auto load = [&](int step) {
-#pragma unroll
-                for (int x = 0; x < R; ++x) {
-                    if constexpr (FMT == LF_FP8) {
-                        const int m = 128 * step + 16 * j;
-                        v[step][x] = e[x] && m < CODES ? __ldg(reinterpret_cast<const uint4*>(e[x] + m)) : zero;
-                    } else {
-                        v[step][x] = e[x] ? __ldg(reinterpret_cast<const uint4*>(e[x] + 64 * step + 16 * j)) : zero;
-                        scale4[step] = e[x] ? __ldg(reinterpret_cast<const uint16_t*>(e[x] + 256 + 8 * step + 2 * j)) : 0u;
-                    }
-                }
+            const uint32_t base = smem_u32(kv_smem) + st * C::STAGE_BYTES;
+            const auto put = [&](int r, int m, const uint32_t (&o)[4]) {  // eight values from dim m on
+                const uint32_t dst = base + (m >> 6) * LA_CHUNK + r * 128 + (((m >> 3 & 7) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                             : "memory");
             };
-            const auto load_tail = [&]() {
-                if constexpr (FMT == LF_FP8) {
-#pragma unroll
-                    for (int x = 0; x < R; ++x) {
-                        tail[x] = e[x] ? __ldg(reinterpret_cast<const uint4*>(e[x] + CODES + 16 * j)) : zero;
-                        scale[x] = e[x] ? __ldg(reinterpret_cast<const uint2*>(e[x] + CODES + 2 * LT_TAIL)) : make_uint2(0u, 0u);
-                    }
-                }
-            };
-            // the next tile's rows; false at the end
-            const auto rows = [&](uint32_t i) {
-                const int a = i % LA_ADDR;
-                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], i / LA_ADDR & 1, &s.abort));
-                if (!ok || s.end[a]) return false;
+            for (it = half;; it += 2) {
+                const int a = it % LA_ADDR;
+                ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
+                if (!ok || s.end[a]) break;
+                const uint8_t* e[R];
 #pragma unroll
                 for (int x = 0; x < R; ++x) e[x] = s.entry[a][row + 32 * x];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.addr_empty[a]);
-                return true;
-            };
-            bool more = rows(0);
-            if (more) {
-                load_tail();
+                uint4 v[4][R], tail[R];
+                uint2 scale[R];
+                uint32_t scale4[4];
 #pragma unroll
-                for (int step = 0; step < 4; ++step) load(step);
-            }
-            while (more) {
-                const int st = it & 1;
-                const uint32_t base = smem_u32(kv_smem) + st * C::STAGE_BYTES;
-                const auto put = [&](int r, int m, const uint32_t (&o)[4]) {  // eight values from dim m on
-                    const uint32_t dst = base + (m >> 6) * LA_CHUNK + r * 128 + (((m >> 3 & 7) ^ (r & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                                 "r"(o[3])
-                                 : "memory");
-                };
-                const auto there = [&](int c) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.full[st][c / C::GROUP]);
-                };
-                uint2 sc[R];
-                uint4 tl[R];
+                for (int x = 0; x < R; ++x) {
+                    if constexpr (FMT == LF_FP8) {
+                        scale[x] = e[x] ? load_ahead8(e[x] + CODES + 2 * LT_TAIL) : make_uint2(0u, 0u);
 #pragma unroll
-                for (int x = 0; x < R; ++x) sc[x] = scale[x], tl[x] = tail[x];
-                more = rows(it + 1);
-                if (!ok) break;
-                if (more) load_tail();
+                        for (int step = 0; step < 4; ++step) {
+                            const int m = 128 * step + 16 * j;
+                            v[step][x] = e[x] && m < CODES ? load_ahead16(e[x] + m) : zero;
+                        }
+                        tail[x] = e[x] ? load_ahead16(e[x] + CODES + 16 * j) : zero;
+                    } else {
+#pragma unroll
+                        for (int step = 0; step < 4; ++step) {
+                            scale4[step] = e[x] ? load_ahead2(e[x] + 256 + 8 * step + 2 * j) : 0u;
+                            v[step][x] = e[x] ? load_ahead16(e[x] + 64 * step + 16 * j) : zero;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int step = 0; step < 4; ++step) {
                     ok = __all_sync(~0u, wait_bounded(&s.empty[st][step], (it / 2 & 1) ^ 1, &s.abort));
@@ -771,47 +771,48 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
 #pragma unroll
                     for (int x = 0; x < R; ++x) {
                         uint32_t o[4];
+                        const uint32_t t[4] = {tail[x].x, tail[x].y, tail[x].z, tail[x].w};
                         if constexpr (FMT == LF_FP8) {
                             const int m = 128 * step + 16 * j;
                             if (m < CODES) {
-                                const uint32_t both = step < 2 ? sc[x].x : sc[x].y;
+                                const uint32_t both = step < 2 ? scale[x].x : scale[x].y;
                                 const uint32_t byte = both >> (16 * (step & 1) + 8 * (j >> 2)) & 0xFFu;
-                                decode8_fp8(make_uint2(v[step][x].x, v[step][x].y), byte, o);
-                                put(row + 32 * x, m, o);
-                                decode8_fp8(make_uint2(v[step][x].z, v[step][x].w), byte, o);
-                                put(row + 32 * x, m + 8, o);
+                                // a row's second four lanes store their halves the other way round, so that
+                                // eight lanes reach all banks
+                                const uint2 lo = make_uint2(v[step][x].x, v[step][x].y), hi = make_uint2(v[step][x].z, v[step][x].w);
+                                decode8_fp8(j < 4 ? lo : hi, byte, o);
+                                put(row + 32 * x, j < 4 ? m : m + 8, o);
+                                decode8_fp8(j < 4 ? hi : lo, byte, o);
+                                put(row + 32 * x, j < 4 ? m + 8 : m, o);
                             }
-                            if (DIM == LT_VALUE && step == 3) {  // the tail is the value's last chunk
-                                const uint32_t t[4] = {tl[x].x, tl[x].y, tl[x].z, tl[x].w};
-                                put(row + 32 * x, CODES + 8 * j, t);
-                            }
+                            // the tail: past the value, or its last chunk; P has left its place with the last 128 dims
+                            if (step == 3) put(row + 32 * x, CODES + 8 * j, t);
                         } else {
                             const int m = 128 * step + 32 * j;
-                            const uint32_t lo = scale4[step] & 0xFFu, hi = scale4[step] >> 8;
-                            decode8_bf16(v[step][x].x, lo, o);
-                            put(row, m, o);
-                            decode8_bf16(v[step][x].y, lo, o);
-                            put(row, m + 8, o);
-                            decode8_bf16(v[step][x].z, hi, o);
-                            put(row, m + 16, o);
-                            decode8_bf16(v[step][x].w, hi, o);
-                            put(row, m + 24, o);
+                            // (here the second two lanes of a row, by halves)
+                            const bool swap = j >= 2;
+                            const uint4 c = v[step][x];
+                            const uint32_t lo = scale4[step] >> (swap ? 8 : 0) & 0xFFu, hi = scale4[step] >> (swap ? 0 : 8) & 0xFFu;
+                            const int m0 = swap ? m + 16 : m, m1 = swap ? m : m + 16;
+                            decode8_bf16(swap ? c.z : c.x, lo, o);
+                            put(row, m0, o);
+                            decode8_bf16(swap ? c.w : c.y, lo, o);
+                            put(row, m0 + 8, o);
+                            decode8_bf16(swap ? c.x : c.z, hi, o);
+                            put(row, m1, o);
+                            decode8_bf16(swap ? c.y : c.w, hi, o);
+                            put(row, m1 + 8, o);
                         }
                     }
-                    there(2 * step);
-                    if (lane == 0) mbar_arrive(&s.full[st][(2 * step + 1) / C::GROUP]);
-                    if (more) load(step);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&s.full[st][2 * step / C::GROUP]);
+                        mbar_arrive(&s.full[st][(2 * step + 1) / C::GROUP]);
+                        if (step == 3 && C::CHUNKS > 2 * C::PAIRS) mbar_arrive(&s.full[st][C::GROUPS - 1]);
+                    }
                 }
                 if (!ok) break;
-                if constexpr (FMT == LF_FP8 && DIM > LT_VALUE) {
-#pragma unroll
-                    for (int x = 0; x < R; ++x) {
-                        const uint32_t t[4] = {tl[x].x, tl[x].y, tl[x].z, tl[x].w};
-                        put(row + 32 * x, CODES + 8 * j, t);
-                    }
-                    there(C::CHUNKS - 1);
-                }
-                ++it;
             }
         }
     }
@@ -822,54 +823,99 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     if (warp == 4) tmem_dealloc(tmem, 512);
 }
 
-// Joins the units that several runs hold: a block per run, head tile and row, four dims a thread.
-template <typename T>
-__global__ void __launch_bounds__(LT_VALUE / 4) latent_join_kernel(const __grid_constant__ LatentAttendParams p) {
+// Joins the units that several runs hold: a block per run, head tile, four rows and 512 / G dims, two dims a thread;
+// its G groups of threads take every G-th part and are joined through shared memory.
+constexpr int LJ_THREADS = 256;
+template <typename T, int G>
+__global__ void __launch_bounds__(LJ_THREADS) latent_join_kernel(const __grid_constant__ LatentAttendParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int row = blockIdx.x, run = blockIdx.y / p.nht, ht = blockIdx.y % p.nht;
-    const int4 unit = p.desc[blockIdx.y];
-    const int i = row / p.hp, h = ht * p.hp + row % p.hp;
-    if (unit.x == 0 || i >= unit.z || h >= p.H) return;
-    constexpr int AT_ONCE = 8;  // runs whose loads are in flight
-    float m = -INFINITY, l = 0.f;
-    float4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < unit.x; c0 += AT_ONCE) {
-        float mc[AT_ONCE], lc[AT_ONCE];
-        float4 oc[AT_ONCE];
+    constexpr int PER = LJ_THREADS / G;
+    const int row0 = blockIdx.x / G * 4;
+    int at = blockIdx.y;  // the unit's place in desc
+    if constexpr (G > 1) {  // few units: block y takes the y-th that there is
+        const int lane = threadIdx.x & 31, places = p.runs * p.nht;
+        int left = at;
+        at = -1;
+        for (int i0 = 0; i0 < places && at < 0; i0 += 160) {
+            bool is[5];
 #pragma unroll
-        for (int c = 0; c < AT_ONCE; ++c) {
-            mc[c] = -INFINITY;
-            lc[c] = 0.f;
-            if (c0 + c >= unit.x) continue;
-            const float* slot = latent_slot(p, run + c0 + c, ht, c0 + c == 0);
-            mc[c] = slot[LA_ROWS * LT_VALUE + row];
-            lc[c] = slot[LA_ROWS * (LT_VALUE + 1) + row];
-            oc[c] = reinterpret_cast<const float4*>(slot + row * LT_VALUE)[threadIdx.x];
+            for (int x = 0; x < 5; ++x) is[x] = i0 + 32 * x + lane < places && p.desc[i0 + 32 * x + lane].x != 0;
+#pragma unroll
+            for (int x = 0; x < 5; ++x) {
+                uint32_t has = __ballot_sync(~0u, is[x]);
+                const int n = __popc(has);
+                if (at < 0 && left < n) {
+                    for (; left > 0; --left) has &= has - 1;
+                    at = i0 + 32 * x + __ffs(has) - 1;
+                }
+                left -= n;
+            }
         }
-        float top = m;
-#pragma unroll
-        for (int c = 0; c < AT_ONCE; ++c) top = fmaxf(top, mc[c]);
-        const float keep = part_factor(m, top);
-        m = top;
-        l *= keep;
-        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-#pragma unroll
-        for (int c = 0; c < AT_ONCE; ++c) {
-            if (lc[c] == 0.f) continue;  // past the runs, or a part that this row does not see
-            const float f = part_factor(mc[c], m);
-            l += f * lc[c];
-            o.x += f * oc[c].x;
-            o.y += f * oc[c].y;
-            o.z += f * oc[c].z;
-            o.w += f * oc[c].w;
-        }
+        if (at < 0) return;
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int64_t t = unit.y + i;
-    *(reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.ot + (int64_t)h * p.oh) + threadIdx.x) =
-        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-    if (threadIdx.x == 0 && p.lse) p.lse[t * p.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+    const int run = at / p.nht, ht = at % p.nht;
+    const int g = threadIdx.x / PER, t = threadIdx.x % PER, d = 2 * (blockIdx.x % G * PER + t);
+    const int4 unit = p.desc[at];
+    if (unit.x == 0 || row0 >= unit.z * p.hp) return;
+    constexpr int AT_ONCE = 4;  // parts whose loads are in flight
+    float m[4], l[4], o[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r][0] = o[r][1] = 0.f;
+    const auto add = [&](const float4& mc, const float4& lc, const float4& a, const float4& b) {
+        const float mr[4] = {mc.x, mc.y, mc.z, mc.w}, lr[4] = {lc.x, lc.y, lc.z, lc.w};
+        const float ar[4] = {a.x, a.y, a.z, a.w}, br[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (lr[r] == 0.f) continue;  // a part that this row does not see
+            const float top = fmaxf(m[r], mr[r]), keep = part_factor(m[r], top), f = part_factor(mr[r], top);
+            l[r] = l[r] * keep + lr[r] * f;
+            o[r][0] = o[r][0] * keep + ar[r] * f;
+            o[r][1] = o[r][1] * keep + br[r] * f;
+            m[r] = top;
+        }
+    };
+    for (int c0 = g; c0 < unit.x; c0 += G * AT_ONCE) {
+        float4 mc[AT_ONCE], lc[AT_ONCE], a[AT_ONCE], b[AT_ONCE];
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x) {
+            const int c = c0 + x * G;
+            lc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c >= unit.x) continue;
+            const float* slot = latent_slot(p, run + c, ht, c == 0);
+            mc[x] = *reinterpret_cast<const float4*>(slot + LA_ROWS * LT_VALUE + row0);
+            lc[x] = *reinterpret_cast<const float4*>(slot + LA_ROWS * (LT_VALUE + 1) + row0);
+            const float4* v = reinterpret_cast<const float4*>(slot) + row0 / 4 * LT_VALUE + d;
+            a[x] = v[0];
+            b[x] = v[1];
+        }
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x)
+            if (c0 + x * G < unit.x) add(mc[x], lc[x], a[x], b[x]);
+    }
+    if constexpr (G > 1) {
+        __shared__ float4 s_part[G - 1][4][PER];
+        if (g > 0) {
+            s_part[g - 1][0][t] = make_float4(m[0], m[1], m[2], m[3]);
+            s_part[g - 1][1][t] = make_float4(l[0], l[1], l[2], l[3]);
+            s_part[g - 1][2][t] = make_float4(o[0][0], o[1][0], o[2][0], o[3][0]);
+            s_part[g - 1][3][t] = make_float4(o[0][1], o[1][1], o[2][1], o[3][1]);
+        }
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int x = 0; x < G - 1; ++x) add(s_part[x][0][t], s_part[x][1][t], s_part[x][2][t], s_part[x][3][t]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = (row0 + r) * p.inv_hp >> 16, h = ht * p.hp + row0 + r - i * p.hp;
+        if (i >= unit.z || h >= p.H) continue;
+        const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
+        const int64_t tok = unit.y + i;
+        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + tok * p.ot + (int64_t)h * p.oh + d) =
+            pack2<T>(o[r][0] * inv, o[r][1] * inv);
+        if (d == 0 && p.lse) p.lse[tok * p.H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * LN2;
+    }
 }
 
 }  // namespace hsi
