@@ -132,71 +132,51 @@ __device__ __forceinline__ int token_seq_warp(const int32_t* q_start, int B, int
     return b;
 }
 
-constexpr int LT_WARPS = 8;
-
-// A warp per token. A rotated value is rounded to the tokens' type, then kept as
-// the format keeps it, so that the entry is the unrotated append of hsi_rope's result.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(32 * LT_WARPS) latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t t = (int64_t)blockIdx.x * LT_WARPS + (threadIdx.x >> 5);
-    if (t >= p.T) return;
-    const int lane = threadIdx.x & 31, dim = p.c.dim;
-    const T* x = static_cast<const T*>(p.x) + t * p.xt;
-    uint4 raw[3] = {};
+// The same for N tokens at once, lane j < N's being its t: one pass over q_start for all of them.
+template <int N>
+__device__ __forceinline__ int token_seqs_warp(const int32_t* q_start, int B, int64_t t, int64_t total, int32_t* first,
+                                               int32_t* past) {
+    const int lane = threadIdx.x & 31;
+    int b = 0, last = 0;
+    int64_t tj[N];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (lane + 32 * i < dim / 8) raw[i] = __ldg(reinterpret_cast<const uint4*>(x) + lane + 32 * i);
-    int32_t first, past;
-    const int b = token_seq_warp(p.q_start, p.c.B, t, p.T, &first, &past);
-    if (b < 0) return;
-    // by the length as it is: by one clamped to the row, the tokens would land on the entries before them
-    const int32_t n = __ldg(p.c.kv_len + b);
-    const int64_t e = (int64_t)n - (past - t);
-    int64_t most = p.c.capacity;
-    if (!p.c.table) {
-        const int64_t at = __ldg(p.c.off + b);
-        most = at < 0 || at > p.c.n_pages ? 0 : min(most, p.c.n_pages - at);
-    }
-    if (n > most && lane == 0) raise_error(DEVERR_ARG);
-    if (e < 0 || e >= most) {
-        if (lane == 0) raise_error(DEVERR_ARG);
-        return;
-    }
-    uint8_t* dst = latent_entry(p.c, b, (int32_t)e);
-    if (!dst) return;
-
-    if (p.r.steps) {
-        const int32_t pos = __ldg(p.r.pos + t);
-        const int half = p.r.rot / 2;
+    for (int j = 0; j < N; ++j) tj[j] = __shfl_sync(~0u, (long long)t, j);
+    for (int i0 = 0; i0 < B; i0 += 32) {
+        const int64_t end = i0 + lane < B ? __ldg(q_start + i0 + lane + 1) : INT64_MAX;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int m = 8 * (lane + 32 * i), d = m - p.r.off;  // rot is a multiple of 16, off of 8
-            if (m >= dim || d < 0 || d >= p.r.rot) continue;
-            uint32_t* w = &raw[i].x;
-            if (p.r.pairs) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 cs = rope_turn(p.r, d / 2 + j, pos), v = unpack2<T>(w[j]);
-                    w[j] = pack2<T>(v.x * cs.x - v.y * cs.y, v.x * cs.y + v.y * cs.x);
-                }
-            } else {
-                const bool low = d < half;
-                const uint4 other = __ldg(reinterpret_cast<const uint4*>(x + (low ? m + half : m - half)));
-                const uint32_t* o = &other.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int pair = (low ? d : d - half) + 2 * j;
-                    const float2 c0 = rope_turn(p.r, pair, pos), c1 = rope_turn(p.r, pair + 1, pos);
-                    const float2 v = unpack2<T>(w[j]), u = unpack2<T>(o[j]);
-                    // (u, v) -> (u cos - v sin, u sin + v cos): this lane holds u below half, v from there
-                    w[j] = low ? pack2<T>(v.x * c0.x - u.x * c0.y, v.y * c1.x - u.y * c1.y)
-                               : pack2<T>(u.x * c0.y + v.x * c0.x, u.y * c1.y + v.y * c1.x);
-                }
-            }
+        for (int j = 0; j < N; ++j) {
+            const uint32_t before = __ballot_sync(~0u, end <= tj[j]);
+            if (lane != j || !before) continue;
+            b += __popc(before);
+            last = i0 + 32 - __clz(before);
         }
     }
+    __syncwarp();
+    if (lane >= N || b >= B) return -1;
+    if (last != b) {
+        raise_error(DEVERR_ARG);
+        return -1;
+    }
+    *first = __ldg(q_start + b);
+    *past = __ldg(q_start + b + 1);
+    if (t < *first) return -1;
+    if (*first < 0 || *past > total) {
+        raise_error(DEVERR_ARG);
+        return -1;
+    }
+    return b;
+}
+template <typename P>
+__device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
+    return reinterpret_cast<P*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(p), lane));
+}
+
+constexpr int LT_WARPS = 8;
+
+// A token's values, eight a lane and step, as the cache's format keeps them. Whole warp.
+template <typename T, int FMT>
+__device__ __forceinline__ void latent_keep(int dim, const uint4 (&raw)[3], uint8_t* dst) {
+    const int lane = threadIdx.x & 31;
     if constexpr (FMT == LF_BF16 || FMT == LF_FP16) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -264,6 +244,90 @@ __global__ void __launch_bounds__(32 * LT_WARPS) latent_append_kernel(const __gr
         *reinterpret_cast<uint4*>(dst + codes + 2 * LT_TAIL) = make_uint4(scales[0], scales[1], 0u, 0u);
 }
 
+// Cosines and sines (times gain) of a position, a pair a lane and turn.
+__device__ __forceinline__ void latent_turn(const RopeTurn& r, int32_t pos, float2* cs) {
+    for (int i = threadIdx.x & 31; i < r.rot / 2; i += 32) cs[i] = rope_turn(r, i, pos);
+    __syncwarp();
+}
+
+// Token t's rotated dims; rot is a multiple of 16, off of 8, so that eight values are rotated or not.
+template <typename T>
+__device__ __forceinline__ void latent_rotate(const LatentAppendParams& p, int64_t t, const float2* cs, uint4 (&raw)[3]) {
+    const int lane = threadIdx.x & 31, half = p.r.rot / 2;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int m = 8 * (lane + 32 * i), d = m - p.r.off;
+        if (m >= p.c.dim || d < 0 || d >= p.r.rot) continue;
+        uint32_t* w = &raw[i].x;
+        if (p.r.pairs) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 c = cs[d / 2 + j], v = unpack2<T>(w[j]);
+                w[j] = pack2<T>(v.x * c.x - v.y * c.y, v.x * c.y + v.y * c.x);
+            }
+            continue;
+        }
+        const bool low = d < half;
+        const T* x = static_cast<const T*>(p.x) + t * p.xt;
+        const uint4 other = __ldg(reinterpret_cast<const uint4*>(x + (low ? m + half : m - half)));
+        const uint32_t* o = &other.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int pair = (low ? d : d - half) + 2 * j;
+            const float2 c0 = cs[pair], c1 = cs[pair + 1], v = unpack2<T>(w[j]), u = unpack2<T>(o[j]);
+            // (u, v) -> (u cos - v sin, u sin + v cos): this lane holds u below half, v from there
+            w[j] = low ? pack2<T>(v.x * c0.x - u.x * c0.y, v.y * c1.x - u.y * c1.y)
+                       : pack2<T>(u.x * c0.y + v.x * c0.x, u.y * c1.y + v.y * c1.x);
+        }
+    }
+}
+
+constexpr int LT_PAIRS = 288;  // rotated pairs of a token, at most
+
+// A warp per token, whose loads are in flight while its place is looked up (two or four tokens a warp: no faster). A
+// rotated value is rounded to the tokens' type, then kept as the format keeps it, so that the entry is the unrotated
+// append of hsi_rope's result; the cosines and sines are worked out once, a pair a lane.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(32 * LT_WARPS) latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
+    __shared__ float2 s_cs[LT_WARPS][LT_PAIRS];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * LT_WARPS + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const int lane = threadIdx.x & 31, dim = p.c.dim;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.xt);
+    uint4 raw[3] = {};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (lane + 32 * i < dim / 8) raw[i] = __ldg(x + lane + 32 * i);
+    const int32_t pos = p.r.steps ? __ldg(p.r.pos + t) : 0;
+    int32_t first, past;
+    const int b = token_seqs_warp<1>(p.q_start, p.c.B, t, p.T, &first, &past);
+    uint8_t* dst = nullptr;
+    if (lane == 0 && b >= 0) {
+        // by the length as it is: by one clamped to the row, the tokens would land on the entries before them
+        const int32_t len = __ldg(p.c.kv_len + b);
+        const int64_t e = (int64_t)len - (past - t);
+        int64_t most = p.c.capacity;
+        if (!p.c.table) {
+            const int64_t at = __ldg(p.c.off + b);
+            most = at < 0 || at > p.c.n_pages ? 0 : min(most, p.c.n_pages - at);
+        }
+        if (len > most || e < 0) raise_error(DEVERR_ARG);
+        if (e >= 0 && e < most) dst = latent_entry(p.c, b, (int32_t)e);
+    }
+    __syncwarp();
+    dst = shfl_ptr(dst, 0);
+    if (!dst) return;
+    if (p.r.steps) {
+        float2* const cs = s_cs[threadIdx.x >> 5];
+        latent_turn(p.r, pos, cs);
+        latent_rotate<T>(p, t, cs, raw);
+        __syncwarp();
+    }
+    latent_keep<T, FMT>(dim, raw, dst);
+}
+
 // --------------------------------------------------------------------- read --
 
 struct LatentReadParams {
@@ -288,26 +352,28 @@ __global__ void __launch_bounds__(32 * LT_WARPS) latent_read_kernel(const __grid
     const int64_t r0 = ((int64_t)blockIdx.x * LT_WARPS + (threadIdx.x >> 5)) * LT_RPW;
     if (r0 >= p.rows) return;
     const int lane = threadIdx.x & 31, dim = p.c.dim;
+    // the rows' entries, a lane each
+    const int64_t r = r0 + lane;
+    const bool mine = lane < LT_RPW && r < p.rows;
+    const int64_t t = p.idx ? r / p.k : r;
+    int64_t e = mine && p.idx ? __ldg(p.idx + t * p.ld_idx + (r - t * p.k)) : 0;
+    int32_t from, past;
+    const int b = token_seqs_warp<LT_RPW>(p.start, p.c.B, mine ? t : INT64_MAX, p.T, &from, &past);
+    const uint8_t* at = nullptr;
+    if (mine && b >= 0) {
+        if (!p.idx) e = t - from + (p.first ? __ldg(p.first + b) : 0);
+        const int32_t len = latent_len(p.c, b);
+        if (e >= 0 && e < len) at = latent_entry(p.c, b, (int32_t)e);
+        else if (!p.idx || e >= 0) raise_error(DEVERR_ARG);
+    }
+    __syncwarp();
+    const uint32_t known = __ballot_sync(~0u, mine && b >= 0);
     const uint8_t* src[LT_RPW];  // null: zeros
     bool live[LT_RPW];           // rows of some sequence
 #pragma unroll
     for (int j = 0; j < LT_RPW; ++j) {
-        const int64_t r = r0 + j, t = p.idx ? r / p.k : r;
-        src[j] = nullptr;
-        live[j] = false;
-        if (r >= p.rows) continue;
-        int32_t from, past;
-        const int b = token_seq_warp(p.start, p.c.B, t, p.T, &from, &past);
-        if (b < 0) continue;
-        live[j] = true;
-        const int64_t e = p.idx ? __ldg(p.idx + t * p.ld_idx + (r - t * p.k))
-                                : t - from + (p.first ? __ldg(p.first + b) : 0);
-        if (p.idx && e < 0) continue;
-        if (e < 0 || e >= latent_len(p.c, b)) {
-            raise_error(DEVERR_ARG);
-            continue;
-        }
-        src[j] = latent_entry(p.c, b, (int32_t)e);
+        src[j] = shfl_ptr(at, j);
+        live[j] = known >> j & 1;
     }
     constexpr int N = FMT == LF_FP8 || FMT == LF_FP4 ? 2 : 3;
     uint4 v[LT_RPW][3] = {};
@@ -342,8 +408,8 @@ __global__ void __launch_bounds__(32 * LT_WARPS) latent_read_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < LT_RPW; ++j) {
         if (!live[j]) continue;
-        const int64_t r = r0 + j;
-        uint16_t* row = p.idx ? p.out + r / p.k * p.ot + r % p.k * dim : p.out + r * p.ot;
+        const int64_t rj = r0 + j, tj = __shfl_sync(~0u, (long long)t, j);
+        uint16_t* row = p.idx ? p.out + tj * p.ot + (rj - tj * p.k) * dim : p.out + rj * p.ot;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int m = 8 * (lane + 32 * i);

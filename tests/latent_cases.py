@@ -148,7 +148,7 @@ class Latent:
         rows = []
         for b, (n, m) in enumerate(zip(self.kv_lens, self.q_lens)):
             for i in range(m):
-                seen = n - m + i + 1 if causal else n
+                seen = max(0, n - m + i + 1) if causal else n
                 e = torch.full((k,), -1, dtype=torch.int32, device=DEV)
                 pick = torch.randperm(seen, generator=g, device=DEV)[:k].int()
                 e[:pick.numel()] = pick
@@ -174,7 +174,7 @@ class Latent:
         t = 0
         for b, (n, m) in enumerate(zip(self.kv_lens, self.q_lens)):
             for i in range(m):
-                seen = n - m + i + 1 if causal else n
+                seen = max(0, n - m + i + 1) if causal else n
                 kv = self.values[b][:seen] if idx is None else self.values[b][idx[t][idx[t] >= 0].long()]
                 if kv.shape[0]:
                     Q, val = q[t].double(), kv[:, :V]

@@ -98,7 +98,8 @@ def test_append_reports_what_is_not_finite(fmt):
 
 def _rotated(x, pos, rot, off, pairs, gain):
     """fp64 rotation and its error bound: the angle's cosine and sine are off by less than 2^-21 (an fp32 phase of at
-    most pi, and sincospif), and each of the two products and their sum rounds once in fp32."""
+    most pi, and sincospif), and each of the two products and their sum rounds once in fp32. In fp16 numbers below 2^-14
+    are 2^-24 apart, so that their rounding is off by up to 2^-25 however small they are."""
     y, tol = x.double().clone(), torch.zeros_like(x, dtype=torch.float64)
     half = rot // 2
     for i in range(half):
@@ -106,7 +107,7 @@ def _rotated(x, pos, rot, off, pairs, gain):
         m, n = (off + 2 * i, off + 2 * i + 1) if pairs else (off + i, off + half + i)
         u, v = x[:, m].double(), x[:, n].double()
         y[:, m], y[:, n] = gain * (u * a.cos() - v * a.sin()), gain * (u * a.sin() + v * a.cos())
-        tol[:, m] = tol[:, n] = gain * (u.abs() + v.abs()) * 2.0 ** -20
+        tol[:, m] = tol[:, n] = gain * (u.abs() + v.abs()) * 2.0 ** -20 + (2.0 ** -25 if x.dtype == torch.float16 else 0.0)
     return y, tol
 
 
@@ -392,6 +393,65 @@ def test_attention_many_small_weights_are_not_lost():
         c.q = torch.zeros_like(c.q)
         c.q[..., 0] = 16.0
         c.check(1.0)
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP16])
+@pytest.mark.parametrize("q_lens,k", [([1, 1], 0), ([40, 9], 0), ([3, 2], 500)])
+def test_attention_whose_maxima_keep_growing(fmt, q_lens, k):
+    """Some heads' scores rise from tile to tile by far more than the sums take without being rescaled, others fall."""
+    c = Latent(43, [1500, 700], q_lens, 24, fmt, 512, 64)
+    for b, n in enumerate(c.kv_lens):
+        c.x[b][:, 0] = (torch.arange(n, device=DEV) // 64) * 2.0
+        c.values[b] = c.x[b].double()
+        for e in range(0, n, 64):
+            c.data[int(c.table[b, e // 64]), :min(64, n - e)] = c.x[b][e:e + 64]
+    c.q[:, :, 0] = torch.tensor([12.0, -12.0, 0.0, 3.0, 24.0, 1.0], device=DEV).repeat(4)
+    c.check(1.0, True, idx=c.lists(44, k, True).sort(1).values if k else None)
+
+
+def test_attention_of_more_new_tokens_than_entries():
+    """Rows that see nothing beside rows that do: zeros and -inf."""
+    for H in (16, 64, 100):
+        c = Latent(45, [1, 0, 70, 2], [3, 2, 90, 2], H, BF16, 576, 16)
+        c.check(SCALE)
+        assert bool((c.out[:2] == 0).all()) and bool((c.lse[:2] == -math.inf).all())
+        c.check(SCALE, idx=c.lists(46, 9, True))
+
+
+@pytest.mark.parametrize("fmt,dim", [(BF16, 576), (FP8, 576), (FP4, 512)])
+@pytest.mark.parametrize("kv_lens,q_lens,k", [([900, 500], [1, 1], 0), ([20000, 12000], [1, 1], 0), ([600], [90], 0),
+                                              ([700, 90], [2, 3], 200)])
+def test_wait_that_runs_out_is_reported(fmt, dim, kv_lens, q_lens, k):
+    """A copy that is never made: the waits for it end, the status says so, and the next call is right."""
+    c = Latent(47, kv_lens, q_lens, 32, fmt, dim, 16)
+    idx = c.lists(48, k, True) if k else None
+    c.check(SCALE, idx=idx)
+    try:
+        hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 20_000_000)
+        hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 1)
+        hsi.latent_attention(c.cache, c.q, c.q_start, c.max_q, c.max_kv, SCALE, c.out, lse=c.lse, idx=idx)
+        assert hsi.device_error() == -4
+    finally:
+        hsi.debug_set(hsi.DEBUG_SKIP_FIRST_COPY, 0)
+        hsi.debug_set(hsi.DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
+    c.check(SCALE, idx=idx)
+
+
+def test_attention_on_two_streams_at_once():
+    """Calls with a workspace each, side by side."""
+    cases = [Latent(50 + i, [3000, 900], [1, 1], 64, fmt, 576, 64) for i, fmt in enumerate([BF16, FP8])]
+    streams = [torch.cuda.Stream() for _ in cases]
+    work = [hsi.latent_attention_workspace(c.cache, c.q, 1, 3000) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s, ws in zip(cases, streams, work):
+            hsi.latent_attention(c.cache, c.q, c.q_start, 1, 3000, SCALE, c.out, lse=c.lse, ws=ws, stream=s)
+    torch.cuda.synchronize()
+    assert hsi.device_error() == 0
+    for c in cases:
+        out, lse, tol, tol_lse = c.attention(SCALE, True)
+        within(c.out, out, tol)
+        within(c.lse, lse, tol_lse)
 
 
 @pytest.mark.parametrize("q_lens,k", [([1, 1], 0), ([33, 2], 0), ([2, 1], 70)])

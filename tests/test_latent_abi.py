@@ -5,6 +5,7 @@ import shutil
 
 import pytest
 import torch
+from test_warp_barriers import BARRIER, _source
 
 import long_context_decode_lightning_gb300 as hsi
 
@@ -105,6 +106,11 @@ def test_wrong_attentions(L, status, kw):
 def test_lengths_that_31_bits_cannot_count(L):
     wide = cache(table=None, offsets=F, n_pages=(1 << 31) + 5)
     assert attend(L, wide, max_kv=(1 << 31) - 1) == -2
+
+
+def test_kernels_use_the_barrier_helpers():
+    for name in ("latent.cuh", "latent_attend.cuh"):
+        assert not BARRIER.search(_source(name)), name
 
 
 # ------------------------------------------------------------------ the binding --
