@@ -62,6 +62,7 @@ struct LatentAttendParams {
     int64_t ot, oh;
     float* lse;            // [T][H] or null
     int runs;              // runs that the line is cut into, at most
+    int csize, n_rt;       // short form: blocks of a unit (0: the line), units of a sequence at most
     int4* desc;            // [runs][nht]: the unit that begins in this run and ends in another: runs, first token, tokens
     float* part;           // partial sums, latent_slot below
 };
@@ -72,6 +73,43 @@ constexpr int LA_SLOT = LA_ROWS * (LT_VALUE + 2);
 __device__ __forceinline__ float* latent_slot(const LatentAttendParams& p, int run, int ht, int last) {
     return p.part + (((int64_t)run * 2 + last) * p.nht + ht) * LA_SLOT;
 }
+
+// Partial sums of four rows by two dims.
+struct LatentSums {
+    float m[4], l[4], o[4][2];
+    __device__ __forceinline__ LatentSums() {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r][0] = o[r][1] = 0.f;
+    }
+    // a part: maxima, sums and the two dims of the four rows
+    __device__ __forceinline__ void add(const float4& mc, const float4& lc, const float4& a, const float4& b) {
+        const float mr[4] = {mc.x, mc.y, mc.z, mc.w}, lr[4] = {lc.x, lc.y, lc.z, lc.w};
+        const float ar[4] = {a.x, a.y, a.z, a.w}, br[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (lr[r] == 0.f) continue;  // a part that this row does not see
+            const float top = fmaxf(m[r], mr[r]), keep = part_factor(m[r], top), f = part_factor(mr[r], top);
+            l[r] = l[r] * keep + lr[r] * f;
+            o[r][0] = o[r][0] * keep + ar[r] * f;
+            o[r][1] = o[r][1] * keep + br[r] * f;
+            m[r] = top;
+        }
+    }
+    // rows row0 .. row0 + 3 of a unit of ntok tokens from tok0 on, dims d and d + 1
+    template <typename T>
+    __device__ __forceinline__ void store(const LatentAttendParams& p, int tok0, int ntok, int ht, int row0, int d) const {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = (row0 + r) * p.inv_hp >> 16, h = ht * p.hp + row0 + r - i * p.hp;
+            if (i >= ntok || h >= p.H) continue;
+            const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
+            const int64_t t = tok0 + i;
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + t * p.ot + (int64_t)h * p.oh + d) =
+                pack2<T>(o[r][0] * inv, o[r][1] * inv);
+            if (d == 0 && p.lse) p.lse[t * p.H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * LN2;
+        }
+    }
+};
 
 // Lengths of sequence b and what follows from them.
 struct LatentSeq {
@@ -180,6 +218,7 @@ struct LatentCfg {
         float factor[LA_ROWS];
         uint32_t vote[2][4];
         uint32_t tmem, total;
+        int there;                     // short form: the unit is one
         int abort;
         int left, b, rt, tile;         // this block's run: tiles, and where it starts
         LatentSeq q;
@@ -320,6 +359,33 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     }
 }
 
+// The short form instead: a unit a cluster, its tiles in equal parts. One warp.
+template <typename Tail>
+__device__ __forceinline__ void latent_part(const LatentAttendParams& p, int unit, int rank, Tail& s) {
+    LatentWalk k;
+    k.tile0 = 0;
+    k.left = INT32_MAX;
+    if (p.idx) {
+        k.rt = unit;
+        k.left = (p.k + LA_KEYS - 1) / LA_KEYS;  // a unit's, so that begin() ends at a token of no sequence
+        if (!k.begin(p)) k.nt = 0;
+    } else {
+        k.b = unit / p.n_rt;
+        k.rt = unit % p.n_rt;
+        k.q.load(p, k.b);
+        k.nt = k.rt < k.q.n_rt ? k.q.tiles(p, k.rt) : 0;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        const int from = (int)((int64_t)k.nt * rank / p.csize);
+        s.left = (int)((int64_t)k.nt * (rank + 1) / p.csize) - from;
+        s.b = k.b;
+        s.rt = k.rt;
+        s.tile = from;
+        s.q = k.q;
+        s.there = k.nt > 0;
+    }
+}
+
 template <typename T, int DIM, int FMT>
 __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
     using C = LatentCfg<DIM>;
@@ -328,7 +394,9 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     uint8_t* const q_smem = ring;
     uint8_t* const kv_smem = ring + C::KV_OFF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
+    // the line: run, head tile; the short form: unit, head tile, rank
+    const int block = p.csize ? blockIdx.x / p.csize : blockIdx.x, rank = p.csize ? blockIdx.x % p.csize : 0;
+    const int run = block / p.nht, ht = block % p.nht;
     constexpr int LOADERS = latent_loaders(FMT);
     constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
 
@@ -348,8 +416,12 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     if (warp == 4) tmem_alloc(&s.tmem, 512);
     griddep_wait();
     griddep_launch_dependents();
-    if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (warp == 0) latent_line(p, run, s);
+    if (p.csize == 0) {
+        if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (warp == 0) latent_line(p, run, s);
+    } else if (warp == 0) {
+        latent_part(p, run, rank, s);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -491,8 +563,17 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 m_used[h] -= SHIFT;  // what the sums are by
                 if ((lane & 3) == 0) s.factor[ra + 8 * h] = l[h] > 0.f || l[h] != l[h] ? 1.f / l[h] : 0.f;
             }
-            const bool whole = k.whole();
-            float* slot = latent_slot(p, run, ht, k.tile0 == 0);
+            const bool whole = k.whole() && p.csize <= 1;
+            // (the short form's blocks keep their sums in the place of the entries, which are no longer needed)
+            float* slot = p.csize ? reinterpret_cast<float*>(kv_smem) : latent_slot(p, run, ht, k.tile0 == 0);
+            if (!whole && k.tile0 == 0 && threadIdx.x == 0 && p.csize == 0) {  // the unit goes on in later runs
+                const Line line(s.total, p.runs);
+                const int last = (int)line.run(line.cut(run + 1) + (k.nt - k.n) - 1);
+                p.desc[blockIdx.x] = make_int4(last - run + 1, k.tok0, k.ntok, 0);
+            }
+            ok = __all_sync(~0u, wait_bounded(&s.empty[(it - 1) & 1][C::PAIRS - 1], (it - 1) / 2 & 1, &s.abort));
+            if (!vote(false, &any)) break;  // factors and rows are there
+            tc_fence_after();
             if ((lane & 3) == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -507,14 +588,6 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                     }
                 }
             }
-            if (!whole && k.tile0 == 0 && threadIdx.x == 0) {  // the unit goes on in later runs
-                const Line line(s.total, p.runs);
-                const int last = (int)line.run(line.cut(run + 1) + (k.nt - k.n) - 1);
-                p.desc[blockIdx.x] = make_int4(last - run + 1, k.tok0, k.ntok, 0);
-            }
-            ok = __all_sync(~0u, wait_bounded(&s.empty[(it - 1) & 1][C::PAIRS - 1], (it - 1) / 2 & 1, &s.abort));
-            if (!vote(false, &any)) break;  // factors and rows are there
-            tc_fence_after();
             const int rows = k.ntok * p.hp;
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -821,6 +894,29 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     __syncthreads();
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tmem, 512);
+    if (p.csize <= 1) return;
+    // the short form's join: every block takes its share of the unit's rows from all of them
+    float* const mine = reinterpret_cast<float*>(kv_smem);
+    if (s.left == 0 && threadIdx.x < LA_ROWS) mine[LA_ROWS * (LT_VALUE + 1) + threadIdx.x] = 0.f;  // no part
+    cluster_sync();
+    if (s.there) {
+        const int share = LA_ROWS / 4 / p.csize;  // groups of four rows
+        const int tok0 = p.idx ? s.rt : s.q.at + s.rt * p.tpt, ntok = p.idx ? 1 : min(p.tpt, s.q.m - s.rt * p.tpt);
+        for (int i = threadIdx.x; i < share * (LT_VALUE / 2); i += latent_threads(FMT)) {
+            const int g = rank * share + i / (LT_VALUE / 2), d = 2 * (i % (LT_VALUE / 2));
+            if (4 * g >= ntok * p.hp) continue;
+            LatentSums sum;
+            for (int c = 0; c < p.csize; ++c) {
+                const float4 l = cluster_load4(mine + LA_ROWS * (LT_VALUE + 1) + 4 * g, c, p.csize);
+                const float4 m = cluster_load4(mine + LA_ROWS * LT_VALUE + 4 * g, c, p.csize);
+                const float4 a = cluster_load4(mine + 4 * (g * LT_VALUE + d), c, p.csize);
+                const float4 b = cluster_load4(mine + 4 * (g * LT_VALUE + d + 1), c, p.csize);
+                sum.add(m, l, a, b);
+            }
+            sum.store<T>(p, tok0, ntok, ht, 4 * g, d);
+        }
+    }
+    cluster_sync();  // nobody leaves while its sums are read
 }
 
 // Joins the units that several runs hold: a block per run, head tile, four rows and 512 / G dims, two dims a thread;
@@ -859,22 +955,7 @@ __global__ void __launch_bounds__(LJ_THREADS) latent_join_kernel(const __grid_co
     const int4 unit = p.desc[at];
     if (unit.x == 0 || row0 >= unit.z * p.hp) return;
     constexpr int AT_ONCE = 4;  // parts whose loads are in flight
-    float m[4], l[4], o[4][2];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r][0] = o[r][1] = 0.f;
-    const auto add = [&](const float4& mc, const float4& lc, const float4& a, const float4& b) {
-        const float mr[4] = {mc.x, mc.y, mc.z, mc.w}, lr[4] = {lc.x, lc.y, lc.z, lc.w};
-        const float ar[4] = {a.x, a.y, a.z, a.w}, br[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (lr[r] == 0.f) continue;  // a part that this row does not see
-            const float top = fmaxf(m[r], mr[r]), keep = part_factor(m[r], top), f = part_factor(mr[r], top);
-            l[r] = l[r] * keep + lr[r] * f;
-            o[r][0] = o[r][0] * keep + ar[r] * f;
-            o[r][1] = o[r][1] * keep + br[r] * f;
-            m[r] = top;
-        }
-    };
+    LatentSums sum;
     for (int c0 = g; c0 < unit.x; c0 += G * AT_ONCE) {
         float4 mc[AT_ONCE], lc[AT_ONCE], a[AT_ONCE], b[AT_ONCE];
 #pragma unroll
@@ -891,31 +972,22 @@ __global__ void __launch_bounds__(LJ_THREADS) latent_join_kernel(const __grid_co
         }
 #pragma unroll
         for (int x = 0; x < AT_ONCE; ++x)
-            if (c0 + x * G < unit.x) add(mc[x], lc[x], a[x], b[x]);
+            if (c0 + x * G < unit.x) sum.add(mc[x], lc[x], a[x], b[x]);
     }
     if constexpr (G > 1) {
         __shared__ float4 s_part[G - 1][4][PER];
         if (g > 0) {
-            s_part[g - 1][0][t] = make_float4(m[0], m[1], m[2], m[3]);
-            s_part[g - 1][1][t] = make_float4(l[0], l[1], l[2], l[3]);
-            s_part[g - 1][2][t] = make_float4(o[0][0], o[1][0], o[2][0], o[3][0]);
-            s_part[g - 1][3][t] = make_float4(o[0][1], o[1][1], o[2][1], o[3][1]);
+            s_part[g - 1][0][t] = make_float4(sum.m[0], sum.m[1], sum.m[2], sum.m[3]);
+            s_part[g - 1][1][t] = make_float4(sum.l[0], sum.l[1], sum.l[2], sum.l[3]);
+            s_part[g - 1][2][t] = make_float4(sum.o[0][0], sum.o[1][0], sum.o[2][0], sum.o[3][0]);
+            s_part[g - 1][3][t] = make_float4(sum.o[0][1], sum.o[1][1], sum.o[2][1], sum.o[3][1]);
         }
         __syncthreads();
         if (g > 0) return;
 #pragma unroll
-        for (int x = 0; x < G - 1; ++x) add(s_part[x][0][t], s_part[x][1][t], s_part[x][2][t], s_part[x][3][t]);
+        for (int x = 0; x < G - 1; ++x) sum.add(s_part[x][0][t], s_part[x][1][t], s_part[x][2][t], s_part[x][3][t]);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i = (row0 + r) * p.inv_hp >> 16, h = ht * p.hp + row0 + r - i * p.hp;
-        if (i >= unit.z || h >= p.H) continue;
-        const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
-        const int64_t tok = unit.y + i;
-        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + tok * p.ot + (int64_t)h * p.oh + d) =
-            pack2<T>(o[r][0] * inv, o[r][1] * inv);
-        if (d == 0 && p.lse) p.lse[tok * p.H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * LN2;
-    }
+    sum.store<T>(p, unit.y, unit.z, ht, row0, d);
 }
 
 }  // namespace hsi

@@ -272,6 +272,17 @@ def test_attention_over_lists(fmt, dim, causal, k, kv_lens, q_lens, H, page):
     c.check(SCALE, causal, idx=c.lists(23, k, causal))
 
 
+@pytest.mark.parametrize("fmt,dim", [(BF16, 576), (FP16, 512), (FP8, 576), (FP4, 512)])
+@pytest.mark.parametrize("kv_lens,q_lens,H,k", [
+    ([2000, 300], [170, 40], 64, 0), ([900], [900], 20, 0), ([3000, 100], [130, 60], 48, 130), ([500, 40], [90, 17], 128, 65),
+    ([9000], [1], 64, 0), ([5000, 100, 3000, 0, 64, 65], [1, 1, 1, 0, 1, 1], 16, 0), ([300] * 20, [1] * 20, 128, 0),
+    ([4000, 90], [2, 1], 128, 1000), ([700] * 100, [1] * 100, 16, 300)])
+def test_attention_of_units_in_runs_and_clusters(fmt, dim, kv_lens, q_lens, H, k):
+    """More units than SMs, one unit for all of them, clusters of every size, lists of several tiles."""
+    c = Latent(49, kv_lens, q_lens, H, fmt, dim, 64)
+    c.check(SCALE, True, idx=c.lists(50, k, True) if k else None)
+
+
 def test_attention_over_odd_lists():
     """Lists that are empty, that hold one entry in their last place, or the same entry many times; rows apart."""
     c = Latent(24, [500, 80], [3, 2], 24, BF16, 576, 16)
