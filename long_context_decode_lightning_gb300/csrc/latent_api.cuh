@@ -44,13 +44,6 @@ hsi_status latent_view(const hsi_latent_cache* c, LatentView* v) {
 
 bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) { return k > 0 && ld_idx >= k && aligned(idx, 4); }
 
-// Most blocks of a short unit, SMs that clusters of them can take at once, and what the line's partial sums and second
-// kernel cost it, in tiles.
-constexpr int LA_CLUSTER = 8, LA_CLUSTER_SMS = 128;
-#ifndef LA_JOIN_TILES
-#define LA_JOIN_TILES 6
-#endif
-
 // How heads and tokens make units of at most 64 rows.
 struct LatentTiles {
     int nht, hp, tpt;  // head tiles of a token, heads of one, tokens of a unit
@@ -80,14 +73,17 @@ int64_t latent_runs(const LatentTiles& t, int64_t tiles) {
 
 size_t latent_desc_bytes(const LatentTiles& t, int64_t runs) { return align_up((size_t)runs * t.nht * sizeof(int4), 256); }
 
-// The short form: a cluster a unit, no line and no second kernel.
-int64_t short_units(const LatentAttendParams& p) { return p.idx ? p.T : (int64_t)p.c.B * p.n_rt; }
-int latent_short(const LatentAttendParams& p, int64_t tiles) {
-    const int64_t blocks = short_units(p) * p.nht, keys = p.idx ? p.k : p.max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS;
-    if (blocks > sm_count()) return 0;
-    int csize = 1;
-    while (csize < LA_CLUSTER && 2 * csize * blocks <= LA_CLUSTER_SMS && 2 * csize <= nt) csize *= 2;
-    return (nt + csize - 1) / csize <= (tiles + p.runs - 1) / p.runs + LA_JOIN_TILES ? csize : 0;
+// Whether units go whole to blocks (no partial sums, no second kernel): where the most tiles that a block then has are
+// no more than those of the line's runs and what the join costs, eight tiles' time where all SMs leave partial sums.
+// Measured, one token, 64 heads over bf16 entries of 576, us whole against line: 64 tokens of 512 listed entries 24 and
+// 30, 20 of them 22 and 22, 30 sequences of 600 entries 25 and 26, 150 tokens of 256 listed 19 and 25; eight tokens of
+// 1024 listed 35 and 27, one sequence of 200 entries 14 and 11. (Clusters of 2, 4 or 8 blocks a unit, joined through
+// distributed shared memory, were slower than the better of the two in every one of these.)
+bool latent_whole(const LatentAttendParams& p, int64_t tiles) {
+    const int64_t keys = p.idx ? p.k : p.max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS, room = sm_count() / p.nht;
+    const int64_t units = p.idx ? p.T : (int64_t)p.c.B * p.n_rt;
+    if (room <= 0 || (!p.idx && units > room)) return false;
+    return (units + room - 1) / room * nt <= (tiles + p.runs - 1) / p.runs + 1 + 7 * p.runs / room;
 }
 
 template <typename T, int DIM, int FMT>
@@ -95,12 +91,9 @@ hsi_status launch_latent_attend(const LatentAttendParams& p, int64_t units, cuda
     using C = LatentCfg<DIM>;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(latent_attend_kernel<T, DIM, FMT>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
-    if (p.csize)
-        return launch_cluster(latent_attend_kernel<T, DIM, FMT>, dim3((unsigned)(short_units(p) * p.nht * p.csize)),
-                              dim3(latent_threads(FMT)), C::SMEM_BYTES, p.csize, s, p);
     const unsigned grid = (unsigned)(p.runs * p.nht);
     const hsi_status st = launch(latent_attend_kernel<T, DIM, FMT>, dim3(grid), dim3(latent_threads(FMT)), C::SMEM_BYTES, s, p);
-    if (st != HSI_OK || p.runs == 1) return st;
+    if (st != HSI_OK || p.runs == 1 || p.whole) return st;
     const unsigned rows = (p.tpt * p.hp + 3) / 4;  // (the last four may pass the unit's rows, not the slot's)
     if (units >= p.runs / 8) return launch(latent_join_kernel<T, 1>, dim3(rows, grid), dim3(LJ_THREADS), 0, s, p);
     return launch(latent_join_kernel<T, 8>, dim3(rows * 8, (unsigned)units * p.nht), dim3(LJ_THREADS), 0, s, p);
@@ -226,7 +219,9 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + latent_desc_bytes(tiles, p.runs));
     p.inv_hp = 65536 / p.hp + 1;
     p.n_rt = (p.max_q + p.tpt - 1) / p.tpt;
-    p.csize = latent_short(p, most);
+    p.whole = latent_whole(p, most);
+    // (a list's runs are of whole units then, a sequence's units are runs)
+    if (p.whole) p.runs = (int)(idx ? std::min<int64_t>(T, sm_count() / p.nht) : (int64_t)cache->B * p.n_rt);
     const int64_t units = latent_units(tiles, cache->B, T, p.max_q, p.k);
     const bool wide = cache->dim > LT_VALUE;
     switch (cache->format) {

@@ -30,16 +30,8 @@ namespace hsi {
 
 constexpr int LA_ROWS = 64;   // rows of a unit
 constexpr int LA_KEYS = 64;   // entries of a tile
-#ifndef LA_S_GROUPS
-#define LA_S_GROUPS 2
-#endif
-#ifndef LA_PLAIN_LOADERS
-#define LA_PLAIN_LOADERS 8
-#endif
-#ifndef LA_PACE_CLK
-#define LA_PACE_CLK 0
-#endif
-__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? LA_PLAIN_LOADERS : 16; }
+constexpr int LA_S_GROUPS = 2;  // S is issued as soon as half of a tile's dims are there
+__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? 8 : 16; }
 __host__ __device__ constexpr int latent_threads(int fmt) { return 32 * (8 + latent_loaders(fmt)); }
 constexpr int LA_CHUNK = LA_KEYS * 128;  // bytes of 64 dims of a tile, of a unit's queries, and of P
 constexpr int LA_ADDR = 3;    // tiles whose entries are looked up ahead
@@ -62,7 +54,7 @@ struct LatentAttendParams {
     int64_t ot, oh;
     float* lse;            // [T][H] or null
     int runs;              // runs that the line is cut into, at most
-    int csize, n_rt;       // short form: blocks of a unit (0: the line), units of a sequence at most
+    int whole, n_rt;       // short form: no unit is split; units of a sequence at most
     int4* desc;            // [runs][nht]: the unit that begins in this run and ends in another: runs, first token, tokens
     float* part;           // partial sums, latent_slot below
 };
@@ -218,7 +210,6 @@ struct LatentCfg {
         float factor[LA_ROWS];
         uint32_t vote[2][4];
         uint32_t tmem, total;
-        int there;                     // short form: the unit is one
         int abort;
         int left, b, rt, tile;         // this block's run: tiles, and where it starts
         LatentSeq q;
@@ -289,13 +280,26 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     const int lane = threadIdx.x & 31;
     if (p.idx) {
         const uint32_t nt = (p.k + LA_KEYS - 1) / LA_KEYS;
-        const Line line((uint32_t)p.T * nt, p.runs);
+        const Line line((uint32_t)p.T * (p.whole ? 1 : nt), p.runs);
         if (lane == 0) {
             s.total = line.total;
             const uint32_t x = line.cut(run);
-            s.left = run < (int)line.G ? (int)(line.cut(run + 1) - x) : 0;
-            s.rt = x / nt;
-            s.tile = x % nt;
+            s.left = run < (int)line.G ? (int)(line.cut(run + 1) - x) * (p.whole ? nt : 1) : 0;
+            s.rt = p.whole ? x : x / nt;
+            s.tile = p.whole ? 0 : x % nt;
+        }
+        return;
+    }
+    if (p.whole) {  // a unit a block
+        LatentSeq q;
+        const int b = run / p.n_rt, rt = run % p.n_rt;
+        q.load(p, b);
+        if (lane == 0) {
+            s.left = rt < q.n_rt ? q.tiles(p, rt) : 0;
+            s.b = b;
+            s.rt = rt;
+            s.tile = 0;
+            s.q = q;
         }
         return;
     }
@@ -359,33 +363,6 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     }
 }
 
-// The short form instead: a unit a cluster, its tiles in equal parts. One warp.
-template <typename Tail>
-__device__ __forceinline__ void latent_part(const LatentAttendParams& p, int unit, int rank, Tail& s) {
-    LatentWalk k;
-    k.tile0 = 0;
-    k.left = INT32_MAX;
-    if (p.idx) {
-        k.rt = unit;
-        k.left = (p.k + LA_KEYS - 1) / LA_KEYS;  // a unit's, so that begin() ends at a token of no sequence
-        if (!k.begin(p)) k.nt = 0;
-    } else {
-        k.b = unit / p.n_rt;
-        k.rt = unit % p.n_rt;
-        k.q.load(p, k.b);
-        k.nt = k.rt < k.q.n_rt ? k.q.tiles(p, k.rt) : 0;
-    }
-    if ((threadIdx.x & 31) == 0) {
-        const int from = (int)((int64_t)k.nt * rank / p.csize);
-        s.left = (int)((int64_t)k.nt * (rank + 1) / p.csize) - from;
-        s.b = k.b;
-        s.rt = k.rt;
-        s.tile = from;
-        s.q = k.q;
-        s.there = k.nt > 0;
-    }
-}
-
 template <typename T, int DIM, int FMT>
 __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
     using C = LatentCfg<DIM>;
@@ -394,9 +371,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     uint8_t* const q_smem = ring;
     uint8_t* const kv_smem = ring + C::KV_OFF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the line: run, head tile; the short form: unit, head tile, rank
-    const int block = p.csize ? blockIdx.x / p.csize : blockIdx.x, rank = p.csize ? blockIdx.x % p.csize : 0;
-    const int run = block / p.nht, ht = block % p.nht;
+    const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
     constexpr int LOADERS = latent_loaders(FMT);
     constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
 
@@ -416,12 +391,8 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     if (warp == 4) tmem_alloc(&s.tmem, 512);
     griddep_wait();
     griddep_launch_dependents();
-    if (p.csize == 0) {
-        if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-        if (warp == 0) latent_line(p, run, s);
-    } else if (warp == 0) {
-        latent_part(p, run, rank, s);
-    }
+    if (threadIdx.x == 0 && !p.whole) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == 0) latent_line(p, run, s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -563,10 +534,9 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 m_used[h] -= SHIFT;  // what the sums are by
                 if ((lane & 3) == 0) s.factor[ra + 8 * h] = l[h] > 0.f || l[h] != l[h] ? 1.f / l[h] : 0.f;
             }
-            const bool whole = k.whole() && p.csize <= 1;
-            // (the short form's blocks keep their sums in the place of the entries, which are no longer needed)
-            float* slot = p.csize ? reinterpret_cast<float*>(kv_smem) : latent_slot(p, run, ht, k.tile0 == 0);
-            if (!whole && k.tile0 == 0 && threadIdx.x == 0 && p.csize == 0) {  // the unit goes on in later runs
+            const bool whole = k.whole();
+            float* slot = latent_slot(p, run, ht, k.tile0 == 0);
+            if (!whole && k.tile0 == 0 && threadIdx.x == 0) {  // the unit goes on in later runs
                 const Line line(s.total, p.runs);
                 const int last = (int)line.run(line.cut(run + 1) + (k.nt - k.n) - 1);
                 p.desc[blockIdx.x] = make_int4(last - run + 1, k.tok0, k.ntok, 0);
@@ -757,7 +727,6 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         const int w = warp - 8;
         uint32_t it = 0;
         if constexpr (PLAIN) {
-            clock_t last = clock();
             uint32_t n = 0;  // chunks so far: the warps take them in turn
             for (;; ++it) {
                 const int a = it % LA_ADDR, st = it & 1;
@@ -779,10 +748,6 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                     const uint32_t dst = smem_u32(kv_smem) + st * C::STAGE_BYTES + c * LA_CHUNK + (lane >> 3) * 128;
 #pragma unroll
                     for (int x = 0; x < LA_KEYS / 4; ++x) {
-                        if (LA_PACE_CLK) {
-                            while (clock() - last < LA_PACE_CLK) {}
-                            last = clock();
-                        }
                         cp_async16(dst + x * 512 + (((lane & 7) ^ (lane >> 3) ^ (x & 1) * 4) << 4),
                                    e[x] ? e[x] + c * 128 : nullptr, p.c.data);
                     }
@@ -894,29 +859,6 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     __syncthreads();
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tmem, 512);
-    if (p.csize <= 1) return;
-    // the short form's join: every block takes its share of the unit's rows from all of them
-    float* const mine = reinterpret_cast<float*>(kv_smem);
-    if (s.left == 0 && threadIdx.x < LA_ROWS) mine[LA_ROWS * (LT_VALUE + 1) + threadIdx.x] = 0.f;  // no part
-    cluster_sync();
-    if (s.there) {
-        const int share = LA_ROWS / 4 / p.csize;  // groups of four rows
-        const int tok0 = p.idx ? s.rt : s.q.at + s.rt * p.tpt, ntok = p.idx ? 1 : min(p.tpt, s.q.m - s.rt * p.tpt);
-        for (int i = threadIdx.x; i < share * (LT_VALUE / 2); i += latent_threads(FMT)) {
-            const int g = rank * share + i / (LT_VALUE / 2), d = 2 * (i % (LT_VALUE / 2));
-            if (4 * g >= ntok * p.hp) continue;
-            LatentSums sum;
-            for (int c = 0; c < p.csize; ++c) {
-                const float4 l = cluster_load4(mine + LA_ROWS * (LT_VALUE + 1) + 4 * g, c, p.csize);
-                const float4 m = cluster_load4(mine + LA_ROWS * LT_VALUE + 4 * g, c, p.csize);
-                const float4 a = cluster_load4(mine + 4 * (g * LT_VALUE + d), c, p.csize);
-                const float4 b = cluster_load4(mine + 4 * (g * LT_VALUE + d + 1), c, p.csize);
-                sum.add(m, l, a, b);
-            }
-            sum.store<T>(p, tok0, ntok, ht, 4 * g, d);
-        }
-    }
-    cluster_sync();  // nobody leaves while its sums are read
 }
 
 // Joins the units that several runs hold: a block per run, head tile, four rows and 512 / G dims, two dims a thread;
