@@ -830,15 +830,15 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                             // (here the second two lanes of a row, by halves)
                             const bool swap = j >= 2;
                             const uint4 c = v[step][x];
-                            const uint32_t lo = scale4[step] >> (swap ? 8 : 0) & 0xFFu, hi = scale4[step] >> (swap ? 0 : 8) & 0xFFu;
+                            const uint32_t lo = e4m3_pair(scale4[step] >> (swap ? 8 : 0) & 0xFFu), hi = e4m3_pair(scale4[step] >> (swap ? 0 : 8) & 0xFFu);
                             const int m0 = swap ? m + 16 : m, m1 = swap ? m : m + 16;
-                            decode8_bf16(swap ? c.z : c.x, lo, o);
+                            decode8_fp4(swap ? c.z : c.x, lo, o);
                             put(row, m0, o);
-                            decode8_bf16(swap ? c.w : c.y, lo, o);
+                            decode8_fp4(swap ? c.w : c.y, lo, o);
                             put(row, m0 + 8, o);
-                            decode8_bf16(swap ? c.x : c.z, hi, o);
+                            decode8_fp4(swap ? c.x : c.z, hi, o);
                             put(row, m1, o);
-                            decode8_bf16(swap ? c.y : c.w, hi, o);
+                            decode8_fp4(swap ? c.y : c.w, hi, o);
                             put(row, m1 + 8, o);
                         }
                     }
