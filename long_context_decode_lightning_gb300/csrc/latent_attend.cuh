@@ -252,9 +252,9 @@ __device__ __forceinline__ uint4 load_ahead16(const void* p) {
                  : "l"(p));
     return v;
 }
-__device__ __forceinline__ uint2 load_ahead8(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ uint32_t load_ahead1(const void* p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint32_t load_ahead2(const void* p) {
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         mbar_init(&s.q_full, 32), mbar_init(&s.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 4);
-            for (int g = 0; g < C::GROUPS; ++g) mbar_init(&s.full[i][g], (PLAIN ? 32 : LOADERS / 2) * C::in_group(g));
+            for (int g = 0; g < C::GROUPS; ++g) mbar_init(&s.full[i][g], PLAIN ? 32 * C::in_group(g) : LOADERS / 2);
             for (int c = 0; c < C::PAIRS; ++c) mbar_init(&s.empty[i][c], 1);
         }
         mbar_init(&s.o_empty, 4);
@@ -760,11 +760,11 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
             // Eight warps take the even tiles and eight the odd ones: a tile's loads are all issued, then waited for,
             // while the other half decodes. (Loads for the next tile among the steps of this one, by eight warps,
             // were waited for at every step: a warp has few counters of loads in flight, and waits for all on one.)
-            const int half = w >> 3, tid = (w & 7) * 32 + lane, st = half;
+            // A warp takes eight whole rows, 512 bytes of one row (FP4: 256 of two) to a load: a row is no multiple of
+            // 128 bytes, so that 128 bytes of four rows each were eight lines and twelve turns of the data path.
+            const int half = w >> 3, r0 = (w & 7) * 8, st = half;
             constexpr int CODES = FMT == LF_FP8 ? DIM - LT_TAIL : DIM;
-            // FP8: 16 codes of rows tid / 8 and + 32 a step of 128 values, FP4: 32 codes of row tid / 4
-            constexpr int R = FMT == LF_FP8 ? 2 : 1;
-            const int row = FMT == LF_FP8 ? tid >> 3 : tid >> 2, j = FMT == LF_FP8 ? tid & 7 : tid & 3;
+            constexpr int R = FMT == LF_FP8 ? 8 : 4;  // loads of codes
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t base = smem_u32(kv_smem) + st * C::STAGE_BYTES;
             const auto put = [&](int r, int m, const uint32_t (&o)[4]) {  // eight values from dim m on
@@ -776,81 +776,70 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 const int a = it % LA_ADDR;
                 ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
                 if (!ok || s.end[a]) break;
-                const uint8_t* e[R];
-#pragma unroll
-                for (int x = 0; x < R; ++x) e[x] = s.entry[a][row + 32 * x];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.addr_empty[a]);
-                uint4 v[4][R], tail[R];
-                uint2 scale[R];
-                uint32_t scale4[4];
+                uint4 v[R], tail[2];
+                uint32_t scale[R];
 #pragma unroll
                 for (int x = 0; x < R; ++x) {
                     if constexpr (FMT == LF_FP8) {
-                        scale[x] = e[x] ? load_ahead8(e[x] + CODES + 2 * LT_TAIL) : make_uint2(0u, 0u);
-#pragma unroll
-                        for (int step = 0; step < 4; ++step) {
-                            const int m = 128 * step + 16 * j;
-                            v[step][x] = e[x] && m < CODES ? load_ahead16(e[x] + m) : zero;
-                        }
-                        tail[x] = e[x] ? load_ahead16(e[x] + CODES + 16 * j) : zero;
+                        const uint8_t* const e = lane < CODES / 16 ? s.entry[a][r0 + x] : nullptr;
+                        v[x] = e ? load_ahead16(e + 16 * lane) : zero;
+                        scale[x] = e ? load_ahead1(e + CODES + 2 * LT_TAIL + (lane >> 2)) : 0u;
                     } else {
-#pragma unroll
-                        for (int step = 0; step < 4; ++step) {
-                            scale4[step] = e[x] ? load_ahead2(e[x] + 256 + 8 * step + 2 * j) : 0u;
-                            v[step][x] = e[x] ? load_ahead16(e[x] + 64 * step + 16 * j) : zero;
-                        }
+                        const uint8_t* const e = s.entry[a][r0 + 2 * x + (lane >> 4)];
+                        v[x] = e ? load_ahead16(e + 16 * (lane & 15)) : zero;
+                        scale[x] = e ? load_ahead2(e + 256 + 2 * (lane & 15)) : 0u;
                     }
                 }
+                if constexpr (FMT == LF_FP8)
 #pragma unroll
-                for (int step = 0; step < 4; ++step) {
-                    ok = __all_sync(~0u, wait_bounded(&s.empty[st][step], (it / 2 & 1) ^ 1, &s.abort));
-                    if (!ok) break;
-#pragma unroll
-                    for (int x = 0; x < R; ++x) {
-                        uint32_t o[4];
-                        const uint32_t t[4] = {tail[x].x, tail[x].y, tail[x].z, tail[x].w};
-                        if constexpr (FMT == LF_FP8) {
-                            const int m = 128 * step + 16 * j;
-                            if (m < CODES) {
-                                const uint32_t both = step < 2 ? scale[x].x : scale[x].y;
-                                const uint32_t byte = both >> (16 * (step & 1) + 8 * (j >> 2)) & 0xFFu;
-                                // a row's second four lanes store their halves the other way round, so that
-                                // eight lanes reach all banks
-                                const uint2 lo = make_uint2(v[step][x].x, v[step][x].y), hi = make_uint2(v[step][x].z, v[step][x].w);
-                                decode8_fp8(j < 4 ? lo : hi, byte, o);
-                                put(row + 32 * x, j < 4 ? m : m + 8, o);
-                                decode8_fp8(j < 4 ? hi : lo, byte, o);
-                                put(row + 32 * x, j < 4 ? m + 8 : m, o);
-                            }
-                            // the tail: past the value, or its last chunk; P has left its place with the last 128 dims
-                            if (step == 3) put(row + 32 * x, CODES + 8 * j, t);
-                        } else {
-                            const int m = 128 * step + 32 * j;
-                            // (here the second two lanes of a row, by halves)
-                            const bool swap = j >= 2;
-                            const uint4 c = v[step][x];
-                            const uint32_t lo = e4m3_pair(scale4[step] >> (swap ? 8 : 0) & 0xFFu), hi = e4m3_pair(scale4[step] >> (swap ? 0 : 8) & 0xFFu);
-                            const int m0 = swap ? m + 16 : m, m1 = swap ? m : m + 16;
-                            decode8_fp4(swap ? c.z : c.x, lo, o);
-                            put(row, m0, o);
-                            decode8_fp4(swap ? c.w : c.y, lo, o);
-                            put(row, m0 + 8, o);
-                            decode8_fp4(swap ? c.x : c.z, hi, o);
-                            put(row, m1, o);
-                            decode8_fp4(swap ? c.y : c.w, hi, o);
-                            put(row, m1 + 8, o);
-                        }
+                    for (int y = 0; y < 2; ++y) {
+                        const uint8_t* const e = s.entry[a][r0 + 4 * y + (lane >> 3)];
+                        tail[y] = e ? load_ahead16(e + CODES + 16 * (lane & 7)) : zero;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&s.full[st][2 * step / C::GROUP]);
-                        mbar_arrive(&s.full[st][(2 * step + 1) / C::GROUP]);
-                        if (step == 3 && C::CHUNKS > 2 * C::PAIRS) mbar_arrive(&s.full[st][C::GROUPS - 1]);
-                    }
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.addr_empty[a]);
+                // the whole stage: a row has all its dims
+                ok = __all_sync(~0u, wait_bounded(&s.empty[st][C::PAIRS - 1], (it / 2 & 1) ^ 1, &s.abort));
                 if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    uint32_t o[4];
+                    if constexpr (FMT == LF_FP8) {
+                        if (lane < CODES / 16) {
+                            // lanes of odd chunks store their halves the other way round: eight lanes reach all banks
+                            const bool swap = lane & 4;
+                            const uint2 lo = make_uint2(v[x].x, v[x].y), hi = make_uint2(v[x].z, v[x].w);
+                            decode8_fp8(swap ? hi : lo, scale[x], o);
+                            put(r0 + x, 16 * lane + (swap ? 8 : 0), o);
+                            decode8_fp8(swap ? lo : hi, scale[x], o);
+                            put(r0 + x, 16 * lane + (swap ? 0 : 8), o);
+                        }
+                    } else {
+                        // (here the four parts of a lane go round by its chunk)
+                        const int c = lane >> 1 & 3, r = r0 + 2 * x + (lane >> 4), m = 32 * (lane & 15);
+                        const uint32_t s0 = e4m3_pair(scale[x] & 0xFFu), s1 = e4m3_pair(scale[x] >> 8);
+                        const uint32_t p0 = c & 2 ? v[x].z : v[x].x, p1 = c & 2 ? v[x].w : v[x].y;
+                        const uint32_t p2 = c & 2 ? v[x].x : v[x].z, p3 = c & 2 ? v[x].y : v[x].w;
+                        const uint32_t lo = c & 2 ? s1 : s0, hi = c & 2 ? s0 : s1;
+                        decode8_fp4(c & 1 ? p1 : p0, lo, o);
+                        put(r, m + 8 * c, o);
+                        decode8_fp4(c & 1 ? p0 : p1, lo, o);
+                        put(r, m + 8 * (c ^ 1), o);
+                        decode8_fp4(c & 1 ? p3 : p2, hi, o);
+                        put(r, m + 8 * (c ^ 2), o);
+                        decode8_fp4(c & 1 ? p2 : p3, hi, o);
+                        put(r, m + 8 * (c ^ 3), o);
+                    }
+                }
+                if constexpr (FMT == LF_FP8)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t t[4] = {tail[y].x, tail[y].y, tail[y].z, tail[y].w};
+                        put(r0 + 4 * y + (lane >> 3), CODES + 8 * (lane & 7), t);
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane < C::GROUPS) mbar_arrive(&s.full[st][lane]);
             }
         }
     }
