@@ -798,9 +798,13 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
  *          also where it does not see it yet (0 times a NaN is a NaN).
  *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
  *  lse     (dev) fp32 [T][q_heads], may be NULL.
- *  ws      (dev) hsi_latent_attention_ws(...) bytes (k 0 without lists).
- * Rows of tokens outside every sequence are left as they were.
- * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED.
+ *  ws      (dev) hsi_latent_attention_ws(...) bytes (k 0 without lists); calls that
+ *          may run at the same time need one each.
+ * Rows of tokens outside every sequence are left as they were. The same call gives the
+ * same bits.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (the cache's dims; more than 65535 heads;
+ * bounds at which the tiles of work, 64 entries by 64 rows, pass 2^31 for a token's
+ * first 64 heads).
  */
 size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k);
 hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,

@@ -11,8 +11,14 @@
 //          bytes: dim + 80 in all.
 //  FP4     the main KV's entry (mainkv.cuh): 512 values in 288 bytes.
 //
-// Append and read are bound by HBM. Both give a warp whole rows with 8 values a
-// lane and step, so that every access is 4, 8 or 16 bytes a lane side by side.
+// Append and read are bound by HBM where there is much to move, and by a chain of
+// dependent loads (sequence, length, page) where there is little. Both give a warp whole
+// rows with 8 values a lane and step, so that every access is 4, 8 or 16 bytes a lane
+// side by side, and look places up a lane each.
+//
+// Measured: 75000 FP8 entries of 576 read back 24.9 us, 86% of the copy rate; 64 x 512
+// listed ones 13.1 us (67%); 13300 tokens appended as FP8 with rotation 8 us, and read
+// back 7.5 us; 64 tokens appended 3 us (6 a call).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

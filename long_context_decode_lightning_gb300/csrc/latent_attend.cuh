@@ -4,20 +4,41 @@
 // over the entries that a token sees, or those of a list it brings.
 //
 // A unit is up to 64 rows (row = token * heads + head) over the same entries: a
-// token's heads (or 64 of them), several tokens of few heads where there are no
-// lists. Its entries come in tiles of 64, kept in shared memory once, 64 dims of
-// the tile to a chunk, and used twice by the tensor cores:
+// token's heads (or an even share of them, at most 64), several tokens of few heads
+// where there are no lists. Its entries come in tiles of 64, kept in shared memory
+// once, 64 dims of the tile to a chunk, and used twice by the tensor cores:
 //   S = Q K^T       64 rows x 64 entries, K-major chunks
 //   O^T += V^T P^T  512 dims x 64 rows, the same chunks MN-major
 // O is kept transposed, as 64 rows x 512 dims in place take all of tensor
 // memory and leave nothing for S: transposed they are four accumulators of 128
-// dims by 64 columns. A row's rescaling (lazy, as in attend_chunk.cuh) is one of columns then.
+// dims by 64 columns. A row's rescaling (lazy, as in attend_chunk.cuh) is one of
+// columns then, by all softmax warps together; they agree on it by a vote.
 //
-// Warps: four turn S into P and write results, two issue products, one looks
-// entries up (lists, pages) a few tiles ahead, one brings the queries, and
-// eight bring the entries chunk by chunk, decoding FP8 and FP4 on the way.
-// The units' tiles form one line that is cut into equal runs, one per CTA; a
-// unit that spans runs is joined by a second kernel from fp32 partial sums.
+// Bytes and products are near balance: an entry of 1152 bytes costs 128 rows 22 ns
+// of an SM's tensor rate and 26 ns of its share of HBM. 64 rows cost the tensor
+// cores 1920 cycles a tile, which is what shared memory can feed (S 36 products of
+// 64 x 64 x 16 at 32 cycles, P V 16 of 128 x 64 x 16 at 48, both measured alone).
+//
+// Warps: four turn S into P and write results, two issue products (S and P V each
+// wait for others, and from one warp each held the other up: 455 us against 417 on
+// the prompt below), one looks entries up (lists, pages) up to three tiles ahead, one
+// brings the queries, and eight bring the entries by 16-byte asynchronous copies, which
+// take any address and any order of rows and fill with zeros what is not there (or
+// sixteen by loads, decoding FP8 and FP4). The tensor-map gather of four rows was
+// measured at 5.0 us a tile and SM from L2 against 0.7 us, one box of 64 rows at 1.6 us.
+// P stands in the place of the dims past the value, which S is done with.
+//
+// The units' tiles form one line that is cut into equal runs, one per CTA; a unit that
+// spans runs is joined by a second kernel from fp32 partial sums. Where units are as
+// many as SMs, or whole lists to a run leave few idle, none is split.
+//
+// Measured: 1024 tokens of 64 heads over 2048 listed bf16 entries of 576 each 411 us, 711
+// TFLOP/s (37% of the measured burst rate); one token of 16 x 32768 entries at 128 heads 164
+// us (2.8 TB/s, 680 TFLOP/s); of 8 x 65536 FP8 entries at 64 heads 128 us (2.1 TB/s). A tile
+// takes 1.5 to 1.9 us where 1920 cycles are 1.0: two stages leave the chain of a stage (its
+// copies 2000 cycles, S 1200 to 2000 beside the other stage's P V, softmax 1000, P V until the
+// first dims are free 700) as the bound. A first tile comes 5 us after the start, partial
+// sums leave at 32 bytes a cycle and SM (2 us), the join takes 5 to 10 us.
 #pragma once
 #include <cstdint>
 
@@ -851,10 +872,12 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
 }
 
 // Joins the units that several runs hold: a block per run, head tile, four rows and 512 / G dims, two dims a thread;
-// its G groups of threads take every G-th part and are joined through shared memory.
+// its G groups of threads take every G-th part and are joined through shared memory. G = 8 where units are few and
+// of many parts. Bound by latency: two parts' loads in flight at four blocks an SM beat four at two (nine units of 17
+// parts: 5 us less), one at six and three at three.
 constexpr int LJ_THREADS = 256;
 template <typename T, int G>
-__global__ void __launch_bounds__(LJ_THREADS) latent_join_kernel(const __grid_constant__ LatentAttendParams p) {
+__global__ void __launch_bounds__(LJ_THREADS, 4) latent_join_kernel(const __grid_constant__ LatentAttendParams p) {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int PER = LJ_THREADS / G;
@@ -885,7 +908,7 @@ __global__ void __launch_bounds__(LJ_THREADS) latent_join_kernel(const __grid_co
     const int g = threadIdx.x / PER, t = threadIdx.x % PER, d = 2 * (blockIdx.x % G * PER + t);
     const int4 unit = p.desc[at];
     if (unit.x == 0 || row0 >= unit.z * p.hp) return;
-    constexpr int AT_ONCE = 4;  // parts whose loads are in flight
+    constexpr int AT_ONCE = 2;  // parts whose loads are in flight
     LatentSums sum;
     for (int c0 = g; c0 < unit.x; c0 += G * AT_ONCE) {
         float4 mc[AT_ONCE], lc[AT_ONCE], a[AT_ONCE], b[AT_ONCE];
