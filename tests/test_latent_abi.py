@@ -194,3 +194,23 @@ def test_the_binding_refuses_calls(L):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {n} was taken")
+
+
+def test_scratch_that_a_call_makes_belongs_to_its_stream(L, monkeypatch):
+    """Without a workspace the wrapper makes one on the given stream, and hands the kernel that stream."""
+    class Stream:
+        cuda_stream = 77
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, args))
+                return 4096 if name.endswith("_ws") else 0
+            return call
+
+    calls, made_for, s, c = [], [], Stream(), made()
+    monkeypatch.setattr(hsi, "_lib", Lib())
+    monkeypatch.setattr(hsi, "_scratch", lambda n, device, stream: made_for.append((n, stream)) or gpu(n, dtype=torch.uint8))
+    hsi.latent_attention(c, gpu(4, 8, 576), gpu(3, dtype=torch.int32), 1, 64, 0.1, gpu(4, 8, 512), stream=s)
+    assert made_for == [(4096, s)]
+    assert [name for name, _ in calls] == ["hsi_latent_attention_ws", "hsi_latent_attention"] and calls[-1][1][-1] == 77
