@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     typename C::Tail& s = *reinterpret_cast<typename C::Tail*>(ring + C::RING_BYTES);
     uint8_t* const q_smem = ring;
     uint8_t* const kv_smem = ring + C::KV_OFF;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (put into a uniform register, so that the roles' code is known not to part a warp's lanes)
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
     constexpr int LOADERS = latent_loaders(FMT);
     constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
@@ -617,13 +618,14 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
         const uint32_t q_desc = uniform(smem_desc_sw128(smem_u32(q_smem))), k_desc = smem_desc_sw128(smem_u32(kv_smem));
         uint32_t it = 0, seg = 0;  // tiles and segments so far
-        for (; ok && k.begin(p); k.advance(p), ++seg) {
+        for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
+            const int n = (int)uniform(k.n);
             ok = __all_sync(~0u, wait_bounded(&s.q_full, seg & 1, &s.abort));
-            for (int i = 0; ok && i < k.n; ++i, ++it) {
+            for (int i = 0; i < n && __all_sync(~0u, ok); ++i, ++it) {
                 // a stage is filled again when its last tile's P V is done, so its S has been read, too
                 const uint32_t st = uniform(it & 1), d = uniform(tmem + LA_S_COL + st * LA_KEYS);
                 const uint32_t kd = uniform(k_desc + st * STAGE16);
-                const bool end = i + 1 == k.n;
+                const bool end = i + 1 == n;
 #pragma unroll
                 for (int g = 0; g < C::GROUPS; ++g) {
                     ok = ok && wait_bounded(&s.full[st][g], it / 2 & 1, &s.abort);
@@ -657,9 +659,10 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         const uint32_t tm = uniform(tmem), v_desc = smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK),
                        p_desc = smem_desc_sw128(smem_u32(kv_smem) + C::P_OFF);
         uint32_t it = 0, seg = 0;
-        for (; ok && k.begin(p); k.advance(p), ++seg) {
+        for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
+            const int n = (int)uniform(k.n);
             ok = __all_sync(~0u, wait_bounded(&s.o_empty, (seg & 1) ^ 1, &s.abort));
-            for (int i = 0; ok && i < k.n; ++i, ++it) {
+            for (int i = 0; i < n && __all_sync(~0u, ok); ++i, ++it) {
                 const uint32_t st = uniform(it & 1), vd = uniform(v_desc + st * STAGE16);
                 const uint32_t pd = uniform(p_desc + st * STAGE16), more = uniform((uint32_t)i);
                 ok = __all_sync(~0u, wait_bounded(&s.p_full[st], it / 2 & 1, &s.abort));
