@@ -440,12 +440,13 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
             if (lane == 0) all[warp] = mine;
             bar_sync(1, 128);
             const uint32_t sum = all[0] | all[1] | all[2] | all[3];
-            *any = sum & 1u;
-            ok = !(sum & 2u);
+            *any = __any_sync(~0u, sum & 1u);
+            ok = !__any_sync(~0u, sum & 2u);
             return ok;
         };
         bool any;
-        for (; ok && k.begin(p); k.advance(p), ++seg) {
+        for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
+            const int n = (int)uniform(k.n);
             if (threadIdx.x < LA_ROWS) {
                 const int i = (int)threadIdx.x * p.inv_hp >> 16, h = ht * p.hp + threadIdx.x - i * p.hp;
                 s.row_out[threadIdx.x] = i < k.ntok && h < p.H ? (int64_t)(k.tok0 + i) * p.ot + (int64_t)h * p.oh : -1;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
                 lim[h] = p.idx ? INT32_MAX : k.sees(p, min(i, k.ntok - 1));
             }
             const int lim_all = p.idx ? INT32_MAX : k.sees(p, 0);  // entries that every row sees
-            for (int i = 0; i < k.n; ++i, ++it) {
+            for (int i = 0; i < n; ++i, ++it) {
                 const int k0 = (k.tile0 + i) * LA_KEYS, a = it % LA_ADDR;
                 ok = ok && __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort) &&
                                          wait_bounded(&s.s_full[it & 1], it / 2 & 1, &s.abort));
@@ -616,15 +617,15 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     } else if (warp == 4) {  // S: the warp waits, one lane issues
         const uint32_t id_s = idesc_f16(is_bf16<T>, LA_ROWS, LA_KEYS, false) | (p.negate ? 1u << 13 : 0u);  // of -Q
         constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
-        const uint32_t q_desc = uniform(smem_desc_sw128(smem_u32(q_smem))), k_desc = smem_desc_sw128(smem_u32(kv_smem));
+        const uint32_t q_desc = uniform(smem_desc_sw128(smem_u32(q_smem))), tm = uniform(tmem),
+                       k_desc = uniform(smem_desc_sw128(smem_u32(kv_smem)));
         uint32_t it = 0, seg = 0;  // tiles and segments so far
         for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
             const int n = (int)uniform(k.n);
             ok = __all_sync(~0u, wait_bounded(&s.q_full, seg & 1, &s.abort));
             for (int i = 0; i < n && __all_sync(~0u, ok); ++i, ++it) {
                 // a stage is filled again when its last tile's P V is done, so its S has been read, too
-                const uint32_t st = uniform(it & 1), d = uniform(tmem + LA_S_COL + st * LA_KEYS);
-                const uint32_t kd = uniform(k_desc + st * STAGE16);
+                const uint32_t st = it & 1, d = tm + LA_S_COL + st * LA_KEYS, kd = k_desc + st * STAGE16;
                 const bool end = i + 1 == n;
 #pragma unroll
                 for (int g = 0; g < C::GROUPS; ++g) {
@@ -656,15 +657,14 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     } else if (warp == 6) {  // P V, from a warp of its own: each issues while the other waits
         constexpr uint32_t id_o = idesc_f16(is_bf16<T>, 128, LA_ROWS, false) | 1u << 15;  // A = V^T, MN-major
         constexpr uint32_t CHUNK16 = LA_CHUNK >> 4, STAGE16 = C::STAGE_BYTES >> 4;
-        const uint32_t tm = uniform(tmem), v_desc = smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK),
-                       p_desc = smem_desc_sw128(smem_u32(kv_smem) + C::P_OFF);
+        const uint32_t tm = uniform(tmem), v_desc = uniform(smem_desc_sw128(smem_u32(kv_smem), LA_CHUNK)),
+                       p_desc = uniform(smem_desc_sw128(smem_u32(kv_smem) + C::P_OFF));
         uint32_t it = 0, seg = 0;
         for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
             const int n = (int)uniform(k.n);
             ok = __all_sync(~0u, wait_bounded(&s.o_empty, (seg & 1) ^ 1, &s.abort));
             for (int i = 0; i < n && __all_sync(~0u, ok); ++i, ++it) {
-                const uint32_t st = uniform(it & 1), vd = uniform(v_desc + st * STAGE16);
-                const uint32_t pd = uniform(p_desc + st * STAGE16), more = uniform((uint32_t)i);
+                const uint32_t st = it & 1, vd = v_desc + st * STAGE16, pd = p_desc + st * STAGE16, more = i;
                 ok = __all_sync(~0u, wait_bounded(&s.p_full[st], it / 2 & 1, &s.abort));
                 if (!ok) break;
                 fence_proxy_async_smem();  // the entries' copies as well, which the softmax of their S came after
@@ -690,8 +690,9 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
         }
     } else if (warp == 5) {  // entries: where the tiles' rows are
         uint32_t it = 0;
-        for (; ok && k.begin(p); k.advance(p)) {
-            for (int i = 0; i < k.n && ok; ++i, ++it) {
+        for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p)) {
+            const int n = (int)uniform(k.n);
+            for (int i = 0; i < n && __all_sync(~0u, ok); ++i, ++it) {
                 const int k0 = (k.tile0 + i) * LA_KEYS, a = it % LA_ADDR;
                 const uint8_t* at[2];
 #pragma unroll
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     } else if (warp == 7) {  // queries, a unit at a time
         const T* const q = static_cast<const T*>(p.q);
         uint32_t seg = 0;
-        for (; ok && k.begin(p); k.advance(p), ++seg) {
+        for (; __all_sync(~0u, ok && k.begin(p)); k.advance(p), ++seg) {
             ok = __all_sync(~0u, wait_bounded(&s.q_empty, (seg & 1) ^ 1, &s.abort));
             if (!ok) break;
             const int r0 = lane >> 3, j = lane & 7;
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
             for (;; ++it) {
                 const int a = it % LA_ADDR, st = it & 1;
                 ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
-                if (!ok || s.end[a]) break;
+                if (__any_sync(~0u, !ok || s.end[a])) break;
                 const uint8_t* e[LA_KEYS / 4];  // of rows 4 x + lane / 8, this lane's 16 bytes of a chunk
 #pragma unroll
                 for (int x = 0; x < LA_KEYS / 4; ++x) {
@@ -799,7 +800,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
             for (it = half;; it += 2) {
                 const int a = it % LA_ADDR;
                 ok = __all_sync(~0u, wait_bounded(&s.addr_full[a], it / LA_ADDR & 1, &s.abort));
-                if (!ok || s.end[a]) break;
+                if (__any_sync(~0u, !ok || s.end[a])) break;
                 uint4 v[R], tail[2];
                 uint32_t scale[R];
 #pragma unroll
