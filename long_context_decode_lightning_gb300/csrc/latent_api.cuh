@@ -75,10 +75,10 @@ size_t latent_desc_bytes(const LatentTiles& t, int64_t runs) { return align_up((
 
 // Whether units go whole to blocks (no partial sums, no second kernel): where the most tiles that a block then has are
 // no more than those of the line's runs and what the join costs, eight tiles' time where all SMs leave partial sums.
-// Measured, one token, 64 heads over bf16 entries of 576, us whole against line: 64 tokens of 512 listed entries 24 and
-// 30, 20 of them 22 and 22, 30 sequences of 600 entries 25 and 26, 150 tokens of 256 listed 19 and 25; eight tokens of
-// 1024 listed 35 and 27, one sequence of 200 entries 14 and 11. (Clusters of 2, 4 or 8 blocks a unit, joined through
-// distributed shared memory, were slower than the better of the two in every one of these.)
+// Measured, 64 heads over bf16 entries of 576, us whole against line: 64 tokens of 512 listed entries 20 and 27, 20 of
+// them 19 and 20, 30 sequences of 600 entries 22 and 23, 150 tokens of 256 listed 16 and 22; eight tokens of 1024
+// listed 30 and 20, four sequences of 1000 entries 29 and 16. (Clusters of 2, 4 or 8 blocks a unit, joined through
+// distributed shared memory, were slower than the better of the two in all but one of sixteen such cases.)
 bool latent_whole(const LatentAttendParams& p, int64_t tiles) {
     const int64_t keys = p.idx ? p.k : p.max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS, room = sm_count() / p.nht;
     const int64_t units = p.idx ? p.T : (int64_t)p.c.B * p.n_rt;
@@ -88,7 +88,7 @@ bool latent_whole(const LatentAttendParams& p, int64_t tiles) {
 
 template <typename T, int DIM, int FMT>
 hsi_status launch_latent_attend(const LatentAttendParams& p, int64_t units, cudaStream_t s) {
-    using C = LatentCfg<DIM>;
+    using C = LatentCfg<DIM, FMT>;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (smem_attr_once(latent_attend_kernel<T, DIM, FMT>, C::SMEM_BYTES, attr_set) != HSI_OK) return HSI_ERR_CUDA;
     const unsigned grid = (unsigned)(p.runs * p.nht);

@@ -22,7 +22,7 @@
 // Warps: four turn S into P and write results, two issue products (S and P V each
 // wait for others, and from one warp each held the other up: 455 us against 417 on
 // the prompt below), one looks entries up (lists, pages) up to three tiles ahead, one
-// brings the queries, and eight bring the entries by 16-byte asynchronous copies, which
+// brings the queries, and four bring the entries by 16-byte asynchronous copies, which
 // take any address and any order of rows and fill with zeros what is not there (or
 // sixteen by loads, decoding FP8 and FP4). The tensor-map gather of four rows was
 // measured at 5.0 us a tile and SM from L2 against 0.7 us, one box of 64 rows at 1.6 us.
@@ -32,10 +32,10 @@
 // spans runs is joined by a second kernel from fp32 partial sums. Where units are as
 // many as SMs, or whole lists to a run leave few idle, none is split.
 //
-// Measured: 1024 tokens of 64 heads over 2048 listed bf16 entries of 576 each 411 us, 711
-// TFLOP/s (37% of the measured burst rate); one token of 16 x 32768 entries at 128 heads 164
-// us (2.8 TB/s, 680 TFLOP/s); of 8 x 65536 FP8 entries at 64 heads 128 us (2.1 TB/s). A tile
-// takes 1.5 to 1.9 us where 1920 cycles are 1.0: two stages leave the chain of a stage (its
+// Measured: 1024 tokens of 64 heads over 2048 listed bf16 entries of 576 each 372 us, 784
+// TFLOP/s (41% of the measured burst rate); one token of 16 x 32768 entries at 128 heads 153
+// us (3.05 TB/s, 730 TFLOP/s); of 8 x 65536 FP8 entries at 64 heads 117 us (2.3 TB/s). A tile
+// takes 1.3 to 1.7 us where 1920 cycles are 1.0: two stages leave the chain of a stage (its
 // copies 2000 cycles, S 1200 to 2000 beside the other stage's P V, softmax 1000, P V until the
 // first dims are free 700) as the bound. A first tile comes 5 us after the start, partial
 // sums leave at 32 bytes a cycle and SM (2 us), the join takes 5 to 10 us.
@@ -51,8 +51,10 @@ namespace hsi {
 
 constexpr int LA_ROWS = 64;   // rows of a unit
 constexpr int LA_KEYS = 64;   // entries of a tile
-constexpr int LA_S_GROUPS = 2;  // S is issued as soon as half of a tile's dims are there
-__host__ __device__ constexpr int latent_loaders(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16 ? 8 : 16; }
+__host__ __device__ constexpr bool latent_plain(int fmt) { return fmt == LF_BF16 || fmt == LF_FP16; }  // copied as they are
+// Warps that bring entries: four that copy (eight: 448 us against 435 on chunks, the rest within 2%), or two times eight
+// that decode.
+__host__ __device__ constexpr int latent_loaders(int fmt) { return latent_plain(fmt) ? 4 : 16; }
 __host__ __device__ constexpr int latent_threads(int fmt) { return 32 * (8 + latent_loaders(fmt)); }
 constexpr int LA_CHUNK = LA_KEYS * 128;  // bytes of 64 dims of a tile, of a unit's queries, and of P
 constexpr int LA_ADDR = 3;    // tiles whose entries are looked up ahead
@@ -210,14 +212,14 @@ struct LatentWalk {
     }
 };
 
-template <int DIM>
+template <int DIM, int FMT>
 struct LatentCfg {
     static constexpr int CHUNKS = DIM / 64, PAIRS = LT_VALUE / 128;
     // a stage holds a tile: eight chunks of the value, then one of the dims past it, in whose place P comes once S is done
     static constexpr int STAGE_BYTES = (2 * PAIRS + 1) * LA_CHUNK, P_OFF = 2 * PAIRS * LA_CHUNK;
     static constexpr int KV_OFF = CHUNKS * LA_CHUNK, RING_BYTES = KV_OFF + 2 * STAGE_BYTES;
-    // S is issued by groups of chunks
-    static constexpr int GROUPS = LA_S_GROUPS, GROUP = (CHUNKS + GROUPS - 1) / GROUPS;
+    // S is issued by groups of chunks: as soon as half of a tile's dims are there; decoded tiles come whole
+    static constexpr int GROUPS = latent_plain(FMT) ? 2 : 1, GROUP = (CHUNKS + GROUPS - 1) / GROUPS;
     __host__ __device__ static constexpr int in_group(int g) { return g + 1 < GROUPS ? GROUP : CHUNKS - g * GROUP; }
     struct Tail {
         uint64_t q_full, q_empty, s_full[2], p_full[2], o_empty, done[2];
@@ -386,7 +388,7 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
 
 template <typename T, int DIM, int FMT>
 __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
-    using C = LatentCfg<DIM>;
+    using C = LatentCfg<DIM, FMT>;
     extern __shared__ __align__(1024) uint8_t ring[];
     typename C::Tail& s = *reinterpret_cast<typename C::Tail*>(ring + C::RING_BYTES);
     uint8_t* const q_smem = ring;
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int run = blockIdx.x / p.nht, ht = blockIdx.x % p.nht;
     constexpr int LOADERS = latent_loaders(FMT);
-    constexpr bool PLAIN = FMT == LF_BF16 || FMT == LF_FP16;  // copied as they are
+    constexpr bool PLAIN = latent_plain(FMT);
 
     if (threadIdx.x == 0) {
         mbar_init(&s.q_full, 32), mbar_init(&s.q_empty, 1);
