@@ -766,7 +766,7 @@ hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64
 /*
  * Entries back as rows of dim 16-bit values (fp16 of an FP16 cache, bf16 otherwise;
  * every value of FP8 and FP4 entries that hsi_latent_append writes is exact).
- *  idx NULL: row r of row_start[b] .. row_start[b+1] - 1 (of T rows) is entry
+ *  idx NULL (and k 0): row r of row_start[b] .. row_start[b+1] - 1 (of T rows) is entry
  *          (first ? first[b] : 0) + r - row_start[b] of sequence b.
  *  idx     (dev) int32 [T][ld_idx]: the k entries of each of T tokens, sequence b's
  *          being row_start[b] .. row_start[b+1] - 1; a negative one gives zeros. Row i of
@@ -785,7 +785,7 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
  * entries c_e:  out = sum_e p_e c_e[0:512] / sum_e p_e,  p_e = exp(scale q.c_e),
  * lse = ln sum_e p_e  (fp32; -inf for a row that sees no entry, whose out is 0; NaN, as
  * out, for a row that sees a NaN score). Token i of sequence b's n sees
- *  idx NULL: entries e < kv_len[b] - n + i + 1 (causal) or e < kv_len[b];
+ *  idx NULL (and k 0): entries e < kv_len[b] - n + i + 1 (causal) or e < kv_len[b];
  *  idx     (dev) int32 [T][ld_idx]: the k entries of its list. A negative one is passed
  *          over; one that the token does not see by the rule above is passed over and
  *          reported as HSI_ERR_DEVICE_ARG; one that is listed twice counts twice.
@@ -802,9 +802,9 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
  *          may run at the same time need one each.
  * Rows of tokens outside every sequence are left as they were. The same call gives the
  * same bits.
- * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (the cache's dims; more than 65535 heads;
- * bounds at which the tiles of work, 64 entries by 64 rows, pass 2^31 for a token's
- * first 64 heads).
+ * Errors: INVALID_ARG (k other than 0 without idx among them), WORKSPACE, UNSUPPORTED
+ * (the cache's dims; more than 65535 heads; bounds at which the tiles of work, 64
+ * entries by 64 rows, pass 2^31 for a token's first 64 heads).
  */
 size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k);
 hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,

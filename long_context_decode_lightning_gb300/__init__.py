@@ -749,11 +749,14 @@ class LatentCache:
 
 
 def _lists(idx, T: int):
-    """Address, row stride and width of int32 [T, k] lists with contiguous rows."""
+    """Address, row stride and width of int32 [T, k] lists with contiguous rows. A tensor without elements has no address,
+    which would read as a call without lists."""
     if idx is None:
         return None, 0, 0
     if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or idx.stride(1) != 1 or not idx.is_cuda:
         _bad(f"idx: int32 [{T}, entries], rows contiguous, on the GPU")
+    if idx.shape[1] == 0:
+        _bad("idx: lists of one entry at least (negative ones are passed over)")
     return idx.data_ptr(), idx.stride(0) if T > 1 else idx.shape[1], idx.shape[1]
 
 

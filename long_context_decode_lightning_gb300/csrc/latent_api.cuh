@@ -42,7 +42,10 @@ hsi_status latent_view(const hsi_latent_cache* c, LatentView* v) {
     return HSI_OK;
 }
 
-bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) { return k > 0 && ld_idx >= k && aligned(idx, 4); }
+// (a k without lists is the list of a caller whose tensor holds nothing and so has no address)
+bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) {
+    return idx ? k > 0 && ld_idx >= k && aligned(idx, 4) : k == 0;
+}
 
 // How heads and tokens make units of at most 64 rows.
 struct LatentTiles {
@@ -143,7 +146,7 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
     const hsi_status st = latent_view(cache, &p.c);
     if (st != HSI_OK) return st;
     if (!row_start || T <= 0 || T > INT32_MAX || !rows_ok(out, out_stride, 0)) return HSI_ERR_INVALID_ARG;
-    if (idx && (!lists_ok(idx, ld_idx, k) || first)) return HSI_ERR_INVALID_ARG;
+    if (!lists_ok(idx, ld_idx, k) || (idx && first)) return HSI_ERR_INVALID_ARG;
     if (T > 1 && out_stride < (int64_t)cache->dim * (idx ? k : 1)) return HSI_ERR_INVALID_ARG;  // two results in one place
     p.start = row_start;
     p.first = first;
@@ -180,7 +183,7 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     const hsi_status st = latent_view(cache, &p.c);
     if (st != HSI_OK) return st;
     if (!q_start || T <= 0 || T > INT32_MAX || max_q <= 0 || max_kv <= 0 || max_kv > INT32_MAX || q_heads <= 0 ||
-        !rows_ok(q, q_token_stride, q_head_stride) || !(scale == scale) || (idx && !lists_ok(idx, ld_idx, k)))
+        !rows_ok(q, q_token_stride, q_head_stride) || !(scale == scale) || !lists_ok(idx, ld_idx, k))
         return HSI_ERR_INVALID_ARG;
     if (!rows_ok(out, o_token_stride, o_head_stride) || out == q || (T > 1 && o_token_stride < LT_VALUE) ||
         (q_heads > 1 && o_head_stride < LT_VALUE))

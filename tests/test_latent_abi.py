@@ -103,6 +103,13 @@ def test_wrong_attentions(L, status, kw):
     assert attend(L, cache(), **kw) == status
 
 
+def test_a_list_of_no_entries_is_not_the_want_of_lists(L):
+    """k without idx (the address of an empty tensor is NULL): refused, not attention over everything."""
+    assert attend(L, cache(), idx=None, k=5) == -1
+    assert attend(L, cache(), idx=None, ld=5, k=5) == -1
+    assert read(L, cache(), idx=None, ld=5, k=5, ot=5 * 576) == -1
+
+
 def test_lengths_that_31_bits_cannot_count(L):
     wide = cache(table=None, offsets=F, n_pages=(1 << 31) + 5)
     assert attend(L, wide, max_kv=(1 << 31) - 1) == -2
@@ -214,3 +221,19 @@ def test_scratch_that_a_call_makes_belongs_to_its_stream(L, monkeypatch):
     hsi.latent_attention(c, gpu(4, 8, 576), gpu(3, dtype=torch.int32), 1, 64, 0.1, gpu(4, 8, 512), stream=s)
     assert made_for == [(4096, s)]
     assert [name for name, _ in calls] == ["hsi_latent_attention_ws", "hsi_latent_attention"] and calls[-1][1][-1] == 77
+
+
+@pytest.mark.parametrize("idx", [gpu(4, 0, dtype=torch.int32), gpu(4, 7, dtype=torch.int32)[:, :0]])
+def test_the_binding_refuses_lists_of_no_entries(L, monkeypatch, idx):
+    """Such a tensor has no address, which the library would take for a call without lists."""
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: called.append(name) or 0
+
+    c, q_start, called = made(), gpu(3, dtype=torch.int32), []
+    monkeypatch.setattr(hsi, "_lib", Lib())
+    with pytest.raises(ValueError, match="idx"):
+        hsi.latent_attention(c, gpu(4, 8, 576), q_start, 1, 64, 0.1, gpu(4, 8, 512), idx=idx, ws=gpu(8))
+    with pytest.raises(ValueError, match="idx"):
+        hsi.latent_read(c, gpu(4, 0, 576), q_start, idx=idx)
+    assert not called
