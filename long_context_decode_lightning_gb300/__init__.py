@@ -724,6 +724,8 @@ class LatentCache:
         if self.c.offsets:
             _bad("table: the cache is contiguous")
         ld = _table(t, "table", self.B)
+        if t.shape[1] == 0:  # it has no address, by which a paged cache is known
+            _bad("table: one page a sequence at least (none of them need be used)")
         self._table, self.c.table, self.c.ld_table, self.c.table_width = t, t.data_ptr(), ld, t.shape[1]
 
     @property

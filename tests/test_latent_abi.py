@@ -237,3 +237,15 @@ def test_the_binding_refuses_lists_of_no_entries(L, monkeypatch, idx):
     with pytest.raises(ValueError, match="idx"):
         hsi.latent_read(c, gpu(4, 0, 576), q_start, idx=idx)
     assert not called
+
+
+def test_the_binding_refuses_a_table_of_no_pages(L):
+    """Such a tensor has no address, by which a paged cache would count as one that may be given offsets."""
+    for none in (gpu(2, 0, dtype=torch.int32), gpu(2, 4, dtype=torch.int32)[:, :0]):
+        with pytest.raises(ValueError, match="table"):
+            made(table=none)
+        c = made()
+        kept = c.table
+        with pytest.raises(ValueError, match="table"):
+            c.table = none
+        assert c.table is kept and c.c.table == kept.data_ptr()
