@@ -756,8 +756,9 @@ size_t hsi_latent_entry_bytes(hsi_latent_format format, int32_t dim);
  *          by hsi_rope (rot a multiple of 16, rot_offset of 8: UNSUPPORTED otherwise)
  *          and rounded to x's type, then kept as the format keeps them.
  * FP8: e is the smallest in [-118, 120] by which the largest of the 64 values is at
- * most 448, the code E4M3_RN(x / 2^e). FP4: as hsi_quantize_mainkv. Values must be
- * finite for both; others are reported as HSI_ERR_DEVICE_ARG.
+ * most 448, the code E4M3_RN(x / 2^e), at e = 120 no further from 0 than 240 (256 * 2^120
+ * is past bf16). FP4: as hsi_quantize_mainkv. Values must be finite for both; others are
+ * reported as HSI_ERR_DEVICE_ARG.
  */
 hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64_t x_token_stride,
                              const int32_t* q_start, int64_t T, const int32_t* positions, const uint64_t* steps,

@@ -7,8 +7,9 @@
 //  FP8     E4M3 codes of the first dim - 64 values, the last 64 (where rotary
 //          dims lie) in bf16, then a byte for each 64 codes, 127 + e: their values are
 //          code * 2^e, e the smallest by which the largest of the 64 is at most 448. As
-//          the scale is a power of two, decoded values are exact in bf16. Padded to 16
-//          bytes: dim + 80 in all.
+//          the scale is a power of two, decoded values are exact in bf16 (at the largest e
+//          codes end at 240, as 256 * 2^120 is no bf16 number). Padded to 16 bytes:
+//          dim + 80 in all.
 //  FP4     the main KV's entry (mainkv.cuh): 512 values in 288 bytes.
 //
 // Append and read are bound by HBM where there is much to move, and by a chain of
@@ -37,7 +38,8 @@ enum LatentFormat { LF_BF16 = 0, LF_FP16 = 1, LF_FP8 = 2, LF_FP4 = 3 };
 
 constexpr int LT_VALUE = 512;      // dims of the value
 constexpr int LT_TAIL = 64;        // values of an FP8 entry that stay in bf16
-constexpr int LT_MIN_E = -118, LT_MAX_E = 120;  // scales' exponents: every code's value is a bf16 number
+constexpr int LT_MIN_E = -118, LT_MAX_E = 120;  // scales' exponents
+constexpr float LT_MAX_FP8 = 0x1.Ep127f;        // 240 * 2^120: the next code of the largest exponent is past bf16
 
 __host__ __device__ constexpr int latent_entry_bytes(int fmt, int dim) {
     return fmt == LF_FP8 ? dim + 80 : fmt == LF_FP4 ? KV_BYTES : 2 * dim;
@@ -244,6 +246,10 @@ __device__ __forceinline__ void latent_keep(int dim, const uint4 (&raw)[3], uint
             ex = max(LT_MIN_E, min(LT_MAX_E, ex));
             const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (m < codes) {
+                if (ex == LT_MAX_E) {  // values up to 255 * 2^120: 15 in 255 off at most, less than half a step's 2^-4
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(v[j], -LT_MAX_FP8), LT_MAX_FP8);
+                }
                 uint32_t c[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
