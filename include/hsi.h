@@ -804,8 +804,9 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
  * Rows of tokens outside every sequence are left as they were. The same call gives the
  * same bits.
  * Errors: INVALID_ARG (k other than 0 without idx among them), WORKSPACE, UNSUPPORTED
- * (the cache's dims; more than 65535 heads; bounds at which the tiles of work, 64
- * entries by 64 rows, pass 2^31 for a token's first 64 heads).
+ * (the cache's dims; more than 65535 heads; k, or max_kv and what the cache holds, past
+ * 2^31 - 4097; bounds at which the tiles of work, 64 entries by 64 rows, pass 2^31 for a
+ * token's first 64 heads).
  */
 size_t hsi_latent_attention_ws(int32_t B, int32_t q_heads, int64_t T, int32_t max_q, int64_t max_kv, int32_t k);
 hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, int64_t q_token_stride,

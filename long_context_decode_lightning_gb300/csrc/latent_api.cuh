@@ -191,7 +191,7 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     if (q_heads > 65535) return HSI_ERR_UNSUPPORTED;
     p.max_kv = (int)(max_kv < p.c.capacity ? max_kv : p.c.capacity);
     p.max_q = (int)(max_q < T ? max_q : T);
-    if (p.max_kv > INT32_MAX - 4096) return HSI_ERR_UNSUPPORTED;
+    if (p.max_kv > INT32_MAX - 4096 || k > INT32_MAX - 4096) return HSI_ERR_UNSUPPORTED;  // rounded up to tiles in 32 bits
     const LatentTiles tiles(q_heads, idx != nullptr);
     const int64_t most = latent_tiles(tiles, cache->B, T, p.max_q, p.max_kv, idx ? k : 0);
     if (most > INT32_MAX) return HSI_ERR_UNSUPPORTED;  // the kernels count them in 31 bits

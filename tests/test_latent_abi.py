@@ -115,6 +115,17 @@ def test_lengths_that_31_bits_cannot_count(L):
     assert attend(L, wide, max_kv=(1 << 31) - 1) == -2
 
 
+@pytest.mark.parametrize("k", [(1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 4096])
+def test_lists_that_31_bits_cannot_count(L, k):
+    """The kernels round k up to whole tiles in 32 bits; refused before the workspace is looked at."""
+    assert attend(L, cache(), idx=F, ld=k, k=k, T=1, ws=None) == -2
+    assert attend(L, cache(), idx=F, ld=1 << 40, k=k, T=1, ws=None) == -2
+
+
+def test_the_longest_lists_are_counted(L):
+    assert attend(L, cache(), idx=F, ld=(1 << 31) - 1, k=(1 << 31) - 4097, T=1, ws=None) == -5  # (but for the workspace)
+
+
 def test_kernels_use_the_barrier_helpers():
     for name in ("latent.cuh", "latent_attend.cuh"):
         assert not BARRIER.search(_source(name)), name
