@@ -728,7 +728,8 @@ typedef enum {
  * [0, T] is clamped or skipped and reported as HSI_ERR_DEVICE_ARG by
  * hsi_device_error. Tokens lie side by side and belong to sequences as in the paged
  * cache: sequence b's are q_start[b] .. q_start[b+1] - 1, its last entries. What the
- * cache holds outside the sequences' entries never reaches a result.
+ * cache holds outside the sequences' entries never reaches a result. Of one token or
+ * one head, the calls below do not look at the stride between tokens or heads.
  */
 typedef struct {
     void* data;

@@ -755,7 +755,8 @@ def _lists(idx, T: int):
     which would read as a call without lists."""
     if idx is None:
         return None, 0, 0
-    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or idx.stride(1) != 1 or not idx.is_cuda:
+    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or not idx.is_cuda or \
+            (idx.shape[1] > 1 and idx.stride(1) != 1):
         _bad(f"idx: int32 [{T}, entries], rows contiguous, on the GPU")
     if idx.shape[1] == 0:
         _bad("idx: lists of one entry at least (negative ones are passed over)")

@@ -42,6 +42,9 @@ hsi_status latent_view(const hsi_latent_cache* c, LatentView* v) {
     return HSI_OK;
 }
 
+// The distance of n rows; of one row none, whatever the caller's.
+int64_t row_stride(int64_t n, int64_t stride) { return n > 1 ? stride : 0; }
+
 // (a k without lists is the list of a caller whose tensor holds nothing and so has no address)
 bool lists_ok(const int32_t* idx, int64_t ld_idx, int32_t k) {
     return idx ? k > 0 && ld_idx >= k && aligned(idx, 4) : k == 0;
@@ -118,7 +121,8 @@ hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64
     LatentAppendParams p{};
     const hsi_status st = latent_view(cache, &p.c);
     if (st != HSI_OK) return st;
-    if (!q_start || T <= 0 || T > INT32_MAX || !rows_ok(x, x_token_stride, 0)) return HSI_ERR_INVALID_ARG;
+    p.xt = row_stride(T, x_token_stride);
+    if (!q_start || T <= 0 || T > INT32_MAX || !rows_ok(x, p.xt, 0)) return HSI_ERR_INVALID_ARG;
     if (steps) {
         if (!positions || !aligned(positions, 4) || !aligned(steps, 8) || !turn_ok(cache->dim, rot, rot_offset) ||
             !(gain == gain))
@@ -127,7 +131,6 @@ hsi_status hsi_latent_append(const hsi_latent_cache* cache, const void* x, int64
         p.r = {reinterpret_cast<const unsigned long long*>(steps), positions, rot, rot_offset, interleaved != 0, gain, 1.f};
     }
     p.x = x;
-    p.xt = x_token_stride;
     p.T = T;
     p.q_start = q_start;
     const dim3 grid((unsigned)((T + LT_WARPS - 1) / LT_WARPS)), block(32 * LT_WARPS);
@@ -145,9 +148,10 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
     LatentReadParams p{};
     const hsi_status st = latent_view(cache, &p.c);
     if (st != HSI_OK) return st;
-    if (!row_start || T <= 0 || T > INT32_MAX || !rows_ok(out, out_stride, 0)) return HSI_ERR_INVALID_ARG;
+    p.ot = row_stride(T, out_stride);
+    if (!row_start || T <= 0 || T > INT32_MAX || !rows_ok(out, p.ot, 0)) return HSI_ERR_INVALID_ARG;
     if (!lists_ok(idx, ld_idx, k) || (idx && first)) return HSI_ERR_INVALID_ARG;
-    if (T > 1 && out_stride < (int64_t)cache->dim * (idx ? k : 1)) return HSI_ERR_INVALID_ARG;  // two results in one place
+    if (T > 1 && p.ot < (int64_t)cache->dim * (idx ? k : 1)) return HSI_ERR_INVALID_ARG;  // two results in one place
     p.start = row_start;
     p.first = first;
     p.idx = idx;
@@ -156,7 +160,6 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
     p.T = T;
     p.rows = idx ? T * k : T;
     p.out = static_cast<uint16_t*>(out);
-    p.ot = out_stride;
     const int64_t blocks = (p.rows + LT_WARPS * LT_RPW - 1) / (LT_WARPS * LT_RPW);
     if (blocks > INT32_MAX) return HSI_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), block(32 * LT_WARPS);
@@ -182,11 +185,14 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     LatentAttendParams p{};
     const hsi_status st = latent_view(cache, &p.c);
     if (st != HSI_OK) return st;
+    p.qt = row_stride(T, q_token_stride);
+    p.qh = row_stride(q_heads, q_head_stride);
+    p.ot = row_stride(T, o_token_stride);
+    p.oh = row_stride(q_heads, o_head_stride);
     if (!q_start || T <= 0 || T > INT32_MAX || max_q <= 0 || max_kv <= 0 || max_kv > INT32_MAX || q_heads <= 0 ||
-        !rows_ok(q, q_token_stride, q_head_stride) || !(scale == scale) || !lists_ok(idx, ld_idx, k))
+        !rows_ok(q, p.qt, p.qh) || !(scale == scale) || !lists_ok(idx, ld_idx, k))
         return HSI_ERR_INVALID_ARG;
-    if (!rows_ok(out, o_token_stride, o_head_stride) || out == q || (T > 1 && o_token_stride < LT_VALUE) ||
-        (q_heads > 1 && o_head_stride < LT_VALUE))
+    if (!rows_ok(out, p.ot, p.oh) || out == q || (T > 1 && p.ot < LT_VALUE) || (q_heads > 1 && p.oh < LT_VALUE))
         return HSI_ERR_INVALID_ARG;
     if (q_heads > 65535) return HSI_ERR_UNSUPPORTED;
     p.max_kv = (int)(max_kv < p.c.capacity ? max_kv : p.c.capacity);
@@ -198,8 +204,6 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     const size_t need = hsi_latent_attention_ws(cache->B, q_heads, T, p.max_q, p.max_kv, idx ? k : 0);
     if (!ws || ws_bytes < need || !aligned(ws, 256)) return HSI_ERR_WORKSPACE;
     p.q = q;
-    p.qt = q_token_stride;
-    p.qh = q_head_stride;
     p.q_start = q_start;
     p.T = T;
     p.H = q_heads;
@@ -213,8 +217,6 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     p.sl2 = std::fmax(std::fabs(scale * LOG2E), 1e-30f);  // above 0, so that -inf stays -inf: at scale 0 every p is 1
     p.causal = causal != 0;
     p.out = out;
-    p.ot = o_token_stride;
-    p.oh = o_head_stride;
     p.lse = lse;
     p.runs = (int)latent_runs(tiles, most);
     if (p.runs <= 0) return HSI_ERR_CUDA;

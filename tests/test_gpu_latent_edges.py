@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from latent_cases import DEV, E4M3, FP8, Latent, nearest, two
+from latent_cases import BF16, DEV, E4M3, FP8, Latent, nearest, two
 
 import long_context_decode_lightning_gb300 as hsi
 
@@ -90,3 +90,42 @@ def test_attention_over_one_entry_of_the_largest_numbers_is_that_entry(dim):
     assert hsi.device_error() == 0
     assert torch.equal(c.out.double(), _kept(x)[0][:, None, :512].expand(n, 16, 512))
     assert bool((c.lse == 0).all())
+
+
+# ----------------------------------------------------------------------- strides of one row --
+
+@pytest.mark.parametrize("fmt,dim", [(BF16, 576), (FP8, 512)])
+def test_strides_that_no_second_row_uses_are_not_looked_at(fmt, dim):
+    """One token, one head: what lies between rows does not matter where there is one."""
+    c = Latent(75, [90], [1], 1, fmt, dim, 16)
+    x = torch.randn(2, dim + 3, device=DEV).bfloat16()[:1, :dim]
+    assert x.stride(0) % 8
+    before = c.data.clone()
+    hsi.latent_append(c.cache, x, c.q_start)
+    at = c.place(0, 89)
+    dense = torch.zeros_like(c.data)
+    dense.copy_(before)
+    kept = c.data[at].clone()
+    c.data.copy_(before)
+    hsi.latent_append(c.cache, x.contiguous(), c.q_start)
+    assert torch.equal(kept, c.data[at])
+    out = torch.full((2, dim + 3), -7.0, dtype=torch.bfloat16, device=DEV)
+    hsi.latent_read(c.cache, out[:1, :dim], c.q_start, first=torch.tensor([89], dtype=torch.int32, device=DEV))
+    plain = torch.empty(1, dim, dtype=torch.bfloat16, device=DEV)
+    hsi.latent_read(c.cache, plain, c.q_start, first=torch.tensor([89], dtype=torch.int32, device=DEV))
+    assert torch.equal(out[:1, :dim], plain) and bool((out[1] == -7).all()) and bool((out[0, dim:] == -7).all())
+    odd = torch.full((1, 3 * dim + 4), -7.0, dtype=torch.bfloat16, device=DEV).as_strided((1, 3, dim), (3 * dim + 4, dim, 1))
+    idx = torch.tensor([[5, -1, 7]], dtype=torch.int32, device=DEV)
+    even = torch.empty(1, 3, dim, dtype=torch.bfloat16, device=DEV)
+    hsi.latent_read(c.cache, odd, c.q_start, idx=idx)
+    hsi.latent_read(c.cache, even, c.q_start, idx=idx)
+    assert torch.equal(odd, even)
+    want = torch.empty(1, 1, 512, dtype=torch.bfloat16, device=DEV)
+    hsi.latent_attention(c.cache, c.q, c.q_start, 1, 90, SCALE, want)
+    q = torch.zeros(2, dim + 4, dtype=torch.bfloat16, device=DEV)
+    q[0, :dim] = c.q[0, 0]
+    got = torch.full((2, 517), -7.0, dtype=torch.bfloat16, device=DEV)
+    hsi.latent_attention(c.cache, q.as_strided((1, 1, dim), (dim + 4, dim + 3, 1)), c.q_start, 1, 90, SCALE,
+                         got.as_strided((1, 1, 512), (515, 517, 1)))
+    assert hsi.device_error() == 0
+    assert torch.equal(got[0, :512], want[0, 0]) and bool((got[0, 512:] == -7).all()) and bool((got[1] == -7).all())

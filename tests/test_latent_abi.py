@@ -126,6 +126,18 @@ def test_the_longest_lists_are_counted(L):
     assert attend(L, cache(), idx=F, ld=(1 << 31) - 1, k=(1 << 31) - 4097, T=1, ws=None) == -5  # (but for the workspace)
 
 
+def test_strides_that_no_second_row_uses(L):
+    """Of one token or head they are not looked at (calls that a later check refuses); of two they are."""
+    turn = dict(steps=F, pos=F, rot=24)
+    assert append(L, cache(), xt=580, T=1, **turn) == append(L, cache(), xt=-8, T=1, **turn) == -2
+    assert append(L, cache(), xt=580, T=2, **turn) == -1
+    one = dict(T=1, H=1, ws=None)
+    assert attend(L, cache(), qt=577, qh=-3, ot=7, oh=-1, **one) == -5
+    assert attend(L, cache(), qh=577, **dict(one, H=2)) == attend(L, cache(), oh=513, **dict(one, H=2)) == -1
+    assert attend(L, cache(), qt=577, **dict(one, T=2)) == attend(L, cache(), ot=513, **dict(one, T=2)) == -1
+    assert attend(L, cache(), q=F + 8, **one) == attend(L, cache(), out=F + 8, **one) == -1
+
+
 def test_kernels_use_the_barrier_helpers():
     for name in ("latent.cuh", "latent_attend.cuh"):
         assert not BARRIER.search(_source(name)), name
@@ -260,3 +272,14 @@ def test_the_binding_refuses_a_table_of_no_pages(L):
         with pytest.raises(ValueError, match="table"):
             c.table = none
         assert c.table is kept and c.c.table == kept.data_ptr()
+
+
+def test_lists_of_one_entry_may_lie_apart(L):
+    """Of one entry a row, the distance between a row's entries does not matter; of two it does."""
+    wide = gpu(4, 6, dtype=torch.int32)
+    one, two = wide[:, ::7], wide[:, ::3]
+    assert one.shape == (4, 1) and hsi._lists(one, 4) == (wide.data_ptr(), 6, 1)
+    col = wide.view(24)[:4].view(1, 4).T
+    assert col.stride() == (1, 4) and hsi._lists(col, 4) == (wide.data_ptr(), 1, 1)
+    with pytest.raises(ValueError, match="idx"):
+        hsi._lists(two, 4)
