@@ -798,12 +798,15 @@ hsi_status hsi_latent_read(const hsi_latent_cache* cache, const int32_t* row_sta
  *          bf16 otherwise; strides in elements (multiples of 8, 16-byte aligned); distinct.
  *          An entry among a sequence's new tokens must be finite for every one of them,
  *          also where it does not see it yet (0 times a NaN is a NaN).
- *  max_q, max_kv (host) bounds of a sequence's new tokens and entries.
+ *  max_q, max_kv (host) bounds of a sequence's new tokens and entries. With idx max_q is
+ *          not looked at (but above 0); without, a sequence of more new tokens is left
+ *          alone and reported.
  *  lse     (dev) fp32 [T][q_heads], may be NULL.
  *  ws      (dev) hsi_latent_attention_ws(...) bytes (k 0 without lists); calls that
  *          may run at the same time need one each.
- * Rows of tokens outside every sequence are left as they were. The same call gives the
- * same bits.
+ * Rows of tokens outside every sequence are left as they were; without idx every row is
+ * where q_start descends anywhere (sequences would claim the same tokens), with idx
+ * those of the tokens around which it does. The same call gives the same bits.
  * Errors: INVALID_ARG (k other than 0 without idx among them), WORKSPACE, UNSUPPORTED
  * (the cache's dims; more than 65535 heads; k, or max_kv and what the cache holds, past
  * 2^31 - 4097; bounds at which the tiles of work, 64 entries by 64 rows, pass 2^31 for a

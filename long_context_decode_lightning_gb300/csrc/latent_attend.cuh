@@ -313,12 +313,18 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
         }
         return;
     }
+    // Where q_start descends, sequences claim the same tokens: more units than tokens, which the host's bounds do not
+    // cover and whose results would fall into the same rows. No row is written then.
+    bool falls = false;
     if (p.whole) {  // a unit a block
         LatentSeq q;
         const int b = run / p.n_rt, rt = run % p.n_rt;
         q.load(p, b);
+        for (int i = lane; i < p.c.B; i += 32) falls = falls || __ldg(p.q_start + i) > __ldg(p.q_start + i + 1);
+        falls = __any_sync(~0u, falls);
         if (lane == 0) {
-            s.left = rt < q.n_rt ? q.tiles(p, rt) : 0;
+            if (falls) raise_error(DEVERR_ARG);
+            s.left = rt < q.n_rt && !falls ? q.tiles(p, rt) : 0;
             s.b = b;
             s.rt = rt;
             s.tile = 0;
@@ -329,7 +335,10 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     LatentSeq mine;
     const auto load = [&](int b0) {  // tiles of sequence b0 + lane
         mine.n_rt = 0;
-        if (b0 + lane < p.c.B) mine.load(p, b0 + lane);
+        if (b0 + lane < p.c.B) {
+            mine.load(p, b0 + lane);
+            falls = falls || mine.at > __ldg(p.q_start + b0 + lane + 1);  // (reported by paged_new)
+        }
         return mine.n_rt ? mine.before(p, mine.n_rt) : 0u;
     };
     const auto upto = [&](uint32_t n) {
@@ -345,6 +354,7 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
         n = load(b0);
         total += __reduce_add_sync(~0u, n);
     }
+    if (__any_sync(~0u, falls)) total = 0;
     const Line line(total, p.runs);
     const uint32_t x = line.cut(run);
     if (lane == 0) {

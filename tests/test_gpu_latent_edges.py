@@ -1,10 +1,11 @@
 """The latent cache at the edges of its formats, strides and starts, against plain forms in 64 bits."""
+import copy
 import math
 
 import pytest
 import torch
 
-from latent_cases import BF16, DEV, E4M3, FP8, Latent, nearest, two
+from latent_cases import BF16, DEV, E4M3, FP4, FP8, Latent, nearest, two, within, x_type
 
 import long_context_decode_lightning_gb300 as hsi
 
@@ -90,6 +91,113 @@ def test_attention_over_one_entry_of_the_largest_numbers_is_that_entry(dim):
     assert hsi.device_error() == 0
     assert torch.equal(c.out.double(), _kept(x)[0][:, None, :512].expand(n, 16, 512))
     assert bool((c.lse == 0).all())
+
+
+# ------------------------------------------------------------- wrong starts of sequences --
+
+STARTS = [[0, 4, 2, 6], [-1, 2, 4, 6], [0, 2, 4, 7], [6, 4, 2, 0], [0, 2, 1 << 30, 6], [0, 6, 0, 6]]
+FORMS = [(BF16, 576), (FP8, 576), (FP4, 512)]
+
+
+def owners(start, T):
+    """The sequence of each token, from the definition: b where start[b] <= t < start[b+1], where start does not descend
+    around t (the sequences that end at or before t are the first b) and b does not leave [0, T]; or -1."""
+    B, out = len(start) - 1, []
+    for t in range(T):
+        ended = [b for b in range(B) if start[b + 1] <= t]
+        b = len(ended)
+        good = ended == list(range(b)) and b < B and 0 <= start[b] <= t and start[b + 1] <= T
+        out.append(b if good else -1)
+    return out
+
+
+def only(c, b, toks, past):
+    """Sequence b's tokens of a case, as a case whose new tokens they are (past: of the sequence's tokens, the last one's end)."""
+    s = copy.copy(c)
+    s.kv_lens, s.q_lens, s.values, s.T = [c.kv_lens[b] - (past - toks[-1] - 1)], [len(toks)], [c.values[b]], len(toks)
+    return s
+
+
+@pytest.mark.parametrize("fmt,dim", FORMS)
+@pytest.mark.parametrize("start", STARTS)
+def test_read_reports_a_wrong_start(fmt, dim, start):
+    c = Latent(71, [300, 280, 260], [2, 2, 2], 1, fmt, dim, 16)
+    bounds = torch.tensor(start, dtype=torch.int32, device=DEV)
+    first = torch.tensor([10, 20, 30], dtype=torch.int32, device=DEV)
+    own = owners(start, 6)
+    out = torch.full((6, dim), -7.0, dtype=x_type(fmt), device=DEV)
+    hsi.latent_read(c.cache, out, bounds, first=first)
+    assert hsi.device_error() == -6
+    for t, b in enumerate(own):
+        want = c.values[b][10 * (b + 1) + t - start[b]] if b >= 0 else torch.full((dim,), -7.0, device=DEV).double()
+        assert torch.equal(out[t].double(), want), t
+    idx = torch.randint(0, 250, (6, 70), device=DEV, dtype=torch.int32)
+    got = torch.full((6, 70, dim), -7.0, dtype=x_type(fmt), device=DEV)
+    hsi.latent_read(c.cache, got, bounds, idx=idx)
+    assert hsi.device_error() == -6
+    for t, b in enumerate(own):
+        assert torch.equal(got[t].double(), c.values[b][idx[t].long()] if b >= 0 else got[t].double() * 0 - 7), t
+
+
+@pytest.mark.parametrize("fmt,dim", FORMS)
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("lens", [[40, 50, 60], [300, 280, 260], [9000, 5000, 7000]])  # units whole, in runs, joined
+@pytest.mark.parametrize("start", STARTS)
+def test_attention_reports_a_wrong_start(fmt, dim, H, lens, start):
+    """With lists, tokens around which the starts descend and those of a sequence that leaves the call's tokens are left
+    alone. Without, a sequence that leaves them is, and every row is where the starts descend."""
+    c = Latent(72, lens, [2, 2, 2], H, fmt, dim, 64)
+    bounds = torch.tensor(start, dtype=torch.int32, device=DEV)
+    falls = any(a > b for a, b in zip(start, start[1:]))
+    idx = torch.randint(0, 35, (6, 70), device=DEV, dtype=torch.int32)
+    for lists in (None, idx):
+        own = [-1] * 6 if falls and lists is None else owners(start, 6)
+        c.out.fill_(-3.0)
+        c.lse.fill_(-3.0)
+        hsi.latent_attention(c.cache, c.q, bounds, 6, max(lens), SCALE, c.out, lse=c.lse, idx=lists)
+        assert hsi.device_error() == -6
+        for b in range(3):
+            toks = [t for t in range(6) if own[t] == b]
+            if not toks:
+                continue
+            out, lse, tol, tol_lse = only(c, b, toks, start[b + 1]).attention(
+                SCALE, True, None if lists is None else lists[toks], q=c.q[toks])
+            within(c.out[toks], out, tol, "out")
+            within(c.lse[toks], lse, tol_lse, "lse")
+        left = [t for t in range(6) if own[t] < 0]
+        assert bool((c.out[left] == -3).all()) and bool((c.lse[left] == -3).all())
+
+
+@pytest.mark.parametrize("longest", [30, 700])
+@pytest.mark.parametrize("at", [1, 32, 33, 64, 70])
+def test_attention_looks_at_the_starts_of_many_sequences(longest, at):
+    c = Latent(76, [longest - b % 20 for b in range(70)], [1] * 70, 16, BF16, 512, 16)
+    bounds = c.q_start.clone()
+    bounds[at] = at - 2  # before the start of the sequence that it ends
+    hsi.latent_attention(c.cache, c.q, bounds, 3, longest, SCALE, c.out, lse=c.lse)
+    assert hsi.device_error() == -6
+    assert bool((c.out == -3).all()) and bool((c.lse == -3).all())
+    c.check(SCALE)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("lens", [[40, 50, 60], [3000, 2800, 2600]])
+def test_attention_of_more_new_tokens_than_the_bound(H, lens):
+    """Without lists such a sequence is left alone and reported; with lists the bound is not looked at."""
+    c = Latent(73, lens, [2, 5, 1], H, BF16, 576, 64)
+    idx = c.lists(74, 70, True)
+    hsi.latent_attention(c.cache, c.q, c.q_start, 2, max(lens), SCALE, c.out, lse=c.lse)
+    assert hsi.device_error() == -6
+    out, lse, tol, tol_lse = c.attention(SCALE, True)
+    rows = [0, 1, 7]
+    within(c.out[rows], out[rows], tol[rows], "out")
+    within(c.lse[rows], lse[rows], tol_lse[rows], "lse")
+    assert bool((c.out[2:7] == -3).all()) and bool((c.lse[2:7] == -3).all())
+    hsi.latent_attention(c.cache, c.q, c.q_start, 2, max(lens), SCALE, c.out, lse=c.lse, idx=idx)
+    assert hsi.device_error() == 0
+    out, lse, tol, tol_lse = c.attention(SCALE, True, idx)
+    within(c.out, out, tol, "out")
+    within(c.lse, lse, tol_lse, "lse")
 
 
 # ----------------------------------------------------------------------- strides of one row --
