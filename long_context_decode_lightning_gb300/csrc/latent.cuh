@@ -39,7 +39,6 @@ enum LatentFormat { LF_BF16 = 0, LF_FP16 = 1, LF_FP8 = 2, LF_FP4 = 3 };
 constexpr int LT_VALUE = 512;      // dims of the value
 constexpr int LT_TAIL = 64;        // values of an FP8 entry that stay in bf16
 constexpr int LT_MIN_E = -118, LT_MAX_E = 120;  // scales' exponents
-constexpr float LT_MAX_FP8 = 0x1.Ep127f;        // 240 * 2^120: the next code of the largest exponent is past bf16
 
 __host__ __device__ constexpr int latent_entry_bytes(int fmt, int dim) {
     return fmt == LF_FP8 ? dim + 80 : fmt == LF_FP4 ? KV_BYTES : 2 * dim;
@@ -208,6 +207,12 @@ __device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
 
 constexpr int LT_WARPS = 8;
 
+// Four E4M3 codes of LT_MAX_E, whose values are at most 256: that is past bf16 times 2^120, so that it becomes 240 (255 *
+// 2^120, the largest bf16 number, is 15 in 255 off then, less than half a step's 2^-4).
+__device__ __forceinline__ uint32_t e4m3x4_to_240(uint32_t w) {
+    return w - ((w >> 3 & w >> 4 & w >> 5 & w >> 6) & 0x01010101u);
+}
+
 // A token's values, eight a lane and step, as the cache's format keeps them. Whole warp.
 template <typename T, int FMT>
 __device__ __forceinline__ void latent_keep(int dim, const uint4 (&raw)[3], uint8_t* dst) {
@@ -246,17 +251,15 @@ __device__ __forceinline__ void latent_keep(int dim, const uint4 (&raw)[3], uint
             ex = max(LT_MIN_E, min(LT_MAX_E, ex));
             const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (m < codes) {
-                if (ex == LT_MAX_E) {  // values up to 255 * 2^120: 15 in 255 off at most, less than half a step's 2^-4
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(v[j], -LT_MAX_FP8), LT_MAX_FP8);
-                }
                 uint32_t c[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %1, %2; cvt.u32.u16 %0, t; }"
                         : "=r"(c[j])
                         : "f"(v[2 * j + 1] * inv), "f"(v[2 * j] * inv));
-                *reinterpret_cast<uint2*>(dst + m) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                uint2 w = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                if (ex == LT_MAX_E) w = make_uint2(e4m3x4_to_240(w.x), e4m3x4_to_240(w.y));
+                *reinterpret_cast<uint2*>(dst + m) = w;
             } else if (m < dim) {
                 *reinterpret_cast<uint4*>(dst + codes + 2 * (m - codes)) = raw[i];
             }
