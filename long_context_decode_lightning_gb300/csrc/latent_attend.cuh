@@ -234,6 +234,7 @@ struct LatentCfg {
         uint32_t vote[2][4];
         uint32_t tmem, total;
         int abort;
+        int none;                      // q_start descends: no tile is this block's
         int left, b, rt, tile;         // this block's run: tiles, and where it starts
         LatentSeq q;
     };
@@ -313,18 +314,12 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
         }
         return;
     }
-    // Where q_start descends, sequences claim the same tokens: more units than tokens, which the host's bounds do not
-    // cover and whose results would fall into the same rows. No row is written then.
-    bool falls = false;
     if (p.whole) {  // a unit a block
         LatentSeq q;
         const int b = run / p.n_rt, rt = run % p.n_rt;
         q.load(p, b);
-        for (int i = lane; i < p.c.B; i += 32) falls = falls || __ldg(p.q_start + i) > __ldg(p.q_start + i + 1);
-        falls = __any_sync(~0u, falls);
         if (lane == 0) {
-            if (falls) raise_error(DEVERR_ARG);
-            s.left = rt < q.n_rt && !falls ? q.tiles(p, rt) : 0;
+            s.left = rt < q.n_rt ? q.tiles(p, rt) : 0;
             s.b = b;
             s.rt = rt;
             s.tile = 0;
@@ -335,10 +330,7 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     LatentSeq mine;
     const auto load = [&](int b0) {  // tiles of sequence b0 + lane
         mine.n_rt = 0;
-        if (b0 + lane < p.c.B) {
-            mine.load(p, b0 + lane);
-            falls = falls || mine.at > __ldg(p.q_start + b0 + lane + 1);  // (reported by paged_new)
-        }
+        if (b0 + lane < p.c.B) mine.load(p, b0 + lane);
         return mine.n_rt ? mine.before(p, mine.n_rt) : 0u;
     };
     const auto upto = [&](uint32_t n) {
@@ -354,7 +346,6 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
         n = load(b0);
         total += __reduce_add_sync(~0u, n);
     }
-    if (__any_sync(~0u, falls)) total = 0;
     const Line line(total, p.runs);
     const uint32_t x = line.cut(run);
     if (lane == 0) {
@@ -396,6 +387,17 @@ __device__ __forceinline__ void latent_line(const LatentAttendParams& p, int run
     }
 }
 
+// Whether q_start descends (which paged_new reports). Sequences claim the same tokens then: more units than tokens,
+// which the host's bounds do not cover, and two results for a row; so that no row is written without lists. A warp other
+// than that which looks for the run's start (nine sequences of 8191 entries, four tokens each: 34.8 us without the look,
+// 35.0 with it, 36.3 where that warp has it among its lengths).
+__device__ __forceinline__ bool latent_falls(const LatentAttendParams& p) {
+    bool falls = false;
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < p.c.B; i += 32) falls = falls || __ldg(p.q_start + i) > __ldg(p.q_start + i + 1);
+    return __any_sync(~0u, falls);
+}
+
 template <typename T, int DIM, int FMT>
 __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(const __grid_constant__ LatentAttendParams p) {
     using C = LatentCfg<DIM, FMT>;
@@ -427,12 +429,16 @@ __global__ void __launch_bounds__(latent_threads(FMT), 1) latent_attend_kernel(c
     griddep_launch_dependents();
     if (threadIdx.x == 0 && !p.whole) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     if (warp == 0) latent_line(p, run, s);
+    if (warp == 1) {
+        const bool none = !p.idx && latent_falls(p);
+        if (lane == 0) s.none = none;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     LatentWalk k;
-    k.left = s.left;
+    k.left = s.none ? 0 : s.left;
     k.b = s.b;
     k.rt = s.rt;
     k.tile0 = s.tile;
