@@ -71,7 +71,7 @@ int64_t latent_tiles(const LatentTiles& t, int32_t B, int64_t T, int64_t max_q, 
     return units > INT32_MAX || nt > INT32_MAX ? int64_t(1) << 62 : units * nt;
 }
 
-// Runs: a CTA per SM and head tile, no more than there can be tiles.
+// Runs: a CTA per SM and head tile, no more than there can be tiles; one at least.
 int64_t latent_runs(const LatentTiles& t, int64_t tiles) {
     const int64_t sms = sm_count(), room = sms > t.nht ? sms / t.nht : 1;
     return tiles < room ? tiles : room;
@@ -218,8 +218,8 @@ hsi_status hsi_latent_attention(const hsi_latent_cache* cache, const void* q, in
     p.causal = causal != 0;
     p.out = out;
     p.lse = lse;
+    if (sm_count() <= 0) return HSI_ERR_CUDA;
     p.runs = (int)latent_runs(tiles, most);
-    if (p.runs <= 0) return HSI_ERR_CUDA;
     p.desc = static_cast<int4*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + latent_desc_bytes(tiles, p.runs));
     p.inv_hp = 65536 / p.hp + 1;
