@@ -81,10 +81,12 @@ size_t latent_desc_bytes(const LatentTiles& t, int64_t runs) { return align_up((
 
 // Whether units go whole to blocks (no partial sums, no second kernel): where the most tiles that a block then has are
 // no more than those of the line's runs and what the join costs, eight tiles' time where all SMs leave partial sums.
-// Measured, 64 heads over bf16 entries of 576, us whole against line: 64 tokens of 512 listed entries 20 and 27, 20 of
-// them 19 and 20, 30 sequences of 600 entries 22 and 23, 150 tokens of 256 listed 16 and 22; eight tokens of 1024
-// listed 30 and 20, four sequences of 1000 entries 29 and 16. (Clusters of 2, 4 or 8 blocks a unit, joined through
-// distributed shared memory, were slower than the better of the two in all but one of sixteen such cases.)
+// Measured, 64 heads over bf16 entries of 576, us whole against line. Taken whole: 64 tokens of 512 listed entries 20.3
+// and 26.6 (FP4 24.3 and 27.6, FP8 28.3 and 29.5), 150 tokens of 256 listed 15.5 and 22.2, and on the wrong side of the
+// border 20 tokens of 512 listed 19.8 and 19.2 (FP4 22.8 and 20.4), 30 sequences of 600 entries 21.7 and 20.3. Taken
+// along the line: eight tokens of 1024 listed 29.6 and 19.8, four sequences of 1000 entries 29.8 and 16.0, 12 of 400 17.2
+// and 17.4, and on the wrong side 60 of 1000 30.7 and 35.4. (Clusters of 2, 4 or 8 blocks a unit, joined through
+// distributed shared memory, were slower than the better of the two in at least fourteen of sixteen cases.)
 bool latent_whole(const LatentAttendParams& p, int64_t tiles) {
     const int64_t keys = p.idx ? p.k : p.max_kv, nt = (keys + LA_KEYS - 1) / LA_KEYS, room = sm_count() / p.nht;
     const int64_t units = p.idx ? p.T : (int64_t)p.c.B * p.n_rt;

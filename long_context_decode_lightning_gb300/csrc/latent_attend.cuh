@@ -29,16 +29,19 @@
 // P stands in the place of the dims past the value, which S is done with.
 //
 // The units' tiles form one line that is cut into equal runs, one per CTA; a unit that
-// spans runs is joined by a second kernel from fp32 partial sums. Where units are as
-// many as SMs, or whole lists to a run leave few idle, none is split.
+// spans runs is joined by a second kernel from fp32 partial sums. Where that would cost
+// more than it gains, units go to blocks whole, though SMs may stay idle then (64 lists
+// of 512 entries: 88 of 152); latent_whole has the rule and both sides of it.
 //
 // Measured: 1024 tokens of 64 heads over 2048 listed bf16 entries of 576 each 372 us, 784
 // TFLOP/s (41% of the measured burst rate); one token of 16 x 32768 entries at 128 heads 153
 // us (3.05 TB/s, 730 TFLOP/s); of 8 x 65536 FP8 entries at 64 heads 117 us (2.3 TB/s). A tile
-// takes 1.3 to 1.7 us where 1920 cycles are 1.0: two stages leave the chain of a stage (its
-// copies 2000 cycles, S 1200 to 2000 beside the other stage's P V, softmax 1000, P V until the
-// first dims are free 700) as the bound. A first tile comes 5 us after the start, partial
-// sums leave at 32 bytes a cycle and SM (2 us), the join takes 5 to 10 us.
+// of 16-bit entries takes 1.3 to 1.7 us where 1920 cycles are 1.0: two stages leave the chain
+// of a stage (its copies 2000 cycles, S 1200 to 2000 beside the other stage's P V, softmax 1000,
+// P V until the first dims are free 700) as the bound. One of FP8 entries takes 2.5 us (42 an
+// SM in the 117): a stage is decoded after the P V before it, so that decoding is part of the
+// chain. A first tile comes 5 us after the start, partial sums leave at 32 bytes a cycle and
+// SM (2 us), the join takes 5 to 10 us.
 #pragma once
 #include <cstdint>
 
